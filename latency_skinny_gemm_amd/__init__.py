@@ -16,7 +16,10 @@ __all__ = ["SkgPlan", "SkinnyGemmError", "gemm_bf16", "gemm_bf16_planned", "gemm
            "plan_complete", "reserve", "release_all", "status_string", "library_path",
            "KIND_DOT", "KIND_SPLITK", "KIND_TILED", "KIND_ROWS", "REDUCE_NONE", "REDUCE_LAST", "REDUCE_KERNEL", "FLAG_DOT2", "FLAG_TILED_WIDE", "FLAG_DOT_XLDS", "FLAG_ROWS_HALF", "FLAG_DOT_WFIRST",
            "DTYPE_BF16", "DTYPE_FP8", "DTYPE_F32", "DTYPE_FP8_MX", "gemm_bf16_f32", "gemm_fp8_quant",
-           "quant_e4m3"]
+           "quant_e4m3",
+           # the operators around the products (moe.py)
+           "NormOut", "MxfpWeights", "rmsnorm", "route", "quant_mx", "dequant_mx", "mxfp4_pack",
+           "gemm_mxfp4", "moe_mxfp4", "reserve_moe"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libskinny_gemm.so")
@@ -121,6 +124,7 @@ def _load():
     L.skinny_gemm_release_all.restype = I
     L.skinny_gemm_status_string.argtypes = [I]
     L.skinny_gemm_status_string.restype = ctypes.c_char_p
+    moe.declare(L)
     _lib = L
     return L
 
@@ -155,11 +159,13 @@ def _one_device(*ts):
 def _launch(dev, stream, fn, *args):
     """fn(*args, stream) with `dev` current (the library keeps its workspaces
     per current device) on `stream`, else dev's current stream."""
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream() if stream is None else stream
-        if s.device != dev:
-            raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
-        return fn(*args, ctypes.c_void_p(s.cuda_stream))
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, fn, *args)
+    s = torch.cuda.current_stream() if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
+    return fn(*args, ctypes.c_void_p(s.cuda_stream))
 
 
 def _empty(shape, dtype, device, stream):
@@ -174,6 +180,10 @@ def _empty(shape, dtype, device, stream):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_tensors(x, W, bias, out, dtype):
@@ -405,3 +415,8 @@ def reserve(max_M, max_N, max_K, max_S, stream=None):
 
 def release_all():
     _check(_load().skinny_gemm_release_all(), "skinny_gemm_release_all")
+
+
+from . import moe  # noqa: E402  (uses the helpers above)
+from .moe import (MxfpWeights, NormOut, dequant_mx, gemm_mxfp4, moe_mxfp4,  # noqa: E402,F401
+                  mxfp4_pack, quant_mx, reserve_moe, rmsnorm, route)

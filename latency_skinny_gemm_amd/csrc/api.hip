@@ -118,6 +118,8 @@ Workspace *find(int device, hipStream_t stream, long owner) {
     return nullptr;
 }
 
+}  // namespace
+
 // Workspace for this (device, stream, owner) with room for the request.
 // Grows it outside graph capture; during capture a short workspace is an
 // error.
@@ -153,6 +155,8 @@ int acquire(hipStream_t stream, size_t floats, size_t tickets, float **ws, unsig
     t_cache = WorkspaceCache{g_generation.load(std::memory_order_acquire), *w};
     return SKG_OK;
 }
+
+namespace {
 
 int run_bf16(const void *x, const void *W, const void *bias, void *out, int out_f32, int M, int N,
              int K, const SkgPlan &p, hipStream_t stream) {

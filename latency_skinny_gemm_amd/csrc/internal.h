@@ -269,6 +269,11 @@ size_t round_floats(size_t floats);
 size_t quant_floats(int M, int K);
 int tile_count(const SkgPlan &p, int N);
 
+// Workspace of (current device, stream): `floats` fp32 and `tickets` zeroed
+// counters, grown outside graph capture (api.hip).  A workspace belongs to
+// one stream, so its calls run one after another.
+int acquire(hipStream_t stream, size_t floats, size_t tickets, float **ws, unsigned **tk);
+
 // Launchers (kernels_*.hip).  Return a hipError_t as int.
 // out_f32: 1 writes fp32 outputs, 0 bf16.
 int launch_dot(const SkgPlan &p, const void *x, const void *W, const void *bias, void *out,

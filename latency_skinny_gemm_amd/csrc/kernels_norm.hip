@@ -1,0 +1,141 @@
+// kernels_norm.hip -- residual addition and root-mean-square norm in one
+// pass, y = s / sqrt(mean(s^2) + eps) * weight with s = x + residual.
+//
+// A row stays in the registers of the lanes that read it (16-byte vectors,
+// widened to fp32), so x and the residual are read once and the sum of
+// squares costs one reduction.  The 8-bit outputs are made from the same
+// fp32 values: static e4m3, or MX codes whose 32-value blocks are the four
+// neighbouring lanes of a quad.
+#include "device_common.h"
+#include "internal.h"
+#include "moe_internal.h"
+#include "mx_common.h"
+
+namespace skg {
+
+namespace {
+
+struct NormArgs {
+    const uint16_t *x, *residual, *weight;
+    const float *scale;
+    uint8_t *y, *e8;
+    uint16_t *residual_out;
+    float eps;
+    int M, K;
+};
+
+// The eight fp32 sums of vector i of a row, and bf16 of them to residual_out.
+__device__ __forceinline__ void norm_load(const NormArgs &a, size_t row0, int i, float (&s)[8]) {
+    bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.x + row0 + (size_t)i * 8), s);
+    if (a.residual) {
+        float r[8];
+        bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.residual + row0 + (size_t)i * 8), r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += r[j];
+    }
+}
+
+template <int OUT>
+__device__ __forceinline__ void norm_store(const NormArgs &a, int row, size_t row0, int i,
+                                           const float (&s)[8], float inv, float qinv) {
+    float w[8], y[8];
+    bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.weight + (size_t)i * 8), w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = s[j] * inv * w[j];
+    const size_t at = row0 + (size_t)i * 8;
+    if constexpr (OUT == SKG_NORM_BF16) {
+        *reinterpret_cast<u32x4 *>(a.y + at * 2) = f32x8_to_bf16(y);
+    } else if constexpr (OUT == SKG_NORM_E4M3) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = quant_clamp(y[j] * qinv);
+        *reinterpret_cast<uint2 *>(a.y + at) = mx_codes8_e4m3(y, 1.0f);
+    } else {
+        const int e = mx_store8<kMxE4m3>(y, a.y, at);
+        if ((i & 3) == 0) a.e8[at / 32] = (uint8_t)e;
+    }
+}
+
+}  // namespace
+
+// TPR lanes per row (64: one wave, four rows a workgroup; else the whole
+// workgroup), V vectors of 8 values per lane held in registers; V == 0: rows
+// longer than the registers hold, read a second time for the output.
+template <int OUT, int TPR, int V>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs a) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    const int t = threadIdx.x % TPR;
+    const int row = blockIdx.x * ROWS + threadIdx.x / TPR;
+    if (ROWS > 1 && row >= a.M) return;  // whole waves; no barrier below when ROWS > 1
+    const int k8 = a.K / 8;
+    const size_t row0 = (size_t)row * a.K;
+    constexpr int N = V > 0 ? V : 1;
+    float s[N][8];
+    float sq = 0.0f;
+    const int nv = V > 0 ? V : (k8 + TPR - 1) / TPR;
+#pragma unroll
+    for (int v = 0; v < nv; ++v) {
+        const int i = t + v * TPR;
+        float(&sv)[8] = s[V > 0 ? v : 0];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sv[j] = 0.0f;
+        if (i < k8) norm_load(a, row0, i, sv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(sv[j], sv[j], sq);
+    }
+    sq = wave_sum(sq);
+    if constexpr (TPR > 64) {
+        __shared__ float part[TPR / 64];
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = sq;
+        __syncthreads();
+        sq = 0.0f;
+#pragma unroll
+        for (int w = 0; w < TPR / 64; ++w) sq += part[w];
+    }
+    const float inv = 1.0f / sqrtf(sq / (float)a.K + a.eps);
+    const float qinv = OUT == SKG_NORM_E4M3 ? 1.0f / a.scale[0] : 1.0f;
+#pragma unroll
+    for (int v = 0; v < nv; ++v) {
+        const int i = t + v * TPR;
+        if (i >= k8) continue;  // K / 8 is a multiple of 4 for MX: whole quads
+        float(&sv)[8] = s[V > 0 ? v : 0];
+        if constexpr (V == 0) norm_load(a, row0, i, sv);
+        if (a.residual_out)
+            *reinterpret_cast<u32x4 *>(a.residual_out + row0 + (size_t)i * 8) = f32x8_to_bf16(sv);
+        norm_store<OUT>(a, row, row0, i, sv, inv, qinv);
+    }
+}
+
+namespace {
+
+template <int OUT, int TPR, int V>
+int go(const NormArgs &a, hipStream_t stream) {
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    hipLaunchKernelGGL((rmsnorm_kernel<OUT, TPR, V>), dim3((unsigned)((a.M + ROWS - 1) / ROWS)),
+                       dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+    return (int)hipGetLastError();
+}
+
+template <int OUT>
+int pick(const NormArgs &a, hipStream_t stream) {
+    const int k8 = a.K / 8;
+    if (k8 <= 128) return go<OUT, 64, 2>(a, stream);
+    if (k8 <= 1024) return k8 <= 512 ? go<OUT, 256, 2>(a, stream) : go<OUT, 256, 4>(a, stream);
+    if (k8 <= 2048) return go<OUT, 1024, 2>(a, stream);
+    return go<OUT, 1024, 0>(a, stream);
+}
+
+}  // namespace
+
+int launch_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
+                   int out_format, const float *scale, void *y, void *e8, void *residual_out,
+                   int M, int K, hipStream_t stream) {
+    const NormArgs a{(const uint16_t *)x, (const uint16_t *)residual, (const uint16_t *)weight,
+                     scale, (uint8_t *)y, (uint8_t *)e8, (uint16_t *)residual_out, eps, M, K};
+    switch (out_format) {
+    case SKG_NORM_BF16: return pick<SKG_NORM_BF16>(a, stream);
+    case SKG_NORM_E4M3: return pick<SKG_NORM_E4M3>(a, stream);
+    default: return pick<SKG_NORM_MX>(a, stream);
+    }
+}
+
+}  // namespace skg
