@@ -29,7 +29,8 @@ HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-D__HIP_PLATFOR
 LIB_HIP = ["api.hip", "kernels_dot.hip", "kernels_splitk.hip", "kernels_tiled.hip",
            "kernels_fp8.hip", "kernels_quant.hip", "kernels_fp8_tiled.hip", "kernels_rows.hip",
            "kernels_fp8_rows.hip", "api_moe.hip", "kernels_norm.hip", "kernels_route.hip",
-           "kernels_mx.hip", "kernels_mxfp4.hip", "kernels_moe.hip"]
+           "kernels_mx.hip", "kernels_mxfp4.hip", "kernels_mxfp4_rows.hip",
+           "kernels_moe.hip"]
 LIB_HOST = ["plan.cpp"]
 # Per-file flags.  The tiled kernels keep their accumulators in VGPRs: with the
 # compiler's default AGPR form, the loop-carried accumulators were copied
@@ -38,7 +39,8 @@ EXTRA_FLAGS = {"kernels_tiled.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_fp8_tiled.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_fp8_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "kernels_mxfp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "kernels_mxfp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kernels_mxfp4_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 FLOORS_HIP = ["floors.hip"]
 
 

@@ -192,20 +192,26 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
                         {packed, mxfp4_packed_bytes(1, N, K)},
                         {bias, (size_t)N * 2}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
+    Mxfp4Args a{(const uint8_t *)x, (const uint8_t *)x_e8m0, K / 32, x_format,
+                (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
+    const bool few = M <= kMxRowsMaxCodes;
+    if (few && (x_e8m0 || M <= kMxRowsMaxBf16)) return status(launch_mxfp4_rows(a, stream));
     float *ws = nullptr;
     unsigned *tk = nullptr;
     rc = acquire(stream, floats_of(linear_workspace_bytes((size_t)M, K)), 0, &ws, &tk);
     if (rc != SKG_OK) return rc;
     uint8_t *codes = (uint8_t *)ws, *scales = codes + round256(n);
     int e;
-    if (x_e8m0)
+    if (x_e8m0) {
         e = launch_pad_scales(x_e8m0, scales, M, K, stream);
-    else
+    } else {
         e = launch_quant_mx(x, codes, scales, x_format, M, K, mx_scale_stride(K), stream);
+        a.x = codes;
+    }
     if (e != (int)hipSuccess) return SKG_ERR_HIP;
-    const Mxfp4Args a{x_e8m0 ? (const uint8_t *)x : codes, scales, x_format,
-                      (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
-    return status(launch_mxfp4(a, stream));
+    a.xe = scales;
+    a.es = mx_scale_stride(K);
+    return status(few ? launch_mxfp4_rows(a, stream) : launch_mxfp4(a, stream));
 }
 
 extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weights,

@@ -118,9 +118,12 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
 
 }  // namespace
 
+// Whether each pair reads its expert's weights for itself.
+static bool moe_unsorted(int T, int k, int E) { return (long)T * k <= 16 || T == 1; }
+
 int moe_tile_rows(int T, int k, int E) {
     const long avg = (long)T * k / E;
-    return avg <= 8 ? 16 : avg <= 20 ? 32 : avg <= 44 ? 64 : 128;
+    return avg <= 8 ? 16 : avg <= 20 ? 32 : 64;
 }
 
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
@@ -130,6 +133,7 @@ size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
 int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const MoeSpace s = moe_space(a.T, a.k, a.H, a.I, a.E, a.fmt);
     uint8_t *b = (uint8_t *)workspace;
+    if (moe_unsorted(a.T, a.k, a.E)) return launch_moe_rows(a, b + s.h, b + s.he, stream);
     const int P = a.T * a.k, rows = moe_tile_rows(a.T, a.k, a.E);
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),

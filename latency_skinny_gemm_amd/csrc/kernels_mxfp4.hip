@@ -28,6 +28,7 @@ struct TileArgs {
     const int *pairs;       // grouped: sorted row -> pair
     int top;                // grouped: pairs per token
     int col_tiles;          // workgroups side by side in a row tile
+    int row_tiles;          // dense
 };
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
@@ -39,6 +40,14 @@ __device__ __forceinline__ unsigned row_max(unsigned v) {
     v = max(a[0], a[1]);
     const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
     return max(b[0], b[1]);
+}
+
+// Workgroup b's place in the work list of n: the workgroups of one XCD (b % 8)
+// take one contiguous run of it, so that neighbours in the list, which share
+// weights, share that XCD's L2.  -1: nothing left.
+__device__ __forceinline__ int xcd_order(int b, int n) {
+    const int per = (n + 7) / 8, at = (b & 7) * per + (b >> 3);
+    return (b >> 3) < per && at < n ? at : -1;
 }
 
 }  // namespace
@@ -71,11 +80,12 @@ __global__ void __launch_bounds__(256) mxfp4_tile_kernel(TileArgs a) {
 
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int rt = blockIdx.x / a.col_tiles;           // row tile
-    const int ct = blockIdx.x - rt * a.col_tiles;      // column tile
+    const int row_tiles = MODE == kDense ? a.row_tiles : a.count[0];
+    const int at = xcd_order(blockIdx.x, a.col_tiles * row_tiles);
+    if (at < 0) return;
+    const int ct = at / row_tiles, rt = at - ct * row_tiles;  // column tile, row tile
     int row0 = rt * ROWS, rows = min(ROWS, a.M - row0), expert = 0;
     if constexpr (MODE != kDense) {
-        if (rt >= a.count[0]) return;
         const MoeTile tile = a.tiles[rt];
         row0 = tile.row;
         rows = tile.rows;
@@ -289,8 +299,9 @@ int go(TileArgs a, int tiles, hipStream_t stream) {
     if (e != hipSuccess) return (int)e;
     const int cols = MODE == kGateUp ? 128 : 64 * NBW;
     a.col_tiles = (a.N + cols - 1) / cols;
+    a.row_tiles = tiles;
     hipLaunchKernelGGL((mxfp4_tile_kernel<MT, NBW, FX, MODE>),
-                       dim3((unsigned)a.col_tiles * (unsigned)tiles), dim3(256), bytes, stream, a);
+                       dim3(((unsigned)a.col_tiles * (unsigned)tiles + 7) / 8 * 8), dim3(256), bytes, stream, a);
     return (int)hipGetLastError();
 }
 

@@ -42,10 +42,11 @@ int launch_rmsnorm(const void *x, const void *residual, const void *weight, floa
 int launch_route(const void *logits, int dtype, const float *bias, const skinny_route_options &o,
                  float *weights, int *ids, int T, int E, hipStream_t stream);
 
-// A product with packed weights.  x: codes [M][K], xe: padded scale rows.
+// A product with packed weights.
 struct Mxfp4Args {
-    const uint8_t *x;
-    const uint8_t *xe;
+    const uint8_t *x;   // bf16 rows (xe null) or codes
+    const uint8_t *xe;  // scale bytes, es a row
+    int es;
     int fmt;
     const uint8_t *W;
     const uint16_t *bias;
@@ -53,7 +54,12 @@ struct Mxfp4Args {
     int out_f32;
     int M, N, K;
 };
+// Codes with padded scale rows, any number of rows.
 int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
+// Few rows: codes, or bf16 rows quantised on the way.
+constexpr int kMxRowsMaxBf16 = 16;
+constexpr int kMxRowsMaxCodes = 64;
+int launch_mxfp4_rows(const Mxfp4Args &a, hipStream_t stream);
 
 // ---------------------------------------------------------------- experts
 // Pairs (token, choice) sorted by expert, and the row tiles of the grouped
@@ -91,6 +97,8 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
                        uint8_t *h, uint8_t *he, int rows, int tiles, hipStream_t stream);
 int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const uint8_t *he,
                     float *y, int rows, int tiles, hipStream_t stream);
+// Few pairs, unsorted: h and he have a row per pair; combines as well.
+int launch_moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream);
 // Bytes of workspace the experts need.
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt);
 int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream);
