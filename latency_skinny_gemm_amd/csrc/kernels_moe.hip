@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256)
     if (e == 0 && t == 0) count[0] = ttotal[0] + ttotal[1] + ttotal[2] + ttotal[3];
     const int n = mine[0] + mine[1] + mine[2] + mine[3];
     for (int i = t; i * tile_rows < n; i += 256)
-        tiles[tile0 + i] = MoeTile{e, row0 + i * tile_rows, min(tile_rows, n - i * tile_rows), 0};
+        tiles[tile0 + i] = MoeTile{e, row0, n, tile0};
     int at = row0;
     for (int w = 0; w < wave; ++w) at += mine[w];
     for (int p = p0; p < p1; p += 64) {
@@ -119,7 +119,9 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
 }  // namespace
 
 // Whether each pair reads its expert's weights for itself.
-static bool moe_unsorted(int T, int k, int E) { return (long)T * k <= 16 || T == 1; }
+static bool moe_unsorted(const MoeArgs &a) {
+    return ((long)a.T * a.k <= 16 || a.T == 1) && mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds;
+}
 
 int moe_tile_rows(int T, int k, int E) {
     const long avg = (long)T * k / E;
@@ -133,7 +135,7 @@ size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
 int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const MoeSpace s = moe_space(a.T, a.k, a.H, a.I, a.E, a.fmt);
     uint8_t *b = (uint8_t *)workspace;
-    if (moe_unsorted(a.T, a.k, a.E)) return launch_moe_rows(a, b + s.h, b + s.he, stream);
+    if (moe_unsorted(a)) return launch_moe_rows(a, b + s.h, b + s.he, stream);
     const int P = a.T * a.k, rows = moe_tile_rows(a.T, a.k, a.E);
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),

@@ -44,16 +44,18 @@ __device__ __forceinline__ unsigned row_max(unsigned v) {
 
 // Workgroup b's place in the work list of n: the workgroups of one XCD (b % 8)
 // take one contiguous run of it, so that neighbours in the list, which share
-// weights, share that XCD's L2.  -1: nothing left.
+// operands, share that XCD's L2.  -1: nothing left.
 __device__ __forceinline__ int xcd_order(int b, int n) {
     const int per = (n + 7) / 8, at = (b & 7) * per + (b >> 3);
     return (b >> 3) < per && at < n ? at : -1;
 }
 
-}  // namespace
+template <int N>
+struct Blocks {
+    static constexpr int value = N;
+};
 
-// Scale bytes of a stage: 16 a row, in whole KB (a load fills one).
-constexpr int tile_scale_bytes(int MT) { return MT * 256 < 1024 ? 1024 : MT * 256; }
+}  // namespace
 
 // The key that piece c of row r is stored under: the rows that share a
 // 256-byte window of the banks get different ones.
@@ -62,37 +64,52 @@ __device__ __forceinline__ int piece_key(int r) {
     return (r / (16 / CPR)) & (CPR - 1);
 }
 
+// Chunks of K (512 each) whose scale bytes a tile keeps in LDS at a time.
+constexpr int kTileScaleChunks = 16;
+constexpr int kTileSlots = 4;  // steps of x in LDS
+constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
+// chunks: those of K, up to kTileScaleChunks.  Scale loads fill whole KB.
+constexpr size_t tile_lds_bytes(int MT, int FX, int chunks) {
+    return (size_t)kTileSlots * tile_slot_bytes(MT, FX) + 1024 + ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
+}
+
 // A workgroup of four waves computes MT * 16 rows x (4 waves * NBW * 16)
-// columns over the whole K.  Stages of 256 K: the rows' codes and scale bytes
-// go to LDS by direct loads (two stages), each wave's weights to registers,
-// both one stage ahead of the products.  A 16-byte piece c of row r sits at
+// columns over the whole K, in steps of 128: the rows' codes go to a ring of
+// four LDS slots by direct loads, each wave's weights to registers (they are
+// used by that wave alone, and packed so that a load is 1 KB in a row), both
+// three steps ahead of the products.  One wait and one barrier a step: the
+// wait leaves the loads of the two younger steps in flight.  The rows' scale
+// bytes are loaded once for 8192 K.  A 16-byte piece c of row r sits at
 // c ^ piece_key(r), so that the 16 rows of a fragment read hit all banks once.
 template <int MT, int NBW, int FX, int MODE>
-__global__ void __launch_bounds__(256) mxfp4_tile_kernel(TileArgs a) {
-    constexpr int RB = FX == kMxE4m3 ? 256 : 128;  // bytes of a row and stage
-    constexpr int CPR = RB / 16;                   // pieces of a row and stage
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+    mxfp4_tile_kernel(TileArgs a) {
+    constexpr int RB = FX == kMxE4m3 ? 128 : 64;   // bytes of a row and step
+    constexpr int CPR = RB / 16;                   // pieces of a row and step
     constexpr int ROWS = MT * 16;
-    constexpr int XS = ROWS * RB;                  // codes of a stage
-    constexpr int STAGE = XS + tile_scale_bytes(MT);  // and 16 scale bytes a row
-    constexpr int XI = XS / 1024 / 4 > 0 ? XS / 1024 / 4 : 1;  // loads per wave
-    constexpr int XW = XS / 1024 < 4 ? XS / 1024 : 4;          // waves that load codes
+    constexpr int SLOT = tile_slot_bytes(MT, FX);
+    constexpr int XI = SLOT / 1024;                // loads of a step
+    constexpr int XPW = (XI + 3) / 4;              // of a wave; the spare ones fill a KB of their own
+    constexpr int LOADS = XPW + 2 * NBW;           // a step's loads of a wave
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
+    unsigned char *const pad = lds_raw + kTileSlots * SLOT;
+    unsigned char *const scales = pad + 1024;
 
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int row_tiles = MODE == kDense ? a.row_tiles : a.count[0];
-    const int at = xcd_order(blockIdx.x, a.col_tiles * row_tiles);
+    // The work list goes expert by expert (dense: one), in it column tile by
+    // column tile, the row tiles of a column tile side by side: those share
+    // their weights, and all of an expert's share its rows of x.
+    const int tiles = MODE == kDense ? a.row_tiles : a.count[0];
+    const int at = xcd_order(blockIdx.x, a.col_tiles * tiles);
     if (at < 0) return;
-    const int ct = at / row_tiles, rt = at - ct * row_tiles;  // column tile, row tile
-    int row0 = rt * ROWS, rows = min(ROWS, a.M - row0), expert = 0;
-    if constexpr (MODE != kDense) {
-        const MoeTile tile = a.tiles[rt];
-        row0 = tile.row;
-        rows = tile.rows;
-        expert = tile.expert;
-    }
+    MoeTile own{0, 0, a.M, 0};
+    if constexpr (MODE != kDense) own = a.tiles[at / a.col_tiles];
+    const int nt = (own.rows + ROWS - 1) / ROWS, local = at - own.first * a.col_tiles;
+    const int ct = local / nt, rt = local - ct * nt;  // column tile, row tile
+    const int row0 = own.row + rt * ROWS, rows = min(ROWS, own.rows - rt * ROWS), expert = own.expert;
     const int live = (rows + 15) / 16;  // row blocks that hold rows
-    const int KS = mxfp4_steps(a.K), nst = (KS + 1) / 2;
+    const int KS = mxfp4_steps(a.K), KC = mxfp4_chunks(a.K);
     const size_t gb = mxfp4_group_bytes(a.K);
     const unsigned rowb = FX == kMxE4m3 ? (unsigned)a.K : (unsigned)a.K / 2;
     const unsigned es = (unsigned)mx_scale_stride(a.K);
@@ -100,7 +117,7 @@ __global__ void __launch_bounds__(256) mxfp4_tile_kernel(TileArgs a) {
     // this wave's column groups
     const int ng = mxfp4_groups(MODE == kGateUp ? 2 * a.N : a.N);
     const uint8_t *We = a.W + (size_t)expert * ng * gb;
-    Rsrc wr[NBW], sr[NBW];
+    Rsrc wr[NBW];
 #pragma unroll
     for (int b = 0; b < NBW; ++b) {
         int j;
@@ -113,54 +130,46 @@ __global__ void __launch_bounds__(256) mxfp4_tile_kernel(TileArgs a) {
             j = (ct * 4 + wave) * NBW + b;
             in = j < ng;
         }
-        wr[b] = make_rsrc(We + (in ? j * gb : 0), in ? (unsigned)KS * 1024u : 0u);
-        sr[b] = make_rsrc(We + (in ? j * gb : 0) + (size_t)KS * 1024,
-                          in ? (unsigned)mxfp4_chunks(a.K) * 256u : 0u);
+        wr[b] = make_rsrc(We + (in ? j * gb : 0), in ? (unsigned)gb : 0u);
     }
 
     // this lane's pieces of the rows
     const Rsrc xr = make_rsrc(a.x, a.x_rows * rowb);
     const Rsrc er = make_rsrc(a.xe, a.x_rows * es);
-    auto row_of = [&](int r) -> int {  // x row of tile row r < rows
-        if constexpr (MODE == kGateUp) return a.pairs[row0 + r] / a.top;
-        else return row0 + r;
+    auto row_of = [&](int r) -> unsigned {  // x row of tile row r < rows
+        if constexpr (MODE == kGateUp) return (unsigned)(a.pairs[row0 + r] / a.top);
+        else return (unsigned)(row0 + r);
     };
-    unsigned xoff[XI];
-    unsigned xcol[XI];
+    unsigned xoff[XPW], xcol[XPW];
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-        const int lin = ((wave * XI + i) * 64 + lane);
+    for (int i = 0; i < XPW; ++i) {
+        const int q = wave + 4 * i, lin = q * 64 + lane;
         const int r = lin / CPR, c = (lin % CPR) ^ piece_key<CPR>(r);
         xcol[i] = (unsigned)c * 16u;
-        xoff[i] = r < rows && wave < XW ? (unsigned)row_of(r) * rowb + xcol[i] : kOOB;
+        xoff[i] = q < XI && r < rows ? row_of(r) * rowb + xcol[i] : kOOB;
     }
-    const int erow = wave * 64 + lane;
-    const unsigned eoff = erow < rows ? (unsigned)row_of(erow) * es : kOOB;
 
-    auto issue_x = [&](int slot, int st) {
-        unsigned char *base = lds_raw + slot * STAGE;
-        if (wave < XW)
+    u32x4 w[4][NBW];
+    // The chunk's dword of scale bytes, loaded with every step (three loads in
+    // four hit the L1): kept from step to step it would be copied between
+    // registers, and the compiler waits for nearly all loads before a copy.
+    unsigned ws[4][NBW];
+    auto issue = [&](int slot, int st) {
+        const unsigned k = (unsigned)st * RB;
 #pragma unroll
-            for (int i = 0; i < XI; ++i) {
-                const unsigned k = (unsigned)st * RB;
-                lds_load16<kCacheDefault>(xr, base + (wave * XI + i) * 1024,
-                                          k + xcol[i] < rowb ? xoff[i] + k : kOOB);
-            }
-        if (wave * 64 < ROWS)
-            lds_load16<kCacheDefault>(er, base + XS + wave * 1024,
-                                      eoff == kOOB ? kOOB : eoff + (unsigned)(st / 2) * 16u);
-    };
-    u32x4 w[2][2][NBW];  // [buffer][step][group]
-    unsigned ws[2][NBW];
-    auto issue_w = [&](int buf, int st) {
-#pragma unroll
-        for (int b = 0; b < NBW; ++b) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                w[buf][s][b] = load16<kCacheDefault>(wr[b], (unsigned)(2 * st + s) * 1024u + lane * 16u);
-            ws[buf][b] = __builtin_amdgcn_raw_buffer_load_b32(
-                sr[b], (unsigned)(st / 2) * 256u + lane * 4u, 0, kCacheDefault);
+        for (int i = 0; i < XPW; ++i) {
+            const int q = wave + 4 * i;
+            lds_load16<kCacheDefault>(xr, q < XI ? lds_raw + slot * SLOT + q * 1024 : pad,
+                                      xoff[i] != kOOB && k + xcol[i] < rowb ? xoff[i] + k : kOOB);
         }
+#pragma unroll
+        for (int b = 0; b < NBW; ++b)
+            w[slot][b] = load16<kCacheDefault>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
+#pragma unroll
+        for (int b = 0; b < NBW; ++b)
+            ws[slot][b] = __builtin_amdgcn_raw_buffer_load_b32(
+                wr[b], st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB, 0,
+                kCacheDefault);
     };
 
     f32x4 acc[MT][NBW];
@@ -170,65 +179,87 @@ __global__ void __launch_bounds__(256) mxfp4_tile_kernel(TileArgs a) {
         for (int b = 0; b < NBW; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int fr = lane & 15, fg = lane >> 4;
-    auto compute = [&](int slot, int buf, int st) {
-        const unsigned char *base = lds_raw + slot * STAGE;
-        int wsc[NBW];
+    int sstride = 0;  // bytes between the scale rows in LDS
+    auto compute = [&](auto blocks, int s, int chunk) {
+        const unsigned char *base = lds_raw + s * SLOT;
 #pragma unroll
-        for (int b = 0; b < NBW; ++b) wsc[b] = (int)(ws[buf][b] >> (16 * (st & 1)));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (m >= live) break;
+        for (int m = 0; m < decltype(blocks)::value; ++m) {
             const unsigned char *rp = base + (m * 16 + fr) * RB;
-            const uint2 ev = *reinterpret_cast<const uint2 *>(base + XS + (m * 16 + fr) * 16 +
-                                                              8 * (st & 1));
+            const int xsc = (int)(*reinterpret_cast<const unsigned *>(
+                                      scales + (m * 16 + fr) * sstride + chunk * 16 + s * 4) >> (8 * fg));
+            const u32x4 p = *reinterpret_cast<const u32x4 *>(rp + ((fg ^ piece_key<CPR>(fr)) * 16));
+            i32x8 xf{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+            if constexpr (FX == kMxE4m3) {
+                const u32x4 q = *reinterpret_cast<const u32x4 *>(rp + (((4 + fg) ^ piece_key<CPR>(fr)) * 16));
+                xf = i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
+            }
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                i32x8 xf{0, 0, 0, 0, 0, 0, 0, 0};
-                if constexpr (FX == kMxE4m3) {
-                    const u32x4 p0 = *reinterpret_cast<const u32x4 *>(rp + (((8 * s + fg) ^ piece_key<CPR>(fr)) * 16));
-                    const u32x4 p1 = *reinterpret_cast<const u32x4 *>(rp + (((8 * s + 4 + fg) ^ piece_key<CPR>(fr)) * 16));
-                    xf = i32x8{(int)p0.x, (int)p0.y, (int)p0.z, (int)p0.w,
-                               (int)p1.x, (int)p1.y, (int)p1.z, (int)p1.w};
-                } else {
-                    const u32x4 p0 = *reinterpret_cast<const u32x4 *>(rp + (((4 * s + fg) ^ piece_key<CPR>(fr)) * 16));
-                    xf = i32x8{(int)p0.x, (int)p0.y, (int)p0.z, (int)p0.w, 0, 0, 0, 0};
-                }
-                const int xsc = (int)((s ? ev.y : ev.x) >> (8 * fg));
-#pragma unroll
-                for (int b = 0; b < NBW; ++b) {
-                    const u32x4 q = w[buf][s][b];
-                    const i32x8 wf{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
-                    if (s == 0)
-                        acc[m][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, xf, acc[m][b], kMxE2m1, FX, 0, wsc[b], 0, xsc);
-                    else
-                        acc[m][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, xf, acc[m][b], kMxE2m1, FX, 1, wsc[b], 0, xsc);
-                }
+            for (int b = 0; b < NBW; ++b) {
+                const u32x4 q = w[s][b];
+                const i32x8 wf{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+                f32x4 &d = acc[m][b];
+                const int sc = (int)ws[s][b];
+                if (s == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 0, sc, 0, xsc);
+                if (s == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 1, sc, 0, xsc);
+                if (s == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 2, sc, 0, xsc);
+                if (s == 3) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 3, sc, 0, xsc);
             }
         }
     };
 
-    issue_x(0, 0);
-    issue_w(0, 0);
-    for (int st = 0; st < nst; st += 2) {
-        // nst is the same for every wave: every wave reaches every barrier
-        wait_vmcnt_lds<0>();
-        barrier_nofence();
-        if (st + 1 < nst) {
-            issue_x(1, st + 1);
-            issue_w(1, st + 1);
+    // L: row blocks to compute.  One straight loop for each L: with a test per
+    // block the accumulators were copied at every join.
+    auto run = [&](auto L) {
+    for (int c0 = 0; c0 < KC; c0 += kTileScaleChunks) {
+        // the scale bytes of these chunks: piece q of row r is slot r * nc + q
+        const int nc = min(kTileScaleChunks, KC - c0);
+        sstride = nc * 16;
+        if (c0 > 0) {  // every wave has read the bytes that these replace
+            wait_vmcnt_lds<0>();
+            barrier_nofence();
         }
-        compute(0, 0, st);
-        if (st + 1 >= nst) break;
-        wait_vmcnt_lds<0>();
-        barrier_nofence();
-        if (st + 2 < nst) {
-            issue_x(0, st + 2);
-            issue_w(0, st + 2);
+        for (int b = wave * 64; b < ROWS * nc; b += 256) {
+            const int r = (b + lane) / nc, q = (b + lane) - r * nc;
+            lds_load16<kCacheDefault>(er, scales + b * 16,
+                                      r < rows ? row_of(r) * es + (unsigned)(c0 + q) * 16u : kOOB);
         }
-        compute(1, 1, st + 1);
+        if (c0 == 0) {  // these are younger: waiting for them covers the bytes
+            issue(0, 0);
+            issue(1, 1);
+            issue(2, 2);
+        } else {
+            wait_vmcnt_lds<0>();
+        }
+        // The steps of the last chunk past K are gone through as zeros: left
+        // early, the loop would carry loads that the compiler then waits for
+        // at its head.
+        for (int c = 0; c < nc; ++c) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                // all but the two younger steps' loads have landed; the counts
+                // are the same for every wave, so every wave reaches every barrier
+                wait_vmcnt_lds<2 * LOADS>();
+                barrier_nofence();
+                issue((s + 3) & 3, (c0 + c) * 4 + s + 3);
+                __builtin_amdgcn_sched_barrier(0);
+                compute(L, s, c);
+            }
+        }
     }
+    };
+    if constexpr (MT == 1) {
+        run(Blocks<1>{});
+    } else if constexpr (MT == 2) {
+        if (live == 1) run(Blocks<1>{});
+        else run(Blocks<2>{});
+    } else {
+        static_assert(MT == 4, "row blocks");
+        if (live == 1) run(Blocks<1>{});
+        else if (live == 2) run(Blocks<2>{});
+        else if (live == 3) run(Blocks<3>{});
+        else run(Blocks<4>{});
+    }
+    wait_vmcnt_lds<0>();  // no load to LDS outlives the loop
 
     // lane (fr, fg) holds, of row m * 16 + fr, columns 4 fg + 0..3 of each group
 #pragma unroll
@@ -292,10 +323,12 @@ namespace {
 
 template <int MT, int NBW, int FX, int MODE>
 int go(TileArgs a, int tiles, hipStream_t stream) {
-    constexpr size_t bytes = 2 * (MT * 16 * (FX == kMxE4m3 ? 256 : 128) + tile_scale_bytes(MT));
+    const int chunks = mxfp4_chunks(a.K) < kTileScaleChunks ? mxfp4_chunks(a.K) : kTileScaleChunks;
+    const size_t bytes = tile_lds_bytes(MT, FX, chunks);
+    constexpr size_t most = tile_lds_bytes(MT, FX, kTileScaleChunks);
     static std::atomic<unsigned long long> lds_set{0};
     const hipError_t e = allow_dynamic_lds(
-        reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE>), bytes, lds_set);
+        reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE>), most, lds_set);
     if (e != hipSuccess) return (int)e;
     const int cols = MODE == kGateUp ? 128 : 64 * NBW;
     a.col_tiles = (a.N + cols - 1) / cols;
@@ -310,13 +343,11 @@ int pick(const TileArgs &a, int fmt, int rows, int tiles, hipStream_t stream) {
     if (fmt == kMxE4m3) {
         if (rows <= 16) return go<1, NBW, kMxE4m3, MODE>(a, tiles, stream);
         if (rows <= 32) return go<2, NBW, kMxE4m3, MODE>(a, tiles, stream);
-        if (rows <= 64) return go<4, NBW, kMxE4m3, MODE>(a, tiles, stream);
-        return go<8, NBW, kMxE4m3, MODE>(a, tiles, stream);
+        return go<4, NBW, kMxE4m3, MODE>(a, tiles, stream);
     }
     if (rows <= 16) return go<1, NBW, kMxE2m1, MODE>(a, tiles, stream);
     if (rows <= 32) return go<2, NBW, kMxE2m1, MODE>(a, tiles, stream);
-    if (rows <= 64) return go<4, NBW, kMxE2m1, MODE>(a, tiles, stream);
-    return go<8, NBW, kMxE2m1, MODE>(a, tiles, stream);
+    return go<4, NBW, kMxE2m1, MODE>(a, tiles, stream);
 }
 
 }  // namespace
@@ -333,8 +364,9 @@ int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
     a.M = p.M;
     a.N = p.N;
     a.K = p.K;
-    const int rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-    return pick<1, kDense>(a, p.fmt, rows, (p.M + rows - 1) / rows, stream);
+    const int tiles = (p.M + 63) / 64;
+    return p.fmt == kMxE4m3 ? go<4, 2, kMxE4m3, kDense>(a, tiles, stream)
+                            : go<4, 2, kMxE2m1, kDense>(a, tiles, stream);
 }
 
 // The two products of the routed experts (kernels_moe.hip sorts and combines).

@@ -11,6 +11,7 @@
 // the weights' latency), which saves the launch that would do it.
 #include "device_common.h"
 #include "internal.h"
+#include "lds_limit.h"
 #include "moe_internal.h"
 #include "mx_common.h"
 
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     constexpr bool ONE = MODE != kRowsDense;  // one row: only lanes of row 0 hold data
     constexpr int ROWS = ONE ? 1 : MT * 16;
     __shared__ float part[NW][ROWS][R * 16];
+    extern __shared__ __attribute__((aligned(16))) uint8_t row_lds[];  // gate-up: the row's codes and scales
     const int t = threadIdx.x, lane = t & 63, fr = lane & 15, fg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int KS = mxfp4_steps(a.K);
@@ -185,11 +187,16 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     const unsigned xrows = MODE == kRowsGateUp ? 1u : MODE == kRowsDown ? (unsigned)a.top : (unsigned)a.M;
     const Rsrc xr = make_rsrc(a.x + x0 * rowb, xrows * rowb);
     const Rsrc er = make_rsrc(BF16 ? nullptr : a.xe + x0 * a.es, BF16 ? 0u : xrows * a.es);
+    constexpr bool LDS_ROW = MODE == kRowsGateUp;
     constexpr int XV = BF16 ? 4 : FX == kMxE4m3 ? 2 : 1;  // 16-byte pieces of a lane and step
+    constexpr int XM = LDS_ROW ? 0 : MT;                  // blocks whose rows come straight to registers
+    constexpr unsigned CB = FX == kMxE4m3 ? 128u : 64u;   // bytes of a row's codes in a step
 
-    for (int u0 = wave; u0 < units; u0 += NW * U) {
-        u32x4 w[U][R], x[U][MT][XV];
-        unsigned ws[U][R], xs[U][MT];
+    const int batches = (units + NW * U - 1) / (NW * U);  // the same for every wave
+    for (int it = 0; it < batches; ++it) {
+        const int u0 = it * NW * U + wave;
+        u32x4 w[U][R], x[U][XM > 0 ? XM : 1][XV];
+        unsigned ws[U][R], xs[U][XM > 0 ? XM : 1];
         float wt[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -220,10 +227,10 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                     wr, s < 0 ? kOOB : (unsigned)KS * 1024u + so / 4u * 256u + lane * 4u, 0, kCacheDefault);
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = ONE ? (MODE == kRowsDown ? j : 0) : m * 16 + fr;
+            for (int m = 0; m < XM; ++m) {
+                const int r = ONE ? j : m * 16 + fr;
                 const bool has = s >= 0 && (ONE ? fr == 0 : r < a.M);
-                const unsigned stepb = BF16 ? 256u : FX == kMxE4m3 ? 128u : 64u;
+                const unsigned stepb = BF16 ? 256u : CB;
 #pragma unroll
                 for (int v = 0; v < XV; ++v) {
                     const unsigned in = so * stepb + (BF16 ? bf16_piece<FX>(fg, v)
@@ -240,6 +247,25 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
         // every load of the batch goes out before the first product; steps past
         // the end hold zeros, which add nothing
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (LDS_ROW) {
+            // The one row, quantised once by the workgroup while the weights
+            // are on their way: 8 values a thread, a block per quad; codes to
+            // the end of the last step (zeros past K), then the scale bytes.
+            if (it == 0) {
+                uint8_t *const rs = row_lds + (size_t)KS * CB;
+                for (int i = t; i < KS * 16; i += NW * 64) {
+                    const u32x4 v = load16<kCacheDefault>(xr, (unsigned)i * 16u < rowb ? (unsigned)i * 16u : kOOB);
+                    const unsigned am = quad_max(fold16(amax8(v)));
+                    const int e = mx_exponent16<FX>(am);
+                    if constexpr (FX == kMxE4m3)
+                        *reinterpret_cast<uint2 *>(row_lds + i * 8) = codes8_e4m3(v, scale_of(e));
+                    else
+                        *reinterpret_cast<unsigned *>(row_lds + i * 4) = codes8_e2m1(v, scale_of(e));
+                    if ((i & 3) == 0) rs[i / 4] = (uint8_t)e;
+                }
+                __syncthreads();
+            }
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int u = u0 + i * NW;
@@ -247,7 +273,17 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 Frag f;
-                if constexpr (BF16) {
+                if constexpr (LDS_ROW) {
+                    // every lane row holds the one row; only column 0 of the
+                    // result is used
+                    const int sl = min(s, KS - 1);
+                    const uint8_t *rp = row_lds + sl * CB + fg * 16;
+                    const u32x4 p = *reinterpret_cast<const u32x4 *>(rp);
+                    const u32x4 q = *reinterpret_cast<const u32x4 *>(rp + (FX == kMxE4m3 ? 64 : 0));
+                    f.q = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
+                                        : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+                    f.e = row_lds[(size_t)KS * CB + sl * 4 + fg];
+                } else if constexpr (BF16) {
                     f = quantise_frag<FX>(x[i][m], fg);
                 } else {
                     const u32x4 p = x[i][m][0], q = x[i][m][XV - 1];
@@ -324,8 +360,17 @@ namespace {
 
 template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U>
 int go(const RowArgs &a, size_t grid, hipStream_t stream) {
+    size_t lds = 0;
+    if (MODE == kRowsGateUp) {
+        lds = mxfp4_row_lds_bytes(FX, a.K);
+        static std::atomic<unsigned long long> lds_set{0};
+        const hipError_t e = allow_dynamic_lds(
+            reinterpret_cast<const void *>(&mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U>),
+            kMxRowMaxLds, lds_set);
+        if (e != hipSuccess) return (int)e;
+    }
     hipLaunchKernelGGL((mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U>), dim3((unsigned)grid),
-                       dim3(NW * 64), 0, stream, a);
+                       dim3(NW * 64), lds, stream, a);
     return (int)hipGetLastError();
 }
 

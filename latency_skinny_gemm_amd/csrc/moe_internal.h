@@ -64,11 +64,13 @@ int launch_mxfp4_rows(const Mxfp4Args &a, hipStream_t stream);
 // ---------------------------------------------------------------- experts
 // Pairs (token, choice) sorted by expert, and the row tiles of the grouped
 // products.
+// A tile's expert, whole: its tiles are first .. first + ceil(rows / height) - 1,
+// over sorted rows row .. row + rows - 1.
 struct MoeTile {
     int expert;
-    int row;   // first sorted row
-    int rows;  // rows of this tile
-    int pad;
+    int row;
+    int rows;
+    int first;
 };
 // Rows a tile may hold, by the average number of pairs an expert gets.
 int moe_tile_rows(int T, int k, int E);
@@ -97,6 +99,11 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
                        uint8_t *h, uint8_t *he, int rows, int tiles, hipStream_t stream);
 int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const uint8_t *he,
                     float *y, int rows, int tiles, hipStream_t stream);
+// LDS of a row's codes and scale bytes, in whole steps, and the most of it.
+constexpr size_t mxfp4_row_lds_bytes(int fmt, int K) {
+    return (size_t)mxfp4_steps(K) * ((fmt == SKG_MX_E4M3 ? 128 : 64) + 4);
+}
+constexpr size_t kMxRowMaxLds = 128 * 1024;
 // Few pairs, unsorted: h and he have a row per pair; combines as well.
 int launch_moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream);
 // Bytes of workspace the experts need.
