@@ -46,7 +46,8 @@ int check_mx(int format, int M, int K) {
 // Quantised rows in a workspace: codes, then padded scale rows.
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t linear_workspace_bytes(size_t M, int K) {
-    return round256(M * (size_t)K) + round256(M * (size_t)mx_scale_stride(K));
+    // e4m3 codes are the larger of the two formats
+    return round256(M * (size_t)mx_code_stride(SKG_MX_E4M3, K)) + round256(M * (size_t)mx_scale_stride(K));
 }
 
 int check_linear(int M, int N, int K) {
@@ -62,8 +63,9 @@ int check_moe(int T, int k, int H, int I, int E) {
         k > SKG_ROUTE_MAX_K)
         return SKG_ERR_UNSUPPORTED;
     const long P = (long)T * k, wide = H > I ? H : I;
-    if (P > kMaxBufferBytes || (long)T * H > kMaxBufferBytes || P * I > kMaxBufferBytes ||
-        P * wide * 4 >= 1L << 40)
+    const int f = SKG_MX_E4M3;  // the wider codes: a row map spans less than 2 GiB
+    if (P > kMaxBufferBytes || (long)T * mx_code_stride(f, H) > kMaxBufferBytes ||
+        P * mx_code_stride(f, I) > kMaxBufferBytes || P * wide * 4 >= 1L << 40)
         return SKG_ERR_UNSUPPORTED;
     return SKG_OK;
 }
@@ -82,7 +84,7 @@ extern "C" int skinny_quant_mx(const void *x, void *q, void *e8m0, int format, i
     const size_t n = (size_t)M * K;
     const Span outs[] = {{q, code_bytes(format, n)}, {e8m0, n / 32}}, ins[] = {{x, n * 2}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    return status(launch_quant_mx(x, q, e8m0, format, M, K, 0, stream));
+    return status(launch_quant_mx(x, q, e8m0, format, M, K, false, stream));
 }
 
 extern "C" int skinny_dequant_mx(const void *q, const void *e8m0, int format, void *out, int M,
@@ -192,7 +194,7 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
                         {packed, mxfp4_packed_bytes(1, N, K)},
                         {bias, (size_t)N * 2}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    Mxfp4Args a{(const uint8_t *)x, (const uint8_t *)x_e8m0, K / 32, x_format,
+    Mxfp4Args a{(const uint8_t *)x, (int)code_bytes(x_format, K), (const uint8_t *)x_e8m0, K / 32, x_format,
                 (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
     const bool few = M <= kMxRowsMaxCodes;
     if (few && (x_e8m0 || M <= kMxRowsMaxBf16)) return status(launch_mxfp4_rows(a, stream));
@@ -200,13 +202,14 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     unsigned *tk = nullptr;
     rc = acquire(stream, floats_of(linear_workspace_bytes((size_t)M, K)), 0, &ws, &tk);
     if (rc != SKG_OK) return rc;
-    uint8_t *codes = (uint8_t *)ws, *scales = codes + round256(n);
+    uint8_t *codes = (uint8_t *)ws, *scales = codes + round256((size_t)M * mx_code_stride(x_format, K));
     int e;
     if (x_e8m0) {
         e = launch_pad_scales(x_e8m0, scales, M, K, stream);
     } else {
-        e = launch_quant_mx(x, codes, scales, x_format, M, K, mx_scale_stride(K), stream);
+        e = launch_quant_mx(x, codes, scales, x_format, M, K, true, stream);
         a.x = codes;
+        a.xs = mx_code_stride(x_format, K);
     }
     if (e != (int)hipSuccess) return SKG_ERR_HIP;
     a.xe = scales;

@@ -49,6 +49,11 @@ __device__ __forceinline__ void lds_load16(Rsrc r, unsigned char *dst, unsigned 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, off, 0, 0, POLICY);
 }
 
+// The same with 4 bytes per lane, at dst + 4 * lane.
+__device__ __forceinline__ void lds_load4(Rsrc r, unsigned char *dst, unsigned off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 4, off, 0, 0, kCacheDefault);
+}
+
 // s_waitcnt vmcnt(N) lgkmcnt(0) (gfx9 encoding: vmcnt in bits 3:0 and
 // 15:14, expcnt 6:4 left at its maximum, lgkmcnt 11:8 = 0).  Vector memory
 // loads return in issue order, so vmcnt(N) means all but this wave's last

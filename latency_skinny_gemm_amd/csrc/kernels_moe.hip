@@ -103,10 +103,9 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
         return here;
     };
     const size_t P = (size_t)T * k;
-    const size_t half = fmt == kMxE4m3 ? 1 : 2;
-    s.xq = take((size_t)T * H / half);
+    s.xq = take((size_t)T * mx_code_stride(fmt, H));
     s.xe = take((size_t)T * mx_scale_stride(H));
-    s.h = take(P * I / half);
+    s.h = take(P * mx_code_stride(fmt, I));
     s.he = take(P * mx_scale_stride(I));
     s.y = take(P * H * 4);
     s.pairs = take(P * 4);
@@ -140,7 +139,7 @@ int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),
                          (const int *)(b + s.pairs)};
-    int e = launch_quant_mx(a.x, b + s.xq, b + s.xe, a.fmt, a.T, a.H, mx_scale_stride(a.H), stream);
+    int e = launch_quant_mx(a.x, b + s.xq, b + s.xe, a.fmt, a.T, a.H, true, stream);
     if (e != (int)hipSuccess) return e;
     hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)a.E), dim3(256), (size_t)a.E * 4, stream,
                        a.ids, P, a.E, rows, (int *)(b + s.pairs), (MoeTile *)(b + s.tiles),

@@ -12,26 +12,29 @@ namespace skg {
 
 // Thread i quantises values [8i, 8i + 8): one 16-byte load, one store of 8
 // (e4m3) or 4 (e2m1) bytes, and the block's byte from one lane of the quad
-// that holds the block.  PAD: scale rows are e_stride bytes apart (the
-// products' workspace) and the bytes past K / 32 are written as 0.
+// that holds the block.  PAD: rows of codes and scales are q_stride and
+// e_stride bytes apart (the products' workspace) and the scale bytes past
+// K / 32 are written as 0.
 template <int FMT, bool PAD>
 __global__ void __launch_bounds__(256)
     quant_mx_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q,
-                    uint8_t *__restrict__ e8, unsigned n8, unsigned k8, unsigned e_stride) {
+                    uint8_t *__restrict__ e8, unsigned n8, unsigned k8, unsigned q_stride,
+                    unsigned e_stride) {
     const unsigned i = blockIdx.x * 256u + threadIdx.x;
     if (i >= n8) return;  // n8 is a multiple of 4: whole quads leave
     float v[8];
     bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(x + (size_t)i * 8), v);
-    const int e = mx_store8<FMT>(v, q, (size_t)i * 8);
-    if ((i & 3u) != 0) return;
     if constexpr (!PAD) {
-        e8[i / 4] = (uint8_t)e;
+        const int e = mx_store8<FMT>(v, q, (size_t)i * 8);
+        if ((i & 3u) == 0) e8[i / 4] = (uint8_t)e;
     } else {
-        const unsigned row = i / k8, b = (i - row * k8) / 4;
+        const unsigned row = i / k8, c = i - row * k8;
+        const int e = mx_store8<FMT>(v, q + (size_t)row * q_stride, (size_t)c * 8);
+        if ((i & 3u) != 0) return;
         uint8_t *er = e8 + (size_t)row * e_stride;
-        er[b] = (uint8_t)e;
-        if (b == k8 / 4 - 1)
-            for (unsigned z = b + 1; z < e_stride; ++z) er[z] = 0;
+        er[c / 4] = (uint8_t)e;
+        if (c / 4 == k8 / 4 - 1)
+            for (unsigned z = k8 / 4; z < e_stride; ++z) er[z] = 0;
     }
 }
 
@@ -115,29 +118,14 @@ namespace {
 unsigned blocks_of(size_t n) { return (unsigned)((n + 255) / 256); }
 }  // namespace
 
-int launch_quant_mx(const void *x, void *q, void *e8, int fmt, int M, int K, int e_stride,
+int launch_quant_mx(const void *x, void *q, void *e8, int fmt, int M, int K, bool padded,
                     hipStream_t stream) {
     const unsigned n8 = (unsigned)((size_t)M * K / 8), k8 = (unsigned)K / 8;
-    const dim3 grid(blocks_of(n8)), block(256);
-    const auto *xs = (const uint16_t *)x;
-    auto *qs = (uint8_t *)q;
-    auto *es = (uint8_t *)e8;
-    const bool pad = e_stride != 0;
-    if (fmt == kMxE4m3) {
-        if (pad)
-            hipLaunchKernelGGL((quant_mx_kernel<kMxE4m3, true>), grid, block, 0, stream, xs, qs, es,
-                               n8, k8, (unsigned)e_stride);
-        else
-            hipLaunchKernelGGL((quant_mx_kernel<kMxE4m3, false>), grid, block, 0, stream, xs, qs,
-                               es, n8, k8, 0u);
-    } else {
-        if (pad)
-            hipLaunchKernelGGL((quant_mx_kernel<kMxE2m1, true>), grid, block, 0, stream, xs, qs, es,
-                               n8, k8, (unsigned)e_stride);
-        else
-            hipLaunchKernelGGL((quant_mx_kernel<kMxE2m1, false>), grid, block, 0, stream, xs, qs,
-                               es, n8, k8, 0u);
-    }
+    const unsigned qs = (unsigned)mx_code_stride(fmt, K), es = (unsigned)mx_scale_stride(K);
+    auto *const f = fmt == kMxE4m3 ? (padded ? quant_mx_kernel<kMxE4m3, true> : quant_mx_kernel<kMxE4m3, false>)
+                                   : (padded ? quant_mx_kernel<kMxE2m1, true> : quant_mx_kernel<kMxE2m1, false>);
+    hipLaunchKernelGGL(f, dim3(blocks_of(n8)), dim3(256), 0, stream, (const uint16_t *)x,
+                       (uint8_t *)q, (uint8_t *)e8, n8, k8, qs, es);
     return (int)hipGetLastError();
 }
 

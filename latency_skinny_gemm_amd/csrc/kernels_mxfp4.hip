@@ -14,7 +14,8 @@ namespace {
 enum { kDense = 0, kGateUp = 1, kDown = 2 };
 
 struct TileArgs {
-    const uint8_t *x;       // codes, K (or K / 2) bytes a row
+    const uint8_t *x;       // codes, x_stride bytes from row to row
+    unsigned x_stride;
     const uint8_t *xe;      // scale bytes, mx_scale_stride(K) a row
     unsigned x_rows;        // rows of x
     const uint8_t *W;       // packed
@@ -69,8 +70,9 @@ constexpr int kTileScaleChunks = 16;
 constexpr int kTileSlots = 4;  // steps of x in LDS
 constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
 // chunks: those of K, up to kTileScaleChunks.  Scale loads fill whole KB.
-constexpr size_t tile_lds_bytes(int MT, int FX, int chunks) {
-    return (size_t)kTileSlots * tile_slot_bytes(MT, FX) + 1024 + ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
+constexpr int tile_wscale_bytes(int NBW) { return 2 * 4 * NBW * 256; }  // two chunks, four waves
+constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int chunks) {
+    return (size_t)kTileSlots * tile_slot_bytes(MT, FX) + 1024 + tile_wscale_bytes(NBW) + ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
 }
 
 // A workgroup of four waves computes MT * 16 rows x (4 waves * NBW * 16)
@@ -90,10 +92,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     constexpr int SLOT = tile_slot_bytes(MT, FX);
     constexpr int XI = SLOT / 1024;                // loads of a step
     constexpr int XPW = (XI + 3) / 4;              // of a wave; the spare ones fill a KB of their own
-    constexpr int LOADS = XPW + 2 * NBW;           // a step's loads of a wave
+    constexpr int LOADS = XPW + NBW;               // a step's loads of a wave, at least
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     unsigned char *const pad = lds_raw + kTileSlots * SLOT;
-    unsigned char *const scales = pad + 1024;
+    unsigned char *const scales = pad + 1024 + tile_wscale_bytes(NBW);
 
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     const int live = (rows + 15) / 16;  // row blocks that hold rows
     const int KS = mxfp4_steps(a.K), KC = mxfp4_chunks(a.K);
     const size_t gb = mxfp4_group_bytes(a.K);
-    const unsigned rowb = FX == kMxE4m3 ? (unsigned)a.K : (unsigned)a.K / 2;
+    const unsigned rowb = FX == kMxE4m3 ? (unsigned)a.K : (unsigned)a.K / 2, xs = a.x_stride;
     const unsigned es = (unsigned)mx_scale_stride(a.K);
 
     // this wave's column groups
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     }
 
     // this lane's pieces of the rows
-    const Rsrc xr = make_rsrc(a.x, a.x_rows * rowb);
+    const Rsrc xr = make_rsrc(a.x, (a.x_rows - 1) * xs + rowb);
     const Rsrc er = make_rsrc(a.xe, a.x_rows * es);
     auto row_of = [&](int r) -> unsigned {  // x row of tile row r < rows
         if constexpr (MODE == kGateUp) return (unsigned)(a.pairs[row0 + r] / a.top);
@@ -146,14 +148,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         const int q = wave + 4 * i, lin = q * 64 + lane;
         const int r = lin / CPR, c = (lin % CPR) ^ piece_key<CPR>(r);
         xcol[i] = (unsigned)c * 16u;
-        xoff[i] = q < XI && r < rows ? row_of(r) * rowb + xcol[i] : kOOB;
+        xoff[i] = q < XI && r < rows ? row_of(r) * xs + xcol[i] : kOOB;
     }
 
     u32x4 w[4][NBW];
-    // The chunk's dword of scale bytes, loaded with every step (three loads in
-    // four hit the L1): kept from step to step it would be copied between
-    // registers, and the compiler waits for nearly all loads before a copy.
-    unsigned ws[4][NBW];
+    // A chunk's dwords of scale bytes go to LDS with its first step: loaded
+    // with every step they would be asked of the L1 again while on their way.
+    unsigned char *const wscales = pad + 1024 + wave * (NBW * 256);  // two chunks, 4 waves apart
     auto issue = [&](int slot, int st) {
         const unsigned k = (unsigned)st * RB;
 #pragma unroll
@@ -165,11 +166,11 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 #pragma unroll
         for (int b = 0; b < NBW; ++b)
             w[slot][b] = load16<kCacheDefault>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
+        if (slot == 0)
 #pragma unroll
-        for (int b = 0; b < NBW; ++b)
-            ws[slot][b] = __builtin_amdgcn_raw_buffer_load_b32(
-                wr[b], st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB, 0,
-                kCacheDefault);
+            for (int b = 0; b < NBW; ++b)
+                lds_load4(wr[b], wscales + ((st / 4) & 1) * (4 * NBW * 256) + b * 256,
+                          st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB);
     };
 
     f32x4 acc[MT][NBW];
@@ -182,6 +183,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     int sstride = 0;  // bytes between the scale rows in LDS
     auto compute = [&](auto blocks, int s, int chunk) {
         const unsigned char *base = lds_raw + s * SLOT;
+        int wsc[NBW];
+#pragma unroll
+        for (int b = 0; b < NBW; ++b)
+            wsc[b] = *reinterpret_cast<const int *>(wscales + (chunk & 1) * (4 * NBW * 256) + b * 256 + lane * 4);
 #pragma unroll
         for (int m = 0; m < decltype(blocks)::value; ++m) {
             const unsigned char *rp = base + (m * 16 + fr) * RB;
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
                 const u32x4 q = w[s][b];
                 const i32x8 wf{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
                 f32x4 &d = acc[m][b];
-                const int sc = (int)ws[s][b];
+                const int sc = wsc[b];
                 if (s == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 0, sc, 0, xsc);
                 if (s == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 1, sc, 0, xsc);
                 if (s == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 2, sc, 0, xsc);
@@ -278,15 +283,15 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
             for (int i = 0; i < 8; ++i) big = mx_abs_max(big, mx_abs(h[i]));
             const int e = mx_exponent<FX>(__uint_as_float(row_max(big)));
             if (r >= rows || c0 >= a.N) continue;
-            const size_t o = (size_t)(row0 + r) * a.N + c0 + 4 * fg;
+            uint8_t *const hr = a.out + (size_t)(row0 + r) * mx_code_stride(FX, a.N);
             if constexpr (FX == kMxE4m3) {
                 const uint2 q = mx_codes8_e4m3(h, mx_factor(e));
-                *reinterpret_cast<unsigned *>(a.out + o) = q.x;
-                *reinterpret_cast<unsigned *>(a.out + o + 16) = q.y;
+                *reinterpret_cast<unsigned *>(hr + c0 + 4 * fg) = q.x;
+                *reinterpret_cast<unsigned *>(hr + c0 + 4 * fg + 16) = q.y;
             } else {
                 const unsigned q = mx_codes8_e2m1(h, mx_factor(e));
-                *reinterpret_cast<uint16_t *>(a.out + o / 2) = (uint16_t)q;
-                *reinterpret_cast<uint16_t *>(a.out + o / 2 + 8) = (uint16_t)(q >> 16);
+                *reinterpret_cast<uint16_t *>(hr + c0 / 2 + 2 * fg) = (uint16_t)q;
+                *reinterpret_cast<uint16_t *>(hr + c0 / 2 + 2 * fg + 8) = (uint16_t)(q >> 16);
             }
             if (fg == 0) {
                 const unsigned hs = (unsigned)mx_scale_stride(a.N);
@@ -324,8 +329,8 @@ namespace {
 template <int MT, int NBW, int FX, int MODE>
 int go(TileArgs a, int tiles, hipStream_t stream) {
     const int chunks = mxfp4_chunks(a.K) < kTileScaleChunks ? mxfp4_chunks(a.K) : kTileScaleChunks;
-    const size_t bytes = tile_lds_bytes(MT, FX, chunks);
-    constexpr size_t most = tile_lds_bytes(MT, FX, kTileScaleChunks);
+    const size_t bytes = tile_lds_bytes(MT, NBW, FX, chunks);
+    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, kTileScaleChunks);
     static std::atomic<unsigned long long> lds_set{0};
     const hipError_t e = allow_dynamic_lds(
         reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE>), most, lds_set);
@@ -355,6 +360,7 @@ int pick(const TileArgs &a, int fmt, int rows, int tiles, hipStream_t stream) {
 int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
     TileArgs a{};
     a.x = p.x;
+    a.x_stride = (unsigned)p.xs;
     a.xe = p.xe;
     a.x_rows = (unsigned)p.M;
     a.W = p.W;
@@ -374,6 +380,7 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
                        uint8_t *h, uint8_t *he, int rows, int tiles, hipStream_t stream) {
     TileArgs a{};
     a.x = xq;
+    a.x_stride = (unsigned)mx_code_stride(m.fmt, m.H);
     a.xe = xe;
     a.x_rows = (unsigned)m.T;
     a.W = m.W13;
@@ -392,6 +399,7 @@ int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const
                     float *y, int rows, int tiles, hipStream_t stream) {
     TileArgs a{};
     a.x = h;
+    a.x_stride = (unsigned)mx_code_stride(m.fmt, m.I);
     a.xe = he;
     a.x_rows = (unsigned)(m.T * m.k);
     a.W = m.W2;

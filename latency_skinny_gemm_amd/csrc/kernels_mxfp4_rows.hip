@@ -120,6 +120,7 @@ enum { kRowsDense = 0, kRowsGateUp = 1, kRowsDown = 2 };
 
 struct RowArgs {
     const uint8_t *x;        // bf16 rows, or codes
+    unsigned xs;             // bytes from row to row
     const uint8_t *xe;       // codes: scale bytes, es a row
     unsigned es;
     const uint8_t *W;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     // the rows: a view that ends with the last one
     const size_t x0 = MODE == kRowsGateUp ? (size_t)(row / a.top) : MODE == kRowsDown ? (size_t)row * a.top : 0;
     const unsigned xrows = MODE == kRowsGateUp ? 1u : MODE == kRowsDown ? (unsigned)a.top : (unsigned)a.M;
-    const Rsrc xr = make_rsrc(a.x + x0 * rowb, xrows * rowb);
+    const Rsrc xr = make_rsrc(a.x + x0 * a.xs, (xrows - 1) * a.xs + rowb);
     const Rsrc er = make_rsrc(BF16 ? nullptr : a.xe + x0 * a.es, BF16 ? 0u : xrows * a.es);
     constexpr bool LDS_ROW = MODE == kRowsGateUp;
     constexpr int XV = BF16 ? 4 : FX == kMxE4m3 ? 2 : 1;  // 16-byte pieces of a lane and step
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                 for (int v = 0; v < XV; ++v) {
                     const unsigned in = so * stepb + (BF16 ? bf16_piece<FX>(fg, v)
                                                            : (unsigned)(v * 64 + fg * 16));
-                    x[i][m][v] = load16<kCacheDefault>(xr, has && in < rowb ? (unsigned)r * rowb + in : kOOB);
+                    x[i][m][v] = load16<kCacheDefault>(xr, has && in < rowb ? (unsigned)r * a.xs + in : kOOB);
                 }
                 if constexpr (!BF16) {
                     const unsigned blk = so * 4u + fg;
@@ -337,11 +338,11 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
         const float hf = h * mx_factor(e);
         if (FX == kMxE4m3) {
             if (t < 32)
-                a.out[(size_t)row * a.N + j0 * 16 + c] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(hf, hf, 0, false);
+                a.out[(size_t)row * mx_code_stride(FX, a.N) + j0 * 16 + c] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(hf, hf, 0, false);
         } else {
             const float next = __shfl_xor(hf, 1, 64);
             if (t < 32 && (c & 1) == 0)
-                a.out[((size_t)row * a.N + j0 * 16 + c) / 2] =
+                a.out[(size_t)row * mx_code_stride(FX, a.N) + (j0 * 16 + c) / 2] =
                     (uint8_t)__builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, hf, next, 1.0f, 0);
         }
         if (t == 0) a.out_e[(size_t)row * mx_scale_stride(a.N) + j0 / 2] = (uint8_t)e;
@@ -397,6 +398,7 @@ int dense(const RowArgs &a, bool bf16, hipStream_t stream) {
 int launch_mxfp4_rows(const Mxfp4Args &p, hipStream_t stream) {
     RowArgs a{};
     a.x = p.x;
+    a.xs = (unsigned)(p.xe ? p.xs : p.K * 2);
     a.xe = p.xe;
     a.es = (unsigned)p.es;
     a.W = p.W;
@@ -415,6 +417,7 @@ template <int FX>
 int moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream) {
     RowArgs a{};
     a.x = (const uint8_t *)m.x;
+    a.xs = (unsigned)m.H * 2;
     a.W = m.W13;
     a.out = h;
     a.out_e = he;
@@ -427,6 +430,7 @@ int moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream) {
     int e = go<kRowsGateUp, 1, 4, FX, true, 8, 3>(a, (size_t)m.T * m.k * (m.I / 32), stream);
     if (e != (int)hipSuccess) return e;
     a.x = h;
+    a.xs = (unsigned)mx_code_stride(m.fmt, m.I);
     a.xe = he;
     a.es = (unsigned)mx_scale_stride(m.I);
     a.W = m.W2;

@@ -25,11 +25,16 @@ constexpr size_t mxfp4_packed_bytes(int E, int N, int K) {
 // Scale rows of quantised activations in a workspace: whole 16-byte pieces,
 // one a chunk.
 constexpr int mx_scale_stride(int K) { return mxfp4_chunks(K) * 16; }
+// Their code rows: whole steps, and whole 128-byte lines, so that a line is
+// asked for once.
+constexpr int mx_code_stride(int fmt, int K) {
+    return fmt == SKG_MX_E4M3 ? mxfp4_steps(K) * 128 : (mxfp4_steps(K) + 1) / 2 * 128;
+}
 
 // ---------------------------------------------------------------- launchers
 // Each returns a hipError_t as int.  fmt: kMxE4m3 or kMxE2m1.
-// e_stride 0: scale bytes [M][K/32]; else padded rows of e_stride bytes.
-int launch_quant_mx(const void *x, void *q, void *e8, int fmt, int M, int K, int e_stride,
+// padded: rows of mx_code_stride and mx_scale_stride bytes, else dense ones.
+int launch_quant_mx(const void *x, void *q, void *e8, int fmt, int M, int K, bool padded,
                     hipStream_t stream);
 int launch_dequant_mx(const void *q, const void *e8, int fmt, void *out, int M, int K,
                       hipStream_t stream);
@@ -45,6 +50,7 @@ int launch_route(const void *logits, int dtype, const float *bias, const skinny_
 // A product with packed weights.
 struct Mxfp4Args {
     const uint8_t *x;   // bf16 rows (xe null) or codes
+    int xs;             // codes: bytes from row to row
     const uint8_t *xe;  // scale bytes, es a row
     int es;
     int fmt;
