@@ -8,60 +8,116 @@
 
 namespace skg {
 
-// Workgroup e gathers the pairs of expert e, in the order of their index,
-// after those of the experts before it, and lists its row tiles.  Each
-// workgroup counts every expert's pairs itself (LDS counters), so no
-// workgroup waits for another.  Pairs whose id is outside [0, E) are left out.
-__global__ void __launch_bounds__(256)
-    moe_sort_kernel(const int *__restrict__ ids, int P, int E, int tile_rows,
-                    int *__restrict__ pairs, MoeTile *__restrict__ tiles, int *__restrict__ count) {
-    extern __shared__ int hist[];  // [E]
-    __shared__ int mine[4], before[4], tbefore[4], ttotal[4];
-    const int e = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int i = t; i < E; i += 256) hist[i] = 0;
-    __syncthreads();
-    // wave w takes the w-th quarter of the pairs, in whole groups of 64
-    const int q = ((P + 255) / 256) * 64, p0 = wave * q, p1 = min(P, p0 + q);
-    int eq = 0;
-    for (int p = p0 + lane; p < p1; p += 64) {
-        const int id = ids[p];
-        if ((unsigned)id < (unsigned)E) atomicAdd(&hist[id], 1);
-        eq += id == e;
+namespace {
+constexpr int kPrepThreads = 1024;
+constexpr int kPrepWaves = kPrepThreads / 64;
+constexpr int kIdsInFlight = 8;  // loads of ids a lane has out at once
+
+struct PrepArgs {
+    const uint16_t *x;
+    uint8_t *xq, *xe;
+    unsigned n8, k8, q_stride, e_stride;
+    const int *ids;
+    int P, E, tile_rows;
+    int *pairs;
+    MoeTile *tiles;
+    int *count;
+};
+
+// Sum over the workgroup of three values per thread, in every thread.
+__device__ __forceinline__ int3 block_sum(int3 v, int (*lds)[3]) {
+    for (int d = 32; d > 0; d >>= 1) {
+        v.x += __shfl_xor(v.x, d, 64);
+        v.y += __shfl_xor(v.y, d, 64);
+        v.z += __shfl_xor(v.z, d, 64);
     }
-    for (int d = 32; d > 0; d >>= 1) eq += __shfl_xor(eq, d, 64);
+    if ((threadIdx.x & 63) == 0) {
+        int *o = lds[threadIdx.x >> 6];
+        o[0] = v.x;
+        o[1] = v.y;
+        o[2] = v.z;
+    }
+    __syncthreads();
+    v = int3{0, 0, 0};
+    for (int w = 0; w < kPrepWaves; ++w) {
+        v.x += lds[w][0];
+        v.y += lds[w][1];
+        v.z += lds[w][2];
+    }
+    return v;
+}
+
+// Workgroup e < E gathers the pairs of expert e, in the order of their index,
+// after those of the experts before it, and lists its row tiles.  Each
+// workgroup counts every expert's pairs itself (LDS counters; integer sums, so
+// their order does not matter) and none waits for another: the ids are read E
+// times from L2, 16 waves with eight loads each in flight.  Pairs whose id is
+// outside [0, E) are left out.
+__device__ __forceinline__ void sort_pairs(const PrepArgs &a, int *hist) {
+    __shared__ int mine[kPrepWaves], sums[kPrepWaves][3];
+    const int e = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int i = t; i < a.E; i += kPrepThreads) hist[i] = 0;
+    __syncthreads();
+    // wave w takes the w-th run of the pairs, in whole groups of 64
+    const int run = ((a.P + kPrepThreads - 1) / kPrepThreads) * 64;
+    const int p0 = min(a.P, wave * run), p1 = min(a.P, p0 + run);
+    int eq = 0;
+    for (int p = p0; p < p1; p += 64 * kIdsInFlight) {
+        int id[kIdsInFlight];
+#pragma unroll
+        for (int i = 0; i < kIdsInFlight; ++i) {
+            const int q = p + i * 64 + lane;
+            id[i] = q < p1 ? a.ids[q] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kIdsInFlight; ++i) {
+            if ((unsigned)id[i] < (unsigned)a.E) atomicAdd(&hist[id[i]], 1);
+            eq += __popcll(__ballot(id[i] == e));
+        }
+    }
     if (lane == 0) mine[wave] = eq;
     __syncthreads();
-    int b = 0, tb = 0, tt = 0;  // rows and tiles of the experts before e, tiles of all
-    for (int i = t; i < E; i += 256) {
-        const int c = hist[i], ct = (c + tile_rows - 1) / tile_rows;
-        b += i < e ? c : 0;
-        tb += i < e ? ct : 0;
-        tt += ct;
+    int3 v{0, 0, 0};  // rows and tiles of the experts before e, tiles of all
+    for (int i = t; i < a.E; i += kPrepThreads) {
+        const int c = hist[i], ct = (c + a.tile_rows - 1) / a.tile_rows;
+        v.x += i < e ? c : 0;
+        v.y += i < e ? ct : 0;
+        v.z += ct;
     }
-    for (int d = 32; d > 0; d >>= 1) {
-        b += __shfl_xor(b, d, 64);
-        tb += __shfl_xor(tb, d, 64);
-        tt += __shfl_xor(tt, d, 64);
-    }
-    if (lane == 0) {
-        before[wave] = b;
-        tbefore[wave] = tb;
-        ttotal[wave] = tt;
-    }
-    __syncthreads();
-    const int row0 = before[0] + before[1] + before[2] + before[3];
-    const int tile0 = tbefore[0] + tbefore[1] + tbefore[2] + tbefore[3];
-    if (e == 0 && t == 0) count[0] = ttotal[0] + ttotal[1] + ttotal[2] + ttotal[3];
-    const int n = mine[0] + mine[1] + mine[2] + mine[3];
-    for (int i = t; i * tile_rows < n; i += 256)
-        tiles[tile0 + i] = MoeTile{e, row0, n, tile0};
-    int at = row0;
+    v = block_sum(v, sums);
+    if (e == 0 && t == 0) a.count[0] = v.z;
+    const int n = hist[e];
+    for (int i = t; i * a.tile_rows < n; i += kPrepThreads) a.tiles[v.y + i] = MoeTile{e, v.x, n, v.y};
+    int at = v.x;
     for (int w = 0; w < wave; ++w) at += mine[w];
-    for (int p = p0; p < p1; p += 64) {
-        const bool here = p + lane < p1 && ids[p + lane] == e;
-        const unsigned long long m = __ballot(here);
-        if (here) pairs[at + __popcll(m & ((1ull << lane) - 1ull))] = p + lane;
-        at += __popcll(m);
+    for (int p = p0; p < p1; p += 64 * kIdsInFlight) {
+        int id[kIdsInFlight];
+#pragma unroll
+        for (int i = 0; i < kIdsInFlight; ++i) {
+            const int q = p + i * 64 + lane;
+            id[i] = q < p1 ? a.ids[q] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kIdsInFlight; ++i) {
+            const bool here = id[i] == e;
+            const unsigned long long m = __ballot(here);
+            if (here) a.pairs[at + __popcll(m & ((1ull << lane) - 1ull))] = p + i * 64 + lane;
+            at += __popcll(m);
+        }
+    }
+}
+}  // namespace
+
+// What the products need first, in one launch: workgroups [0, E) sort, the
+// rest quantise x.
+template <int FMT>
+__global__ void __launch_bounds__(kPrepThreads) moe_prepare_kernel(PrepArgs a) {
+    extern __shared__ int hist[];  // [E]
+    if ((int)blockIdx.x < a.E) {
+        sort_pairs(a, hist);
+    } else {
+        const unsigned i = (blockIdx.x - a.E) * kPrepThreads + threadIdx.x;
+        if (i < a.n8) quant_padded8<FMT>(a.x, a.xq, a.xe, i, a.k8, a.q_stride, a.e_stride);
     }
 }
 
@@ -139,12 +195,17 @@ int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),
                          (const int *)(b + s.pairs)};
-    int e = launch_quant_mx(a.x, b + s.xq, b + s.xe, a.fmt, a.T, a.H, true, stream);
-    if (e != (int)hipSuccess) return e;
-    hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)a.E), dim3(256), (size_t)a.E * 4, stream,
-                       a.ids, P, a.E, rows, (int *)(b + s.pairs), (MoeTile *)(b + s.tiles),
-                       (int *)(b + s.count));
-    e = (int)hipGetLastError();
+    const unsigned n8 = (unsigned)((size_t)a.T * a.H / 8);
+    const PrepArgs prep{a.x, b + s.xq, b + s.xe, n8, (unsigned)a.H / 8,
+                        (unsigned)mx_code_stride(a.fmt, a.H), (unsigned)mx_scale_stride(a.H),
+                        a.ids, P, a.E, rows, (int *)(b + s.pairs), (MoeTile *)(b + s.tiles),
+                        (int *)(b + s.count)};
+    const dim3 grid((unsigned)a.E + (n8 + kPrepThreads - 1) / kPrepThreads);
+    if (a.fmt == kMxE4m3)
+        hipLaunchKernelGGL(moe_prepare_kernel<kMxE4m3>, grid, dim3(kPrepThreads), (size_t)a.E * 4, stream, prep);
+    else
+        hipLaunchKernelGGL(moe_prepare_kernel<kMxE2m1>, grid, dim3(kPrepThreads), (size_t)a.E * 4, stream, prep);
+    int e = (int)hipGetLastError();
     if (e != (int)hipSuccess) return e;
     e = launch_moe_gate_up(a, lists, b + s.xq, b + s.xe, b + s.h, b + s.he, rows, tiles, stream);
     if (e != (int)hipSuccess) return e;

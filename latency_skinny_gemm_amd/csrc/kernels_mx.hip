@@ -22,19 +22,13 @@ __global__ void __launch_bounds__(256)
                     unsigned e_stride) {
     const unsigned i = blockIdx.x * 256u + threadIdx.x;
     if (i >= n8) return;  // n8 is a multiple of 4: whole quads leave
-    float v[8];
-    bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(x + (size_t)i * 8), v);
-    if constexpr (!PAD) {
+    if constexpr (PAD) {
+        quant_padded8<FMT>(x, q, e8, i, k8, q_stride, e_stride);
+    } else {
+        float v[8];
+        bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(x + (size_t)i * 8), v);
         const int e = mx_store8<FMT>(v, q, (size_t)i * 8);
         if ((i & 3u) == 0) e8[i / 4] = (uint8_t)e;
-    } else {
-        const unsigned row = i / k8, c = i - row * k8;
-        const int e = mx_store8<FMT>(v, q + (size_t)row * q_stride, (size_t)c * 8);
-        if ((i & 3u) != 0) return;
-        uint8_t *er = e8 + (size_t)row * e_stride;
-        er[c / 4] = (uint8_t)e;
-        if (c / 4 == k8 / 4 - 1)
-            for (unsigned z = k8 / 4; z < e_stride; ++z) er[z] = 0;
     }
 }
 

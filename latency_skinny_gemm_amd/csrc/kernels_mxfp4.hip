@@ -32,7 +32,6 @@ struct TileArgs {
     int row_tiles;          // dense
 };
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // Larger of two over lanes l, l ^ 16, l ^ 32, l ^ 48 (the four lanes that
 // hold one output row).
@@ -51,11 +50,6 @@ __device__ __forceinline__ int xcd_order(int b, int n) {
     return (b >> 3) < per && at < n ? at : -1;
 }
 
-template <int N>
-struct Blocks {
-    static constexpr int value = N;
-};
-
 }  // namespace
 
 // The key that piece c of row r is stored under: the rows that share a
@@ -67,23 +61,35 @@ __device__ __forceinline__ int piece_key(int r) {
 
 // Chunks of K (512 each) whose scale bytes a tile keeps in LDS at a time.
 constexpr int kTileScaleChunks = 16;
-constexpr int kTileSlots = 4;  // steps of x in LDS
 constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
-// chunks: those of K, up to kTileScaleChunks.  Scale loads fill whole KB.
-constexpr int tile_wscale_bytes(int NBW) { return 2 * 4 * NBW * 256; }  // two chunks, four waves
-constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int chunks) {
-    return (size_t)kTileSlots * tile_slot_bytes(MT, FX) + 1024 + tile_wscale_bytes(NBW) + ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
+// Chunks of weight scales in LDS: those of the steps in flight and one more,
+// as a power of two.
+constexpr int tile_wchunks(int SL) { return SL == 4 ? 2 : 4; }
+constexpr int tile_wscale_bytes(int NBW, int SL) { return tile_wchunks(SL) * 4 * NBW * 256; }
+// Chunks of row scales in LDS when n remain: whole rounds of the ring.
+__host__ __device__ constexpr int tile_scale_chunks(int n, int SL) {
+    return n >= kTileScaleChunks ? kTileScaleChunks : (n + SL / 4 - 1) / (SL / 4) * (SL / 4);
+}
+// chunks: as tile_scale_chunks.  Scale loads fill whole KB.
+constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
+    return (size_t)SL * tile_slot_bytes(MT, FX) + 1024 + tile_wscale_bytes(NBW, SL) +
+           ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
 }
 
 // A workgroup of four waves computes MT * 16 rows x (4 waves * NBW * 16)
-// columns over the whole K, in steps of 128: the rows' codes go to a ring of
-// four LDS slots by direct loads, each wave's weights to registers (they are
-// used by that wave alone, and packed so that a load is 1 KB in a row), both
-// three steps ahead of the products.  One wait and one barrier a step: the
-// wait leaves the loads of the two younger steps in flight.  The rows' scale
-// bytes are loaded once for 8192 K.  A 16-byte piece c of row r sits at
-// c ^ piece_key(r), so that the 16 rows of a fragment read hit all banks once.
-template <int MT, int NBW, int FX, int MODE>
+// columns over the whole K, in steps of 128: the rows' codes go to a ring of SL
+// LDS slots by direct loads, each wave's weights to registers (they are used by
+// that wave alone, and packed so that a load is 1 KB in a row), both about SL
+// steps ahead of the products.  One wait and one barrier a step; the wait
+// leaves all younger steps' loads in flight.  The rows' scale bytes are loaded
+// once for 8192 K.  A 16-byte piece c of row r sits at c ^ piece_key(r), so that
+// the 16 rows of a fragment read hit all banks once.
+//
+// AHEAD reads a step's fragments from LDS under the products of the step
+// before and spreads the loads between the products.  That pays where a SIMD
+// holds one wave (dense: 24.9 -> 21 us at 512 x 4096 x 7168) and loses, for the
+// registers it takes, where it holds two or more (experts).
+template <int MT, int NBW, int FX, int MODE, int SL, bool AHEAD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     mxfp4_tile_kernel(TileArgs a) {
     constexpr int RB = FX == kMxE4m3 ? 128 : 64;   // bytes of a row and step
@@ -93,11 +99,12 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     constexpr int XI = SLOT / 1024;                // loads of a step
     constexpr int XPW = (XI + 3) / 4;              // of a wave; the spare ones fill a KB of their own
     constexpr int LOADS = XPW + NBW;               // a step's loads of a wave, at least
+    constexpr int WC = tile_wchunks(SL);
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
-    unsigned char *const pad = lds_raw + kTileSlots * SLOT;
-    unsigned char *const scales = pad + 1024 + tile_wscale_bytes(NBW);
+    unsigned char *const pad = lds_raw + SL * SLOT;
+    unsigned char *const scales = pad + 1024 + tile_wscale_bytes(NBW, SL);
 
-    const int t = threadIdx.x, lane = t & 63;
+    const int t = threadIdx.x, lane = t & 63, fr = lane & 15, fg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     // The work list goes expert by expert (dense: one), in it column tile by
     // column tile, the row tiles of a column tile side by side: those share
@@ -108,17 +115,18 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     MoeTile own{0, 0, a.M, 0};
     if constexpr (MODE != kDense) own = a.tiles[at / a.col_tiles];
     const int nt = (own.rows + ROWS - 1) / ROWS, local = at - own.first * a.col_tiles;
-    const int ct = local / nt, rt = local - ct * nt;  // column tile, row tile
-    const int row0 = own.row + rt * ROWS, rows = min(ROWS, own.rows - rt * ROWS), expert = own.expert;
-    const int live = (rows + 15) / 16;  // row blocks that hold rows
+    const int ct = local / nt, rt = local - ct * nt;
+    const int row0 = own.row + rt * ROWS, rows = min(ROWS, own.rows - rt * ROWS);
     const int KS = mxfp4_steps(a.K), KC = mxfp4_chunks(a.K);
+    const int KP = (KS + SL - 1) / SL * SL;              // steps gone through, whole rounds of the ring
     const size_t gb = mxfp4_group_bytes(a.K);
     const unsigned rowb = FX == kMxE4m3 ? (unsigned)a.K : (unsigned)a.K / 2, xs = a.x_stride;
     const unsigned es = (unsigned)mx_scale_stride(a.K);
 
-    // this wave's column groups
+    // this wave's column groups; past the last, a view of nothing: its loads
+    // return 0
     const int ng = mxfp4_groups(MODE == kGateUp ? 2 * a.N : a.N);
-    const uint8_t *We = a.W + (size_t)expert * ng * gb;
+    const uint8_t *const We = a.W + (size_t)own.expert * ng * gb;
     Rsrc wr[NBW];
 #pragma unroll
     for (int b = 0; b < NBW; ++b) {
@@ -135,6 +143,22 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         wr[b] = make_rsrc(We + (in ? j * gb : 0), in ? (unsigned)gb : 0u);
     }
 
+    u32x4 w[SL][NBW];
+    // A chunk's dwords of scale bytes go to LDS with its first step: loaded
+    // with every step they would be asked of the L1 again while on their way.
+    unsigned char *const wscales = pad + 1024 + wave * (NBW * 256);  // chunks 4 waves apart
+    auto issue_w = [&](int slot, int st, int chunk, int b) {
+        if (slot % 4 == 0)
+            lds_load4(wr[b], wscales + (chunk & (WC - 1)) * (4 * NBW * 256) + b * 256,
+                      st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB);
+        w[slot][b] = load16<kCacheDefault>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
+    };
+    // the weights' first round goes out before the rows are known
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+#pragma unroll
+        for (int b = 0; b < NBW; ++b) issue_w(s, s, s / 4, b);
+
     // this lane's pieces of the rows
     const Rsrc xr = make_rsrc(a.x, (a.x_rows - 1) * xs + rowb);
     const Rsrc er = make_rsrc(a.xe, a.x_rows * es);
@@ -150,12 +174,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         xcol[i] = (unsigned)c * 16u;
         xoff[i] = q < XI && r < rows ? row_of(r) * xs + xcol[i] : kOOB;
     }
-
-    u32x4 w[4][NBW];
-    // A chunk's dwords of scale bytes go to LDS with its first step: loaded
-    // with every step they would be asked of the L1 again while on their way.
-    unsigned char *const wscales = pad + 1024 + wave * (NBW * 256);  // two chunks, 4 waves apart
-    auto issue = [&](int slot, int st) {
+    auto issue_x = [&](int slot, int st) {
         const unsigned k = (unsigned)st * RB;
 #pragma unroll
         for (int i = 0; i < XPW; ++i) {
@@ -163,106 +182,124 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
             lds_load16<kCacheDefault>(xr, q < XI ? lds_raw + slot * SLOT + q * 1024 : pad,
                                       xoff[i] != kOOB && k + xcol[i] < rowb ? xoff[i] + k : kOOB);
         }
-#pragma unroll
-        for (int b = 0; b < NBW; ++b)
-            w[slot][b] = load16<kCacheDefault>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
-        if (slot == 0)
-#pragma unroll
-            for (int b = 0; b < NBW; ++b)
-                lds_load4(wr[b], wscales + ((st / 4) & 1) * (4 * NBW * 256) + b * 256,
-                          st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB);
     };
+    // the scale bytes of chunks c0 ..: piece q of row r is slot r * nc + q; the
+    // chunks that only fill the ring's last round are zeros (the next row's
+    // bytes in their place might be NaN scales)
+    int sstride = 0;
+    auto load_scales = [&](int c0) {
+        const int nc = tile_scale_chunks(KC - c0, SL);
+        sstride = nc * 16;
+        for (int b = wave * 64; b < ROWS * nc; b += 256) {
+            const int r = (b + lane) / nc, q = (b + lane) - r * nc;
+            lds_load16<kCacheDefault>(er, scales + b * 16,
+                                      r < rows && c0 + q < KC ? row_of(r) * es + (unsigned)(c0 + q) * 16u : kOOB);
+        }
+    };
+    load_scales(0);
+#pragma unroll
+    for (int s = 0; s < (AHEAD ? SL : SL - 1); ++s) issue_x(s, s);
+    int out_row[MT];  // down: the pair of each row that this lane stores
+    if constexpr (MODE == kDown) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) out_row[m] = m * 16 + fr < rows ? a.pairs[row0 + m * 16 + fr] : 0;
+    }
 
     f32x4 acc[MT][NBW];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int b = 0; b < NBW; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int fr = lane & 15, fg = lane >> 4;
-    int sstride = 0;  // bytes between the scale rows in LDS
-    auto compute = [&](auto blocks, int s, int chunk) {
+    // A step's fragments of x and the scale bytes.  AHEAD: read one step before
+    // their products, in two sets.
+    u32x4 xf[AHEAD ? 2 : 1][MT][FX == kMxE4m3 ? 2 : 1];
+    unsigned xsc[AHEAD ? 2 : 1][MT], wsc[AHEAD ? 2 : 1][NBW];
+    // slot s; chunk: of the scale bytes in LDS; wchunk: of all chunks so far
+    auto read_frags = [&](int f, int s, int chunk, int wchunk) {
         const unsigned char *base = lds_raw + s * SLOT;
-        int wsc[NBW];
 #pragma unroll
         for (int b = 0; b < NBW; ++b)
-            wsc[b] = *reinterpret_cast<const int *>(wscales + (chunk & 1) * (4 * NBW * 256) + b * 256 + lane * 4);
+            wsc[f][b] = *reinterpret_cast<const unsigned *>(wscales + (wchunk & (WC - 1)) * (4 * NBW * 256) + b * 256 + lane * 4);
 #pragma unroll
-        for (int m = 0; m < decltype(blocks)::value; ++m) {
+        for (int m = 0; m < MT; ++m) {
             const unsigned char *rp = base + (m * 16 + fr) * RB;
-            const int xsc = (int)(*reinterpret_cast<const unsigned *>(
-                                      scales + (m * 16 + fr) * sstride + chunk * 16 + s * 4) >> (8 * fg));
-            const u32x4 p = *reinterpret_cast<const u32x4 *>(rp + ((fg ^ piece_key<CPR>(fr)) * 16));
-            i32x8 xf{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
-            if constexpr (FX == kMxE4m3) {
-                const u32x4 q = *reinterpret_cast<const u32x4 *>(rp + (((4 + fg) ^ piece_key<CPR>(fr)) * 16));
-                xf = i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w};
+            xsc[f][m] = *reinterpret_cast<const unsigned *>(scales + (m * 16 + fr) * sstride + chunk * 16 + (s % 4) * 4);
+            xf[f][m][0] = *reinterpret_cast<const u32x4 *>(rp + ((fg ^ piece_key<CPR>(fr)) * 16));
+            if constexpr (FX == kMxE4m3)
+                xf[f][m][1] = *reinterpret_cast<const u32x4 *>(rp + (((4 + fg) ^ piece_key<CPR>(fr)) * 16));
+        }
+    };
+    auto multiply = [&](int f, int s, int m, int b) {
+        const u32x4 p = xf[f][m][0], q = xf[f][m][FX == kMxE4m3 ? 1 : 0], v = w[s][b];
+        const i32x8 x8 = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
+                                       : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+        const i32x8 w8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+        const int sx = (int)(xsc[f][m] >> (8 * fg)), sw = (int)wsc[f][b];
+        f32x4 &d = acc[m][b];
+        if (s % 4 == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 0, sw, 0, sx);
+        if (s % 4 == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 1, sw, 0, sx);
+        if (s % 4 == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 2, sw, 0, sx);
+        if (s % 4 == 3) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 3, sw, 0, sx);
+    };
+    wait_vmcnt_lds<0>();  // the first steps were asked for together
+    if constexpr (AHEAD) {
+        barrier_nofence();
+        read_frags(0, 0, 0, 0);
+    }
+    for (int cb = 0;;) {
+        const int nb = cb + SL;  // the loads of a round are the next one's
+        // One round, straight: left early, it would carry loads that the
+        // compiler then waits for at its head.  Steps past K are gone through
+        // as zeros.
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+            // AHEAD: the next step's loads have landed, all but those of the
+            // SL - 2 steps after it.  Else this step's: all but the weights of
+            // SL - 1 steps and the rows of SL - 2.  The counts are the same for
+            // every wave, so every wave reaches every barrier; behind it every
+            // wave has read the slot that is loaded into here.
+            wait_vmcnt_lds<AHEAD ? (SL - 2) * LOADS : (SL - 1) * NBW + (SL - 2) * XPW>();
+            barrier_nofence();
+            if constexpr (AHEAD) {
+                issue_x(s, nb + s);
+                const int u = cb + s + 1;  // the step whose fragments are read
+                read_frags((s + 1) & 1, (s + 1) % SL, u / 4 % kTileScaleChunks, u / 4);
+            } else {
+                if (s == 0) issue_x(SL - 1, cb + SL - 1);
+                else issue_x(s - 1, nb + s - 1);
+                read_frags(0, s, (cb + s) / 4 % kTileScaleChunks, (cb + s) / 4);
             }
+            // A group's products, then the loads into the registers they leave:
+            // free to move, the loads would go first, into as many more.
 #pragma unroll
             for (int b = 0; b < NBW; ++b) {
-                const u32x4 q = w[s][b];
-                const i32x8 wf{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
-                f32x4 &d = acc[m][b];
-                const int sc = wsc[b];
-                if (s == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 0, sc, 0, xsc);
-                if (s == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 1, sc, 0, xsc);
-                if (s == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 2, sc, 0, xsc);
-                if (s == 3) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, d, kMxE2m1, FX, 3, sc, 0, xsc);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) multiply(AHEAD ? s & 1 : 0, s, m, b);
+                __builtin_amdgcn_sched_barrier(0);
+                issue_w(s, nb + s, (nb + s) / 4, b);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-    };
-
-    // L: row blocks to compute.  One straight loop for each L: with a test per
-    // block the accumulators were copied at every join.
-    auto run = [&](auto L) {
-    for (int c0 = 0; c0 < KC; c0 += kTileScaleChunks) {
-        // the scale bytes of these chunks: piece q of row r is slot r * nc + q
-        const int nc = min(kTileScaleChunks, KC - c0);
-        sstride = nc * 16;
-        if (c0 > 0) {  // every wave has read the bytes that these replace
+        // The sums are "used" here: with their next use behind a branch, the
+        // compiler moves the whole round's products behind it.
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int b = 0; b < NBW; ++b) asm volatile("" : "+v"(acc[m][b]));
+        if (nb >= KP) break;
+        cb = nb;
+        if (KC > kTileScaleChunks && nb / 4 % kTileScaleChunks == 0) {
+            // other scale bytes, once every wave has read the old ones
             wait_vmcnt_lds<0>();
             barrier_nofence();
-        }
-        for (int b = wave * 64; b < ROWS * nc; b += 256) {
-            const int r = (b + lane) / nc, q = (b + lane) - r * nc;
-            lds_load16<kCacheDefault>(er, scales + b * 16,
-                                      r < rows ? row_of(r) * es + (unsigned)(c0 + q) * 16u : kOOB);
-        }
-        if (c0 == 0) {  // these are younger: waiting for them covers the bytes
-            issue(0, 0);
-            issue(1, 1);
-            issue(2, 2);
-        } else {
+            load_scales(nb / 4);
             wait_vmcnt_lds<0>();
-        }
-        // The steps of the last chunk past K are gone through as zeros: left
-        // early, the loop would carry loads that the compiler then waits for
-        // at its head.
-        for (int c = 0; c < nc; ++c) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                // all but the two younger steps' loads have landed; the counts
-                // are the same for every wave, so every wave reaches every barrier
-                wait_vmcnt_lds<2 * LOADS>();
+            if constexpr (AHEAD) {
                 barrier_nofence();
-                issue((s + 3) & 3, (c0 + c) * 4 + s + 3);
-                __builtin_amdgcn_sched_barrier(0);
-                compute(L, s, c);
+                read_frags(0, 0, 0, nb / 4);
             }
         }
-    }
-    };
-    if constexpr (MT == 1) {
-        run(Blocks<1>{});
-    } else if constexpr (MT == 2) {
-        if (live == 1) run(Blocks<1>{});
-        else run(Blocks<2>{});
-    } else {
-        static_assert(MT == 4, "row blocks");
-        if (live == 1) run(Blocks<1>{});
-        else if (live == 2) run(Blocks<2>{});
-        else if (live == 3) run(Blocks<3>{});
-        else run(Blocks<4>{});
     }
     wait_vmcnt_lds<0>();  // no load to LDS outlives the loop
 
@@ -272,12 +309,12 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         const int r = m * 16 + fr;
         if constexpr (MODE == kGateUp) {
             static_assert(MODE != kGateUp || NBW == 4, "a wave holds one 32-block of h");
-            if (m >= live) break;  // uniform: the exchange below needs the whole wave
+            if (m * 16 >= rows) break;  // uniform: the exchange below needs the whole wave
             const int c0 = (ct * 4 + wave) * 32;
             float h[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                h[i] = silu(acc[m][i / 4][i % 4]) * acc[m][2 + i / 4][i % 4];
+                h[i] = swiglu(acc[m][i / 4][i % 4], acc[m][2 + i / 4][i % 4]);
             unsigned big = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) big = mx_abs_max(big, mx_abs(h[i]));
@@ -303,7 +340,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         } else {
             if (r >= rows) continue;
             size_t orow = (size_t)(row0 + r);
-            if constexpr (MODE == kDown) orow = (size_t)a.pairs[row0 + r];
+            if constexpr (MODE == kDown) orow = (size_t)out_row[m];
 #pragma unroll
             for (int b = 0; b < NBW; ++b) {
                 const int n0 = ((ct * 4 + wave) * NBW + b) * 16 + 4 * fg;
@@ -326,33 +363,34 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 
 namespace {
 
-template <int MT, int NBW, int FX, int MODE>
+// tiles: row tiles (grouped products: a bound on them).
+template <int MT, int NBW, int FX, int MODE, int SL, bool AHEAD>
 int go(TileArgs a, int tiles, hipStream_t stream) {
-    const int chunks = mxfp4_chunks(a.K) < kTileScaleChunks ? mxfp4_chunks(a.K) : kTileScaleChunks;
-    const size_t bytes = tile_lds_bytes(MT, NBW, FX, chunks);
-    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, kTileScaleChunks);
+    const size_t bytes = tile_lds_bytes(MT, NBW, FX, SL, tile_scale_chunks(mxfp4_chunks(a.K), SL));
+    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, SL, kTileScaleChunks);
     static std::atomic<unsigned long long> lds_set{0};
     const hipError_t e = allow_dynamic_lds(
-        reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE>), most, lds_set);
+        reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE, SL, AHEAD>), most, lds_set);
     if (e != hipSuccess) return (int)e;
     const int cols = MODE == kGateUp ? 128 : 64 * NBW;
     a.col_tiles = (a.N + cols - 1) / cols;
     a.row_tiles = tiles;
-    hipLaunchKernelGGL((mxfp4_tile_kernel<MT, NBW, FX, MODE>),
-                       dim3(((unsigned)a.col_tiles * (unsigned)tiles + 7) / 8 * 8), dim3(256), bytes, stream, a);
+    const unsigned grid = (unsigned)a.col_tiles * (unsigned)tiles;
+    hipLaunchKernelGGL((mxfp4_tile_kernel<MT, NBW, FX, MODE, SL, AHEAD>), dim3((grid + 7) / 8 * 8), dim3(256),
+                       bytes, stream, a);
     return (int)hipGetLastError();
 }
 
 template <int NBW, int MODE>
 int pick(const TileArgs &a, int fmt, int rows, int tiles, hipStream_t stream) {
     if (fmt == kMxE4m3) {
-        if (rows <= 16) return go<1, NBW, kMxE4m3, MODE>(a, tiles, stream);
-        if (rows <= 32) return go<2, NBW, kMxE4m3, MODE>(a, tiles, stream);
-        return go<4, NBW, kMxE4m3, MODE>(a, tiles, stream);
+        if (rows <= 16) return go<1, NBW, kMxE4m3, MODE, 4, false>(a, tiles, stream);
+        if (rows <= 32) return go<2, NBW, kMxE4m3, MODE, 4, false>(a, tiles, stream);
+        return go<4, NBW, kMxE4m3, MODE, 4, false>(a, tiles, stream);
     }
-    if (rows <= 16) return go<1, NBW, kMxE2m1, MODE>(a, tiles, stream);
-    if (rows <= 32) return go<2, NBW, kMxE2m1, MODE>(a, tiles, stream);
-    return go<4, NBW, kMxE2m1, MODE>(a, tiles, stream);
+    if (rows <= 16) return go<1, NBW, kMxE2m1, MODE, 4, false>(a, tiles, stream);
+    if (rows <= 32) return go<2, NBW, kMxE2m1, MODE, 4, false>(a, tiles, stream);
+    return go<4, NBW, kMxE2m1, MODE, 4, false>(a, tiles, stream);
 }
 
 }  // namespace
@@ -371,8 +409,8 @@ int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
     a.N = p.N;
     a.K = p.K;
     const int tiles = (p.M + 63) / 64;
-    return p.fmt == kMxE4m3 ? go<4, 2, kMxE4m3, kDense>(a, tiles, stream)
-                            : go<4, 2, kMxE2m1, kDense>(a, tiles, stream);
+    return p.fmt == kMxE4m3 ? go<4, 2, kMxE4m3, kDense, 8, true>(a, tiles, stream)
+                            : go<4, 2, kMxE2m1, kDense, 8, true>(a, tiles, stream);
 }
 
 // The two products of the routed experts (kernels_moe.hip sorts and combines).

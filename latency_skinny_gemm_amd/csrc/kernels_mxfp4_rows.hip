@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
         if (t >= 64) return;
         // lane c < 32: column c of the 32-block (both halves of the wave alike)
         const int c = t & 31;
-        const float g = sum(0, c), h = g / (1.0f + expf(-g)) * sum(0, 32 + c);
+        const float h = swiglu(sum(0, c), sum(0, 32 + c));
         unsigned m = mx_abs(h);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) m = mx_abs_max(m, (unsigned)__shfl_xor((int)m, d, 64));

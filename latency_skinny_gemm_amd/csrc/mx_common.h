@@ -94,6 +94,13 @@ __device__ __forceinline__ unsigned quad_max(unsigned v) {
     return mx_abs_max(v, dpp_u32<kDppQuadSwap2>(v));
 }
 
+// silu(g) * u = g * u / (1 + exp(-g)) by the hardware's exp2 and reciprocal
+// (1 ulp each): a few 2^-23 of the value for |g| up to 80, far inside the
+// half step of the codes it becomes.  exp(-g) = inf gives -0 * u = 0.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f)) * u;
+}
+
 // A lane's eight values of a 32-block that its quad holds -> their codes at
 // q + bytes of index i0, and the block's scale byte (returned in each lane).
 template <int FMT>
@@ -108,6 +115,23 @@ __device__ __forceinline__ int mx_store8(const float (&v)[8], uint8_t *q, size_t
     else
         *reinterpret_cast<unsigned *>(q + i0 / 2) = mx_codes8_e2m1(v, f);
     return e;
+}
+
+// Values [8i, 8i + 8) of bf16 rows of 8 * k8 values, quantised into rows of
+// codes and scales q_stride and e_stride bytes apart; the scale bytes past the
+// row's blocks become 0.  i runs over whole quads of lanes.
+template <int FMT>
+__device__ __forceinline__ void quant_padded8(const uint16_t *x, uint8_t *q, uint8_t *e8, unsigned i,
+                                              unsigned k8, unsigned q_stride, unsigned e_stride) {
+    float v[8];
+    bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(x + (size_t)i * 8), v);
+    const unsigned row = i / k8, c = i - row * k8;
+    const int e = mx_store8<FMT>(v, q + (size_t)row * q_stride, (size_t)c * 8);
+    if ((i & 3u) != 0) return;
+    uint8_t *er = e8 + (size_t)row * e_stride;
+    er[c / 4] = (uint8_t)e;
+    if (c / 4 == k8 / 4 - 1)
+        for (unsigned z = k8 / 4; z < e_stride; ++z) er[z] = 0;
 }
 
 }  // namespace skg
