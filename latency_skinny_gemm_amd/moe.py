@@ -12,6 +12,7 @@ what the library refuses, no fallback.
     out = moe_mxfp4(n.y, ids, weights, w13, w2)   # w13, w2 = mxfp4_pack(...)
 """
 import ctypes
+import math
 from collections import namedtuple
 
 import torch
@@ -74,14 +75,25 @@ def declare(L):
 
 
 def _tensor(name, t, dtypes, shape=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (the library takes no strides)")
+    raise ValueError(f"{name} must be contiguous (the library takes no strides)")
+
+
+def _same_device(x, *ts):
+    """x's device; the others (None entries skipped) must be on it."""
+    i = x.get_device()
+    for t in ts:
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"all tensors must be on one device, got {x.device} and {t.device}")
+    return x.device
 
 
 def _choice(name, value, table):
@@ -103,15 +115,12 @@ def _codes(name, q, e8m0, fmt):
     if q.dim() < 1:
         raise ValueError(f"{name} must have a row dimension")
     K = q.shape[-1] * (2 if fmt == MX_E2M1 else 1)
-    _tensor(name + "'s e8m0", e8m0, _E8M0, (*q.shape[:-1], K // 32))
-    return q.shape[:-1], K
+    lead = q.shape[:-1]
+    _tensor(name + "'s e8m0", e8m0, _E8M0, (*lead, K // 32))
+    return lead, K
 
 
-def _rows(shape):
-    n = 1
-    for s in shape:
-        n *= s
-    return n
+_rows = math.prod
 
 
 def quant_mx(x, format="e4m3", stream=None):
@@ -142,7 +151,7 @@ def dequant_mx(q, e8m0, stream=None):
     lead, K = _codes("q", q, e8m0, fmt)
     out = _c._empty((*lead, K), torch.bfloat16, q.device, stream)
     M = _rows(lead)
-    rc = _c._launch(_c._one_device(q, e8m0), stream, _c._load().skinny_dequant_mx, q.data_ptr(),
+    rc = _c._launch(_same_device(q, e8m0), stream, _c._load().skinny_dequant_mx, q.data_ptr(),
                     e8m0.data_ptr(), fmt, out.data_ptr(), M, K)
     if rc:
         _c._check(rc, f"skinny_dequant_mx(M={M}, K={K})")
@@ -183,7 +192,7 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out_format="bf16", scale=None, r
     e = _c._empty((*x.shape[:-1], K // 32), torch.uint8, dev, stream) if fmt == NORM_MX else None
     M = _rows(x.shape[:-1])
     p = _c._addr
-    rc = _c._launch(_c._one_device(x, weight, residual, scale, residual_out), stream,
+    rc = _c._launch(_same_device(x, weight, residual, scale, residual_out), stream,
                     _c._load().skinny_rmsnorm, x.data_ptr(), p(residual), weight.data_ptr(), eps,
                     fmt, p(scale), y.data_ptr(), p(e), p(residual_out), M, K)
     if rc:
@@ -206,7 +215,7 @@ def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, renorm
     o = RouteOptions(sc, k, groups, top_groups, 1 if renormalize else 0, factor)
     w = _c._empty((T, max(k, 0)), torch.float32, logits.device, stream)
     ids = _c._empty((T, max(k, 0)), torch.int32, logits.device, stream)
-    rc = _c._launch(_c._one_device(logits, bias), stream, _c._load().skinny_route,
+    rc = _c._launch(_same_device(logits, bias), stream, _c._load().skinny_route,
                     logits.data_ptr(), _c.DTYPE_F32 if logits.dtype == torch.float32
                     else _c.DTYPE_BF16, _c._addr(bias), ctypes.byref(o), w.data_ptr(),
                     ids.data_ptr(), T, E)
@@ -227,7 +236,7 @@ def mxfp4_pack(q, e8m0, stream=None):
     if n == 0:
         _c._check(_c.ERR_UNSUPPORTED, f"skinny_mxfp4_pack(E={E}, N={N}, K={K})")
     packed = _c._empty((n,), torch.uint8, q.device, stream)
-    rc = _c._launch(_c._one_device(q, e8m0), stream, L.skinny_mxfp4_pack, q.data_ptr(),
+    rc = _c._launch(_same_device(q, e8m0), stream, L.skinny_mxfp4_pack, q.data_ptr(),
                     e8m0.data_ptr(), packed.data_ptr(), E or 1, N, K)
     _c._check(rc, f"skinny_mxfp4_pack(E={E}, N={N}, K={K})")
     return MxfpWeights(packed, E, N, K)
@@ -259,7 +268,7 @@ def gemm_mxfp4(x, w, xe=None, x_format="e4m3", bias=None, out_dtype=torch.bfloat
         out = _c._empty((M, N), out_dtype, x.device, stream)
     else:
         _tensor("out", out, (out_dtype,), (M, N))
-    rc = _c._launch(_c._one_device(x, w.packed, xe, bias, out), stream,
+    rc = _c._launch(_same_device(x, w.packed, xe, bias, out), stream,
                     _c._load().skinny_gemm_mxfp4, x.data_ptr(), _c._addr(xe), fmt,
                     w.packed.data_ptr(), _c._addr(bias), out.data_ptr(),
                     _c.DTYPE_F32 if out_dtype == torch.float32 else _c.DTYPE_BF16, M, N, K)
@@ -291,7 +300,7 @@ def moe_mxfp4(x, ids, weights, w13, w2, x_format="e4m3", out=None, stream=None):
         out = _c._empty((T, H), torch.bfloat16, x.device, stream)
     else:
         _tensor("out", out, _BF16, (T, H))
-    rc = _c._launch(_c._one_device(x, ids, weights, w13.packed, w2.packed, out), stream,
+    rc = _c._launch(_same_device(x, ids, weights, w13.packed, w2.packed, out), stream,
                     _c._load().skinny_moe_mxfp4, x.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                     w13.packed.data_ptr(), w2.packed.data_ptr(), out.data_ptr(), fmt, T, k, H, I, E)
     if rc:
