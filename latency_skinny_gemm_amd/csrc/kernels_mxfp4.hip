@@ -59,17 +59,18 @@ __device__ __forceinline__ int piece_key(int r) {
     return (r / (16 / CPR)) & (CPR - 1);
 }
 
-// Chunks of K (512 each) whose scale bytes a tile keeps in LDS at a time.
-constexpr int kTileScaleChunks = 16;
+// Chunks of K (512 each) whose row scales a tile keeps in LDS at a time: whole
+// rounds of a ring of SL steps, up to 16.
+__host__ __device__ constexpr int tile_scale_most(int SL) { return 16 / (SL / 4) * (SL / 4); }
+// ... when n remain.
+__host__ __device__ constexpr int tile_scale_chunks(int n, int SL) {
+    return n >= tile_scale_most(SL) ? tile_scale_most(SL) : (n + SL / 4 - 1) / (SL / 4) * (SL / 4);
+}
 constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
 // Chunks of weight scales in LDS: those of the steps in flight and one more,
 // as a power of two.
-constexpr int tile_wchunks(int SL) { return SL == 4 ? 2 : 4; }
+constexpr int tile_wchunks(int SL) { return SL == 4 ? 2 : SL <= 12 ? 4 : 8; }
 constexpr int tile_wscale_bytes(int NBW, int SL) { return tile_wchunks(SL) * 4 * NBW * 256; }
-// Chunks of row scales in LDS when n remain: whole rounds of the ring.
-__host__ __device__ constexpr int tile_scale_chunks(int n, int SL) {
-    return n >= kTileScaleChunks ? kTileScaleChunks : (n + SL / 4 - 1) / (SL / 4) * (SL / 4);
-}
 // chunks: as tile_scale_chunks.  Scale loads fill whole KB.
 constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
     return (size_t)SL * tile_slot_bytes(MT, FX) + 1024 + tile_wscale_bytes(NBW, SL) +
@@ -85,11 +86,11 @@ constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
 // once for 8192 K.  A 16-byte piece c of row r sits at c ^ piece_key(r), so that
 // the 16 rows of a fragment read hit all banks once.
 //
-// AHEAD reads a step's fragments from LDS under the products of the step
-// before and spreads the loads between the products.  That pays where a SIMD
-// holds one wave (dense: 24.9 -> 21 us at 512 x 4096 x 7168) and loses, for the
-// registers it takes, where it holds two or more (experts).
-template <int MT, int NBW, int FX, int MODE, int SL, bool AHEAD>
+// AHEAD > 0 takes that many steps a barrier and reads their fragments from LDS
+// under the products of the steps before.  That pays where a SIMD holds one
+// wave (dense, 512 x 4096 x 7168: 24.9 -> 21.3 us) and loses, for the registers
+// it takes, where it holds two or more (experts: 283 -> 324 us).
+template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     mxfp4_tile_kernel(TileArgs a) {
     constexpr int RB = FX == kMxE4m3 ? 128 : 64;   // bytes of a row and step
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     constexpr int XI = SLOT / 1024;                // loads of a step
     constexpr int XPW = (XI + 3) / 4;              // of a wave; the spare ones fill a KB of their own
     constexpr int LOADS = XPW + NBW;               // a step's loads of a wave, at least
-    constexpr int WC = tile_wchunks(SL);
+    constexpr int WC = tile_wchunks(SL), SC = tile_scale_most(SL);
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     unsigned char *const pad = lds_raw + SL * SLOT;
     unsigned char *const scales = pad + 1024 + tile_wscale_bytes(NBW, SL);
@@ -210,10 +211,12 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int b = 0; b < NBW; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // A step's fragments of x and the scale bytes.  AHEAD: read one step before
-    // their products, in two sets.
-    u32x4 xf[AHEAD ? 2 : 1][MT][FX == kMxE4m3 ? 2 : 1];
-    unsigned xsc[AHEAD ? 2 : 1][MT], wsc[AHEAD ? 2 : 1][NBW];
+    // A step's fragments of x and the scale bytes.  AHEAD: read AHEAD steps
+    // before their products, in two sets.
+    constexpr int U = AHEAD ? AHEAD : 1;  // steps a barrier
+    constexpr int FS = AHEAD ? 2 * U : 1;
+    u32x4 xf[FS][MT][FX == kMxE4m3 ? 2 : 1];
+    unsigned xsc[FS][MT], wsc[FS][NBW];
     // slot s; chunk: of the scale bytes in LDS; wchunk: of all chunks so far
     auto read_frags = [&](int f, int s, int chunk, int wchunk) {
         const unsigned char *base = lds_raw + s * SLOT;
@@ -244,7 +247,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     wait_vmcnt_lds<0>();  // the first steps were asked for together
     if constexpr (AHEAD) {
         barrier_nofence();
-        read_frags(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) read_frags(u, u, 0, 0);
     }
     for (int cb = 0;;) {
         const int nb = cb + SL;  // the loads of a round are the next one's
@@ -252,33 +256,38 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         // compiler then waits for at its head.  Steps past K are gone through
         // as zeros.
 #pragma unroll
-        for (int s = 0; s < SL; ++s) {
-            // AHEAD: the next step's loads have landed, all but those of the
-            // SL - 2 steps after it.  Else this step's: all but the weights of
-            // SL - 1 steps and the rows of SL - 2.  The counts are the same for
-            // every wave, so every wave reaches every barrier; behind it every
-            // wave has read the slot that is loaded into here.
-            wait_vmcnt_lds<AHEAD ? (SL - 2) * LOADS : (SL - 1) * NBW + (SL - 2) * XPW>();
+        for (int s0 = 0; s0 < SL; s0 += U) {
+            // AHEAD: the next U steps' loads have landed, all but those of the
+            // SL - 2U steps after them.  Else this step's: all but the weights
+            // of SL - 1 steps and the rows of SL - 2.  The counts are the same
+            // for every wave, so every wave reaches every barrier; behind it
+            // every wave has read the slots that are loaded into here.
+            wait_vmcnt_lds<AHEAD ? (SL - 2 * U) * LOADS : (SL - 1) * NBW + (SL - 2) * XPW>();
             barrier_nofence();
             if constexpr (AHEAD) {
-                issue_x(s, nb + s);
-                const int u = cb + s + 1;  // the step whose fragments are read
-                read_frags((s + 1) & 1, (s + 1) % SL, u / 4 % kTileScaleChunks, u / 4);
+#pragma unroll
+                for (int s = s0; s < s0 + U; ++s) {
+                    issue_x(s, nb + s);
+                    const int n = cb + s + U;  // the step whose fragments are read
+                    read_frags((s + U) % FS, (s + U) % SL, n / 4 % SC, n / 4);
+                }
             } else {
-                if (s == 0) issue_x(SL - 1, cb + SL - 1);
-                else issue_x(s - 1, nb + s - 1);
-                read_frags(0, s, (cb + s) / 4 % kTileScaleChunks, (cb + s) / 4);
+                if (s0 == 0) issue_x(SL - 1, cb + SL - 1);
+                else issue_x(s0 - 1, nb + s0 - 1);
+                read_frags(0, s0, (cb + s0) / 4 % SC, (cb + s0) / 4);
             }
             // A group's products, then the loads into the registers they leave:
             // free to move, the loads would go first, into as many more.
 #pragma unroll
-            for (int b = 0; b < NBW; ++b) {
-                __builtin_amdgcn_sched_barrier(0);
+            for (int s = s0; s < s0 + U; ++s)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) multiply(AHEAD ? s & 1 : 0, s, m, b);
-                __builtin_amdgcn_sched_barrier(0);
-                issue_w(s, nb + s, (nb + s) / 4, b);
-            }
+                for (int b = 0; b < NBW; ++b) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) multiply(s % FS, s, m, b);
+                    __builtin_amdgcn_sched_barrier(0);
+                    issue_w(s, nb + s, (nb + s) / 4, b);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
         // The sums are "used" here: with their next use behind a branch, the
@@ -289,7 +298,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
             for (int b = 0; b < NBW; ++b) asm volatile("" : "+v"(acc[m][b]));
         if (nb >= KP) break;
         cb = nb;
-        if (KC > kTileScaleChunks && nb / 4 % kTileScaleChunks == 0) {
+        if (KC > SC && nb / 4 % SC == 0) {
             // other scale bytes, once every wave has read the old ones
             wait_vmcnt_lds<0>();
             barrier_nofence();
@@ -297,7 +306,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
             wait_vmcnt_lds<0>();
             if constexpr (AHEAD) {
                 barrier_nofence();
-                read_frags(0, 0, 0, nb / 4);
+#pragma unroll
+                for (int u = 0; u < U; ++u) read_frags(u, u, 0, nb / 4);
             }
         }
     }
@@ -364,10 +374,11 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 namespace {
 
 // tiles: row tiles (grouped products: a bound on them).
-template <int MT, int NBW, int FX, int MODE, int SL, bool AHEAD>
+template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 int go(TileArgs a, int tiles, hipStream_t stream) {
     const size_t bytes = tile_lds_bytes(MT, NBW, FX, SL, tile_scale_chunks(mxfp4_chunks(a.K), SL));
-    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, SL, kTileScaleChunks);
+    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, SL, tile_scale_most(SL));
+    static_assert(most <= 160 * 1024 - 256, "LDS of a workgroup");
     static std::atomic<unsigned long long> lds_set{0};
     const hipError_t e = allow_dynamic_lds(
         reinterpret_cast<const void *>(&mxfp4_tile_kernel<MT, NBW, FX, MODE, SL, AHEAD>), most, lds_set);
@@ -376,7 +387,8 @@ int go(TileArgs a, int tiles, hipStream_t stream) {
     a.col_tiles = (a.N + cols - 1) / cols;
     a.row_tiles = tiles;
     const unsigned grid = (unsigned)a.col_tiles * (unsigned)tiles;
-    hipLaunchKernelGGL((mxfp4_tile_kernel<MT, NBW, FX, MODE, SL, AHEAD>), dim3((grid + 7) / 8 * 8), dim3(256),
+    hipLaunchKernelGGL((mxfp4_tile_kernel<MT, NBW, FX, MODE, SL, AHEAD>), dim3((grid + 7) / 8 * 8),
+                       dim3(256),
                        bytes, stream, a);
     return (int)hipGetLastError();
 }
@@ -384,9 +396,26 @@ int go(TileArgs a, int tiles, hipStream_t stream) {
 // rows: 16, 32 or 64 a tile.  NB: column groups a wave for 64 rows, and for fewer.
 template <int MODE, int FX, int NB64, int NB>
 int pick(const TileArgs &a, int rows, int tiles, hipStream_t stream) {
-    if (rows <= 16) return go<1, NB, FX, MODE, 4, false>(a, tiles, stream);
-    if (rows <= 32) return go<2, NB, FX, MODE, 4, false>(a, tiles, stream);
-    return go<4, NB64, FX, MODE, 4, false>(a, tiles, stream);
+    if (rows <= 16) return go<1, NB, FX, MODE, 4, 0>(a, tiles, stream);
+    if (rows <= 32) return go<2, NB, FX, MODE, 4, 0>(a, tiles, stream);
+    return go<4, NB64, FX, MODE, 4, 0>(a, tiles, stream);
+}
+
+// The smallest tile whose workgroups are at most one a CU.  A CU takes in
+// 14-17 bytes a clock of these operands however many workgroups it holds and
+// however deep their rings are, so a workgroup's time follows its bytes a step:
+// at K = 7168 13.4, 15.0, 19.9 and 29 us (quantising included) for tiles of
+// 16 x 64, 32 x 64, 32 x 128 and 64 x 128 while they fit, and twice that in a
+// second round (M = 128, N = 4096: 19.0, 15.7, 19.8, 29).
+template <int FX>
+int dense(const TileArgs &a, hipStream_t stream) {
+    const long c64 = (a.N + 63) / 64, c128 = (a.N + 127) / 128;
+    const int r16 = (a.M + 15) / 16, r32 = (a.M + 31) / 32, r64 = (a.M + 63) / 64;
+    if (r16 * c64 <= kNumCusMI355X) return go<1, 1, FX, kDense, 8, 2>(a, r16, stream);
+    if (r32 * c64 <= kNumCusMI355X) return go<2, 1, FX, kDense, 8, 2>(a, r32, stream);
+    if (r32 * c128 <= kNumCusMI355X) return go<2, 2, FX, kDense, 8, 2>(a, r32, stream);
+    // two steps a barrier spill with e4m3 fragments of 64 rows
+    return go<4, 2, FX, kDense, 8, FX == kMxE4m3 ? 1 : 2>(a, r64, stream);
 }
 
 }  // namespace
@@ -404,9 +433,7 @@ int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
     a.M = p.M;
     a.N = p.N;
     a.K = p.K;
-    const int tiles = (p.M + 63) / 64;
-    return p.fmt == kMxE4m3 ? go<4, 2, kMxE4m3, kDense, 8, true>(a, tiles, stream)
-                            : go<4, 2, kMxE2m1, kDense, 8, true>(a, tiles, stream);
+    return p.fmt == kMxE4m3 ? dense<kMxE4m3>(a, stream) : dense<kMxE2m1>(a, stream);
 }
 
 // The two products of the routed experts (kernels_moe.hip sorts and combines).

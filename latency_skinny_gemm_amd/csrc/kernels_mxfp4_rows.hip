@@ -389,8 +389,7 @@ int dense(const RowArgs &a, bool bf16, hipStream_t stream) {
     const int KS = mxfp4_steps(a.K);
     if (bf16) return waves<kRowsDense, 1, 1, FX, true, 4>(a, KS, grid, stream);
     if (a.M <= 16) return waves<kRowsDense, 1, 1, FX, false, 4>(a, KS, grid, stream);
-    if (a.M <= 32) return waves<kRowsDense, 2, 1, FX, false, 4>(a, KS, grid, stream);
-    return waves<kRowsDense, 4, 1, FX, false, 2>(a, KS, grid, stream);
+    return waves<kRowsDense, 2, 1, FX, false, 4>(a, KS, grid, stream);
 }
 
 }  // namespace

@@ -62,9 +62,14 @@ struct Mxfp4Args {
 };
 // Codes with padded scale rows, any number of rows.
 int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
-// Few rows: codes, or bf16 rows quantised on the way.
+// Few rows: codes, or up to 16 bf16 rows quantised on the way (above, every
+// workgroup quantising all of them costs more than a launch that does it once:
+// 37 x 1111 x 2880 took 12.2 us against 7.3 + 2.4).
 constexpr int kMxRowsMaxBf16 = 16;
-constexpr int kMxRowsMaxCodes = 64;
+// Codes: every workgroup takes in all rows, so the tile kernel overtakes it
+// sooner with the wider ones (N = 4096, K = 7168: 12.3 against 13.4 us at 17
+// rows and 15.9 against 13.4 at 32 in e4m3, 12.7 against 13.2 at 32 in e2m1).
+constexpr int mx_rows_max(int fmt) { return fmt == SKG_MX_E4M3 ? 20 : 32; }
 int launch_mxfp4_rows(const Mxfp4Args &a, hipStream_t stream);
 
 // ---------------------------------------------------------------- experts

@@ -568,8 +568,8 @@ def test_layer_in_a_graph_and_on_another_stream(skg):
 def test_capture_needs_reserved_workspace(skg):
     q, e, _ = _weight(1, 16, 64)
     h = skg.mxfp4_pack(q.to(DEV), e.to(DEV))
-    x = torch.zeros(40, 64, dtype=torch.bfloat16, device=DEV)
-    out = torch.empty(40, 16, dtype=torch.bfloat16, device=DEV)
+    x = torch.zeros(100, 64, dtype=torch.bfloat16, device=DEV)  # rows that are quantised first
+    out = torch.empty(100, 16, dtype=torch.bfloat16, device=DEV)
     s = torch.cuda.Stream()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.stream(s):
