@@ -1,6 +1,8 @@
 // kernels_moe.hip -- the routed experts' feed-forward: the pairs (token,
 // choice) sorted by expert, the two products over the sorted rows, and the
 // weighted sum of each token's choices.
+#include <math.h>
+
 #include "device_common.h"
 #include "internal.h"
 #include "moe_internal.h"
@@ -173,14 +175,26 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
 
 }  // namespace
 
-// Whether each pair reads its expert's weights for itself.
+// Whether each pair reads its expert's weights for itself (two launches)
+// instead of sorting (four).  Sorting saves the weights of the experts that
+// several pairs share, and its tiles stream at 5.9 TB/s against 5.0, for about
+// 12 us more.  Both sides measured from 1 to 32 tokens at (E, k, H, I) =
+// (128, 4, 2880, 2880), (32, 4, 2880, 1440) and (256, 8, 2048, 512): they cross
+// at 16-24, 16-24 and 96-128 pairs, where this does.
 static bool moe_unsorted(const MoeArgs &a) {
-    return ((long)a.T * a.k <= 16 || a.T == 1) && mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds;
+    const double P = (double)a.T * a.k, E = a.E;
+    const double shared = E * (1.0 - pow(1.0 - 1.0 / E, P));        // experts that P pairs meet
+    const double expert_us = 3.0 * a.H * a.I * 17 / 32 * 1e-6;      // at 1 TB/s
+    return P * expert_us / 5.0 - shared * expert_us / 5.9 < 12.0 &&
+           mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds;
 }
 
+// Measured at the same sizes from 1 to 1024 tokens: 16 and 32 rows differ by a
+// few per cent up to 4 pairs an expert, 32 wins by 3-7 % to 16, and 64 from
+// about 32 on (128 experts: 394 against 379 us there).
 int moe_tile_rows(int T, int k, int E) {
     const long avg = (long)T * k / E;
-    return avg <= 8 ? 16 : avg <= 20 ? 32 : 64;
+    return avg <= 4 ? 16 : avg <= 24 ? 32 : 64;
 }
 
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {

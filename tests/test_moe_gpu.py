@@ -358,7 +358,9 @@ def _weight(seed, N, K, E=None):
 
 GEMM_SIZES = [(1, 1, 32), (1, 16, 128), (2, 15, 64), (3, 17, 96), (15, 33, 160), (16, 64, 512), (17, 100, 544),
               (1, 2112, 7168), (5, 576, 7168), (16, 1111, 2880), (32, 48, 1024), (33, 128, 2880), (64, 65, 320),
-              (65, 256, 2016), (128, 130, 640), (129, 96, 1024), (200, 31, 5984), (512, 272, 288), (512, 16, 32)]
+              (65, 256, 2016), (128, 130, 640), (129, 96, 1024), (200, 31, 5984), (512, 272, 288), (512, 16, 32),
+              # every tile of the products above 32 rows, and K past the 8192 whose scales a tile holds at once
+              (21, 40, 352), (40, 33, 8480), (512, 600, 96), (500, 1100, 160), (512, 2100, 544), (490, 2180, 8736)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -454,11 +456,20 @@ def test_gemm_mxfp4_refuses(skg):
 # ------------------------------------------------------------ experts
 
 class Experts:
+    """Random codes and scales, their values about N(0, 1/K) in size."""
+
     def __init__(self, skg, E, H, I, seed=0):
-        q1, e1, self.v13 = _weight(seed + 1, 2 * I, H, E)
-        q2, e2, self.v2 = _weight(seed + 2, H, I, E)
-        self.w13 = skg.mxfp4_pack(q1.to(DEV), e1.to(DEV))
-        self.w2 = skg.mxfp4_pack(q2.to(DEV), e2.to(DEV))
+        self.w13, self.v13 = self._make(skg, seed + 1, E, 2 * I, H)
+        self.w2, self.v2 = self._make(skg, seed + 2, E, H, I)
+
+    @staticmethod
+    def _make(skg, seed, E, N, K):
+        g = torch.Generator().manual_seed(seed)
+        c = torch.randint(0, 16, (E, N, K), generator=g, dtype=torch.uint8).numpy()
+        mid = 127 - round(math.log2(2.9 * math.sqrt(K)))
+        e = torch.randint(mid - 1, mid + 2, (E, N, K // 32), generator=g, dtype=torch.uint8).numpy()
+        packed = skg.mxfp4_pack(torch.from_numpy(ref.pack_bytes(c, "e2m1")).to(DEV), torch.from_numpy(e).to(DEV))
+        return packed, ref.dequantise(c.astype(np.int64), e.astype(np.int64), "e2m1")
 
 
 def _choices(seed, T, k, E):
@@ -485,7 +496,10 @@ def _check_experts(skg, m, x, ids, w, fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,k,E,H,I", [(1, 1, 1, 32, 32), (1, 4, 8, 96, 160), (2, 2, 3, 160, 96), (3, 8, 8, 544, 32),
                                        (17, 4, 16, 256, 288), (40, 1, 5, 128, 64), (200, 3, 7, 96, 96),
-                                       (1, 4, 6, 2880, 1440), (9, 2, 130, 64, 64), (70, 64, 64, 64, 32)])
+                                       (1, 4, 6, 2880, 1440), (9, 2, 130, 64, 64), (70, 64, 64, 64, 32),
+                                       # enough bytes to be sorted: tiles of 16, 32 and 64 rows
+                                       (64, 4, 64, 448, 448), (200, 4, 40, 288, 224), (300, 4, 8, 160, 224),
+                                       (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (40, 4, 2, 8480, 64)])
 def test_experts(skg, T, k, E, H, I, fmt):
     m = Experts(skg, E, H, I)
     ids, w = _choices(T, T, k, E)
@@ -493,7 +507,7 @@ def test_experts(skg, T, k, E, H, I, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T", [1, 5, 64, 300])
+@pytest.mark.parametrize("T", [1, 5, 64, 2000])
 def test_experts_skewed_and_absent(skg, T, fmt):
     """Every token on one expert; the same expert twice in a token; ids
     outside [0, E) skipped; a token, then every token, with none left."""
@@ -513,18 +527,22 @@ def test_experts_skewed_and_absent(skg, T, fmt):
     assert torch.all(out == 0)
 
 
-def test_experts_row_does_not_depend_on_its_neighbours(skg):
-    """A token alone and among others: the same bits, whatever the others hold (NaN too)."""
+@pytest.mark.parametrize("T", [3, 90, 3000])
+def test_experts_row_does_not_depend_on_its_neighbours(skg, T):
+    """Other tokens' values and choices (their number the same): the same bits,
+    whatever the others hold, NaN too."""
     E, k, H, I = 5, 2, 160, 96
     m = Experts(skg, E, H, I)
-    x = _randn(9, 90, H).bfloat16()
-    ids, w = _choices(9, 90, k, E)
-    x[7] = math.nan
-    all_ = skg.moe_mxfp4(x.to(DEV), ids.to(DEV), w.to(DEV), m.w13, m.w2).cpu()
-    for t in (0, 8, 89):
-        one = skg.moe_mxfp4(x[t:t + 1].to(DEV), ids[t:t + 1].to(DEV), w[t:t + 1].to(DEV), m.w13, m.w2).cpu()
-        assert torch.equal(one[0], all_[t])
-    assert torch.isnan(all_[7]).all() and torch.isfinite(all_[torch.arange(90) != 7]).all()
+    x = _randn(9, T, H).bfloat16()
+    ids, w = _choices(9, T, k, E)
+    keep = torch.arange(T) % 3 == 0
+    one = skg.moe_mxfp4(x.to(DEV), ids.to(DEV), w.to(DEV), m.w13, m.w2).cpu()
+    x2, (ids2, w2) = _randn(10, T, H).bfloat16(), _choices(11, T, k, E)
+    x2[keep], ids2[keep], w2[keep] = x[keep], ids[keep], w[keep]
+    x2[1] = math.nan
+    two = skg.moe_mxfp4(x2.to(DEV), ids2.to(DEV), w2.to(DEV), m.w13, m.w2).cpu()
+    assert torch.equal(one[keep], two[keep])
+    assert torch.isnan(two[1]).all() and torch.isfinite(two[torch.arange(T) != 1]).all()
 
 
 # ------------------------------------------------------------ streams, graphs, the whole layer
