@@ -499,7 +499,7 @@ def _check_experts(skg, m, x, ids, w, fmt):
                                        (1, 4, 6, 2880, 1440), (9, 2, 130, 64, 64), (70, 64, 64, 64, 32),
                                        # enough bytes to be sorted: tiles of 16, 32 and 64 rows
                                        (64, 4, 64, 448, 448), (200, 4, 40, 288, 224), (300, 4, 8, 160, 224),
-                                       (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (40, 4, 2, 8480, 64)])
+                                       (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (80, 2, 2, 8480, 64)])
 def test_experts(skg, T, k, E, H, I, fmt):
     m = Experts(skg, E, H, I)
     ids, w = _choices(T, T, k, E)
