@@ -135,17 +135,18 @@ int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format, const voi
  * [E, 2I, H] (I rows of g, then I of u); W2 packed [E, H, I].  A choice whose
  * id lies outside [0, E) contributes nothing (an expert held elsewhere); a
  * token with none left gets zeros.  H % 32 == 0, I % 32 == 0, E <= 1024,
- * k <= 64, T * k * max(H, I) * 4 < 2^40 and T * k, T * H, T * k * I < 2^31.
+ * k <= 64, T * k * max(H, I) * 4 < 2^40, and T * k, T * H and T * k * I at most
+ * 2^31 - 1 with H and I rounded up to 128 there.
  * T == 0 is a no-op. */
 int skinny_moe_mxfp4(const void *x, const int *ids, const float *weights, const void *w13,
                      const void *w2, void *out, int x_format, int T, int k, int H, int I, int E,
                      hipStream_t stream);
 
 /* Workspace of `stream` for skinny_gemm_mxfp4 calls of up to max_M x max_K
- * (M, K) and skinny_moe_mxfp4 calls of up to (max_T, k, H, I, E); either set of
+ * (M, K; any N) and skinny_moe_mxfp4 calls of up to (max_T, k, H, I, E); either set of
  * sizes may be 0.  As skinny_gemm_reserve: before graph capture, and a larger
  * call outside capture grows it by itself. */
-int skinny_moe_reserve(int max_M, int max_N, int max_K, int max_T, int k, int H, int I, int E,
+int skinny_moe_reserve(int max_M, int max_K, int max_T, int k, int H, int I, int E,
                        hipStream_t stream);
 
 #ifdef __cplusplus

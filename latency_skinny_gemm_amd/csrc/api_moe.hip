@@ -242,9 +242,9 @@ extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weig
     return status(launch_moe(a, ws, stream));
 }
 
-extern "C" int skinny_moe_reserve(int max_M, int max_N, int max_K, int max_T, int k, int H, int I,
-                                  int E, hipStream_t stream) {
-    int rc = check_linear(max_M, max_N, max_K ? max_K : 32);
+extern "C" int skinny_moe_reserve(int max_M, int max_K, int max_T, int k, int H, int I, int E,
+                                  hipStream_t stream) {
+    int rc = check_linear(max_M, 0, max_K ? max_K : 32);
     if (rc != SKG_OK) return rc;
     if (max_K < 0 || max_T < 0) return SKG_ERR_INVALID_ARG;
     size_t bytes = max_K ? linear_workspace_bytes((size_t)max_M, max_K) : 0;

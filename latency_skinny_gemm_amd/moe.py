@@ -67,7 +67,7 @@ def declare(L):
             ("skinny_mxfp4_pack", [P, P, P, I, I, I, P]),
             ("skinny_gemm_mxfp4", [P, P, I, P, P, P, I, I, I, I, P]),
             ("skinny_moe_mxfp4", [P, P, P, P, P, P, I, I, I, I, I, I, P]),
-            ("skinny_moe_reserve", [I, I, I, I, I, I, I, I, P])):
+            ("skinny_moe_reserve", [I, I, I, I, I, I, I, P])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, I
     L.skinny_mxfp4_packed_bytes.argtypes = [I, I, I]
@@ -308,12 +308,12 @@ def moe_mxfp4(x, ids, weights, w13, w2, x_format="e4m3", out=None, stream=None):
     return out
 
 
-def reserve_moe(max_M=0, max_N=0, max_K=0, max_T=0, k=1, H=32, I=32, E=1, stream=None):
+def reserve_moe(max_M=0, max_K=0, max_T=0, k=1, H=32, I=32, E=1, stream=None):
     """Reserves workspace for `stream` (else the current stream): gemm_mxfp4
-    calls of up to [max_M, max_K] by [max_N, max_K] and moe_mxfp4 calls of up
-    to max_T tokens with these sizes.  Before graph capture."""
+    calls with x up to [max_M, max_K] and moe_mxfp4 calls of up to max_T tokens
+    with these sizes.  Before graph capture."""
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(s.device):
-        _c._check(_c._load().skinny_moe_reserve(max_M, max_N, max_K, max_T, k, H, I, E,
+        _c._check(_c._load().skinny_moe_reserve(max_M, max_K, max_T, k, H, I, E,
                                                 ctypes.c_void_p(s.cuda_stream)),
                   "skinny_moe_reserve")

@@ -174,13 +174,13 @@ def test_moe_refusals(lib, change, status):
 
 def test_reserve_refusals(lib):
     r = lib.skinny_moe_reserve
-    assert r(0, 0, 0, 0, 1, 32, 32, 1, None) == OK      # nothing asked for
-    assert r(513, 16, 64, 0, 1, 32, 32, 1, None) == UNSUP
-    assert r(1, 16, 40, 0, 1, 32, 32, 1, None) == UNSUP
-    assert r(-1, 16, 64, 0, 1, 32, 32, 1, None) == ARG
-    assert r(0, 0, 0, -1, 1, 32, 32, 1, None) == ARG
-    assert r(0, 0, 0, 1, 0, 32, 32, 1, None) == ARG
-    assert r(0, 0, 0, 1, 1, 40, 32, 1, None) == UNSUP
+    assert r(0, 0, 0, 1, 32, 32, 1, None) == OK      # nothing asked for
+    assert r(513, 64, 0, 1, 32, 32, 1, None) == UNSUP
+    assert r(1, 40, 0, 1, 32, 32, 1, None) == UNSUP
+    assert r(-1, 64, 0, 1, 32, 32, 1, None) == ARG
+    assert r(0, 0, -1, 1, 32, 32, 1, None) == ARG
+    assert r(0, 0, 1, 0, 32, 32, 1, None) == ARG
+    assert r(0, 0, 1, 1, 40, 32, 1, None) == UNSUP
 
 
 def test_binding_refusals_need_no_device():

@@ -21,7 +21,9 @@ Tolerances, derived:
   tie; a flip moves a value by at most 2^-2 (e2m1) of it, so the sum by about
   sqrt(1/100) * 2^-2 * rms = 0.025 rms; twice that is allowed.
 """
+import importlib.util
 import math
+import os
 
 import numpy as np
 import pytest
@@ -259,7 +261,8 @@ def _scores(l, scores):
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (5, 60, 4), (3, 64, 64), (7, 65, 1), (130, 384, 8),
-                                   (2, 1024, 64), (9, 513, 10), (4, 129, 6)])
+                                   (2, 1024, 64), (9, 513, 10), (4, 129, 6), (16, 8, 8), (33, 1000, 8),
+                                   (17, 136, 3), (2, 1023, 7), (2051, 72, 5)])
 def test_route(skg, T, E, k, dtype, scores):
     l = 2 * _randn(T * E, T, E)
     for renorm in (True, False):
@@ -269,15 +272,28 @@ def test_route(skg, T, E, k, dtype, scores):
 
 @pytest.mark.parametrize("scores,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
 @pytest.mark.parametrize("E,groups,top,k", [(256, 8, 4, 8), (60, 4, 2, 6), (64, 64, 8, 8), (48, 16, 16, 5),
-                                            (1024, 2, 1, 20), (96, 3, 1, 32), (160, 8, 3, 6), (1000, 40, 7, 64)])
+                                            (1024, 2, 1, 20), (96, 3, 1, 32), (160, 8, 3, 6), (1000, 40, 7, 64),
+                                            (128, 16, 5, 8), (512, 64, 9, 8), (1024, 2, 1, 8), (384, 16, 16, 1)])
 def test_route_groups(skg, E, groups, top, k, scores, bias):
-    _check_route(skg, 2 * _randn(E + k, 200, E), k, scores=scores, groups=groups, top_groups=top,
-                 bias=0.1 * _randn(E, E) if bias else None)
+    for T in (200, 2100):
+        _check_route(skg, 2 * _randn(E + k + T, T, E), k, scores=scores, groups=groups, top_groups=top,
+                     bias=0.1 * _randn(E, E) if bias else None)
+
+
+def test_route_logits_off_16_bytes(skg):
+    for dtype in (torch.float32, torch.bfloat16):
+        l = (2 * _randn(4, 5 * 64 + 1)).to(dtype).to(DEV)
+        for o in (dict(), dict(groups=4, top_groups=2, scores="sigmoid"), dict(renormalize=False)):
+            off = skg.route(l[1:].reshape(5, 64), 6, **o)
+            on = skg.route(l[1:].clone().reshape(5, 64), 6, **o)
+            assert torch.equal(off[1], on[1])
+            assert torch.allclose(off[0], on[0], rtol=2.0 ** -18, atol=0)
 
 
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
-def test_route_ties_go_to_the_lowest_index(skg, scores):
-    T, E, k = 50, 200, 9
+@pytest.mark.parametrize("k", [5, 9])
+def test_route_ties_go_to_the_lowest_index(skg, scores, k):
+    T, E = 50, 200
     l = torch.randint(0, 3, (T, E), generator=torch.Generator().manual_seed(5)).float()
     _, ids = skg.route(l.to(DEV), k, scores=scores)
     want = torch.sort(l, dim=-1, descending=True, stable=True).indices[:, :k]
@@ -287,8 +303,8 @@ def test_route_ties_go_to_the_lowest_index(skg, scores):
     z[1, ::2] = -0.0
     _, ids = skg.route(z.to(DEV), 5, scores=scores)
     assert ids.cpu().tolist() == [[0, 1, 2, 3, 4]] * 2
-    _, ids = skg.route(z.to(DEV), 9, scores=scores, groups=8, top_groups=2)
-    assert ids.cpu().tolist() == [list(range(9))] * 2
+    _, ids = skg.route(z.to(DEV), k, scores=scores, groups=8, top_groups=2)
+    assert ids.cpu().tolist() == [list(range(k))] * 2
 
 
 def test_route_masked_and_non_finite_logits(skg):
@@ -581,6 +597,49 @@ def test_layer_in_a_graph_and_on_another_stream(skg):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_example_block(skg, monkeypatch):
+    """examples/moe_layer.py: the projection and the residual, then the experts
+    on the block's own normed rows and choices, against 64 bits; and its graph
+    against its steps."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    made, pack = [], skg.mxfp4_pack
+
+    def record(q, e):
+        made.append(ref.dequantise(ref.unpack_bytes(_np(q), "e2m1"), _np(e).astype(np.int64), "e2m1"))
+        return pack(q, e)
+
+    monkeypatch.setattr(skg, "mxfp4_pack", record)
+    torch.manual_seed(3)
+    T, H = 11, 320
+    block = mod.MoeBlock(H, 96, 8, 2)
+    wo, v13, v2 = made
+    a, r = _randn(1, T, H).bfloat16(), _randn(2, T, H).bfloat16()
+    out, residual = block.forward(a.to(DEV), r.to(DEV))
+    xq = ref.rounded(ref.f64(a), "e4m3")
+    o = xq @ wo.T
+    s = o + ref.f64(r)
+    # bf16 of the product, fp32 sums with products cut 2^-13 below their group's largest, bf16 of the sum
+    bound = 2.0 ** -8 * (np.abs(o) + 1.01 * np.abs(s)) + 2.0 ** -12 * (np.abs(xq) @ np.abs(wo).T)
+    assert np.all(np.abs(ref.f64(residual) - s) <= bound)
+    n = skg.rmsnorm(skg.gemm_mxfp4(a.to(DEV), block.wo), block.gain, residual=r.to(DEV))
+    assert torch.equal(n.residual, residual)
+    w, ids = skg.route(skg.gemm_bf16_f32(n.y, block.router), 2)
+    want = ref.experts(ref.f64(n.y), ids.cpu().numpy(), ref.f64(w), v13, v2, "e4m3")
+    assert np.linalg.norm(ref.f64(out) - want) <= 0.01 * np.linalg.norm(want)
+    ad, rd = a.to(DEV), r.to(DEV)
+    graph, again = block.capture(ad, rd)
+    for i in range(4):
+        ad.copy_(_randn(20 + i, T, H).bfloat16())
+        step = block.forward(ad, rd)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(step, again)), i
 
 
 def test_capture_needs_reserved_workspace(skg):
