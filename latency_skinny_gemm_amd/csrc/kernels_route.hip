@@ -1,11 +1,15 @@
 // kernels_route.hip -- routing: the k best experts of each token by a score
 // of its router logits, optionally from the best groups, and their weights.
 //
-// One wave holds a token: C keys per lane, expert c * 64 + lane.  Keys are
-// compared as unsigned numbers that order as the floats do, so the largest
-// over the wave is a chain of integer DPP maxima, and among equal keys the
-// smallest index is a second chain.  0 marks a key out of the running; every
-// real key, -inf included, lies above it.
+// Keys are compared as unsigned numbers that order as the floats do.  0 marks
+// a key out of the running; every real key, -inf included, lies above it.
+// Two kernels: sorted lists with 16 lanes to a token (k up to 8), and one
+// choice at a time with a wave to a token (the rest).  Both are bound by
+// vector instructions, not by memory: 16384 tokens of 384 bf16 logits take
+// 8.2 us where their 14 MB would take 3; up to 512 tokens they take what a
+// launch and the chain of dependent steps take, 3 to 5 us.
+#include <type_traits>
+
 #include "device_common.h"
 #include "internal.h"
 #include "moe_internal.h"
@@ -65,6 +69,310 @@ __device__ __forceinline__ float softmax_term(float l, float m) {
 
 }  // namespace
 
+// ---------------------------------------------------------------- sorted lists
+
+namespace {
+
+constexpr int kList = 8;          // best keys a lane keeps
+constexpr int kTokenLanes = 16;   // one row of DPP
+constexpr int kChunk = kList * kTokenLanes;
+
+// A key and its expert in one number, so that one maximum and one minimum
+// exchange two of them and equal keys order by their index.  Keys of bf16
+// logits fill the upper half of 32 bits; other keys and their index are the
+// mantissa of a double in [1, 2), which a maximum of doubles passes on bit for
+// bit (the vector unit does it at the rate of fp32).
+__device__ __forceinline__ void pack_key(unsigned &k, unsigned order, unsigned e) {
+    k = (order & 0xFFFF0000u) | (0xFFFFu - e);
+}
+__device__ __forceinline__ void pack_key(double &k, unsigned order, unsigned e) {
+    k = __longlong_as_double(0x3FF0000000000000ll | (long long)order << 20 | (0xFFFFFu - e));
+}
+__device__ __forceinline__ void no_key(unsigned &k) { k = 0u; }
+__device__ __forceinline__ void no_key(double &k) { k = 1.0; }
+__device__ __forceinline__ int key_expert(unsigned k) { return (int)(0xFFFFu - (k & 0xFFFFu)); }
+__device__ __forceinline__ int key_expert(double k) {
+    return (int)(0xFFFFFu - ((unsigned)__double_as_longlong(k) & 0xFFFFFu));
+}
+__device__ __forceinline__ unsigned key_order(unsigned k) {
+    return (k & 0x80000000u) ? k & 0xFFFF0000u : k | 0xFFFFu;
+}
+__device__ __forceinline__ unsigned key_order(double k) {
+    return (unsigned)((unsigned long long)__double_as_longlong(k) >> 20);
+}
+__device__ __forceinline__ float value_of(unsigned order) {
+    return __uint_as_float((order & 0x80000000u) ? order ^ 0x80000000u : ~order);
+}
+
+__device__ __forceinline__ unsigned key_max(unsigned a, unsigned b) { return max(a, b); }
+__device__ __forceinline__ unsigned key_min(unsigned a, unsigned b) { return min(a, b); }
+// by the instruction: the library call adds one to each operand to quiet NaN
+__device__ __forceinline__ double key_max(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double key_min(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+template <int CTRL>
+__device__ __forceinline__ unsigned key_dpp(unsigned k) { return dpp_u32<CTRL>(k); }
+template <int CTRL>
+__device__ __forceinline__ double key_dpp(double k) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(k);
+    const unsigned lo = dpp_u32<CTRL>((unsigned)u), hi = dpp_u32<CTRL>((unsigned)(u >> 32));
+    return __longlong_as_double((long long)((unsigned long long)hi << 32 | lo));
+}
+
+template <typename K>
+__device__ __forceinline__ void exchange(K &a, K &b) {  // the larger into a
+    const K hi = key_max(a, b);
+    b = key_min(a, b);
+    a = hi;
+}
+
+// Eight keys, largest first: odd-even merge sort, 19 exchanges.
+template <typename K>
+__device__ __forceinline__ void sort8(K (&v)[kList]) {
+    constexpr int at[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                               {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) exchange(v[at[i][0]], v[at[i][1]]);
+}
+
+// a = the eight best of the sorted lists a and b: the larger of a[i] and
+// b[7 - i] is a bitonic sequence of them, which three halvings sort.
+template <typename K>
+__device__ __forceinline__ void merge8(K (&a)[kList], const K (&b)[kList]) {
+#pragma unroll
+    for (int i = 0; i < kList; ++i) a[i] = key_max(a[i], b[kList - 1 - i]);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < kList; ++i)
+            if (!(i & d)) exchange(a[i], a[i + d]);
+}
+template <int CTRL, typename K>
+__device__ __forceinline__ void merge_lanes(K (&a)[kList]) {
+    K b[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) b[i] = key_dpp<CTRL>(a[i]);
+    merge8(a, b);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) { return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v))); }
+// Sum and largest over a token's 16 lanes, the same in each.
+__device__ __forceinline__ float token_sum(float v) {
+    v += dpp_f<kDppQuadSwap1>(v);
+    v += dpp_f<kDppQuadSwap2>(v);
+    v += dpp_f<kDppHalfMirror>(v);
+    return v + dpp_f<kDppMirror>(v);
+}
+__device__ __forceinline__ float token_max(float v) {
+    v = fmaxf(v, dpp_f<kDppQuadSwap1>(v));
+    v = fmaxf(v, dpp_f<kDppQuadSwap2>(v));
+    v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
+    return fmaxf(v, dpp_f<kDppMirror>(v));
+}
+
+// A lane's eight experts of chunk c: neighbours (VEC), or 16 apart.
+template <bool VEC>
+__device__ __forceinline__ int list_expert(int c, int sub, int i) {
+    return c * kChunk + (VEC ? sub * kList + i : i * kTokenLanes + sub);
+}
+// Their values; those past E, -inf (VEC: E is a multiple of 8).
+template <bool VEC>
+__device__ __forceinline__ void list_load(const float *l, int E, int c, int sub, float (&v)[kList]) {
+    if constexpr (VEC) {
+        const int e = min(c * kChunk + sub * kList, E - kList);
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(l + e), b = *reinterpret_cast<const f32x4 *>(l + e + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[i + 4] = b[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kList; ++i) v[i] = l[min(list_expert<false>(c, sub, i), E - 1)];
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void list_load(const uint16_t *l, int E, int c, int sub, float (&v)[kList]) {
+    if constexpr (VEC) {
+        bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(l + min(c * kChunk + sub * kList, E - kList)), v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kList; ++i) v[i] = bf16_to_f32(l[min(list_expert<false>(c, sub, i), E - 1)]);
+    }
+}
+
+struct Softmax {
+    float m, sum;
+};
+
+// The order of a score: l itself, sigmoid(l), or either probability + bias.
+template <bool SIGMOID, bool BIAS>
+__device__ __forceinline__ unsigned score_order(float l, float bias, const Softmax &sm) {
+    float s = l;
+    if constexpr (SIGMOID) s = sigmoid(l);
+    if constexpr (BIAS) {
+        if constexpr (!SIGMOID) s = sm.sum > 0.0f ? softmax_term(l, sm.m) / sm.sum : 0.0f;
+        s = l == l ? s + bias : -__builtin_inff();
+    }
+    return order_of(s);
+}
+
+}  // namespace
+
+// Sixteen lanes to a token, four tokens to a wave.  A lane sorts eight keys at
+// a time and keeps the best eight it has seen; four merges with the lists of
+// its neighbours then leave the token's eight best, in order, in every lane.
+// One instruction serves four tokens at every step, and no step waits for the
+// one before it across the wave.
+// GROUPS (E / groups a multiple of 8, so that a lane's eight experts share a
+// group): a first pass leaves the two best keys of every eight in LDS, from
+// which the groups are ranked; the second takes the kept ones.
+template <typename TL, typename K, bool SIGMOID, bool BIAS, bool VEC, bool GROUPS>
+__global__ void __launch_bounds__(256) route_lists_kernel(RouteArgs a) {
+    extern __shared__ unsigned route_lds[];  // GROUPS: per token E / 8 pairs of keys, 64 scores
+    const int sub = threadIdx.x % kTokenLanes, local = threadIdx.x / kTokenLanes;
+    const int token = blockIdx.x * (256 / kTokenLanes) + local;
+    const int t = min(token, a.T - 1);  // lanes past the last token repeat it and store nothing
+    const TL *l = (const TL *)a.logits + (size_t)t * a.E;
+    const int chunks = (a.E + kChunk - 1) / kChunk;
+    float v[kList];
+
+    Softmax sm{0.0f, 1.0f};
+    // softmax's own division is needed before a bias, or for the weights
+    if (!SIGMOID && (BIAS || !a.renormalize)) {
+        sm.m = -__builtin_inff();
+        for (int c = 0; c < chunks; ++c) {
+            list_load<VEC>(l, a.E, c, sub, v);  // values seen twice do no harm here
+#pragma unroll
+            for (int i = 0; i < kList; ++i) sm.m = fmaxf(sm.m, v[i]);
+        }
+        sm.m = token_max(sm.m);
+        sm.sum = 0.0f;
+        for (int c = 0; c < chunks; ++c) {
+            list_load<VEC>(l, a.E, c, sub, v);
+#pragma unroll
+            for (int i = 0; i < kList; ++i)
+                sm.sum += list_expert<VEC>(c, sub, i) < a.E ? softmax_term(v[i], sm.m) : 0.0f;
+        }
+        sm.sum = token_sum(sm.sum);
+    }
+
+    unsigned long long kept = ~0ull;
+    unsigned magic = 0;
+    if constexpr (GROUPS) {
+        const int size = a.E / a.groups, blocks = a.E / kList, per = size / kList;
+        magic = (1u << 20) / (unsigned)size + 1u;  // e / size for e < 1024
+        unsigned *mine = route_lds + local * (2 * blocks + SKG_ROUTE_MAX_GROUPS), *score = mine + 2 * blocks;
+        for (int c = 0; c < chunks; ++c) {
+            const int e = c * kChunk + sub * kList;
+            list_load<VEC>(l, a.E, c, sub, v);
+            unsigned b1 = 0, b2 = 0;
+#pragma unroll
+            for (int i = 0; i < kList; ++i) {
+                const float b = BIAS ? a.bias[min(e, a.E - kList) + i] : 0.0f;
+                const unsigned q = score_order<SIGMOID, BIAS>(v[i], b, sm);
+                b2 = max(b2, min(b1, q));
+                b1 = max(b1, q);
+            }
+            if (e < a.E) {
+                mine[2 * (e / kList)] = b1;
+                mine[2 * (e / kList) + 1] = b2;
+            }
+        }
+        // a token's lanes are one wave's, whose LDS operations complete in
+        // order; only the compiler must not move the reads up
+        asm volatile("" ::: "memory");
+        for (int g = sub; g < a.groups; g += kTokenLanes) {
+            unsigned b1 = 0, b2 = 0;
+            for (int i = 0; i < per; ++i) {
+                const unsigned o1 = mine[2 * (g * per + i)], o2 = mine[2 * (g * per + i) + 1];
+                b2 = max(max(b2, o2), min(b1, o1));
+                b1 = max(b1, o1);
+            }
+            score[g] = SIGMOID ? order_of(value_of(b1) + value_of(b2)) : b1;
+        }
+        asm volatile("" ::: "memory");
+        kept = 0;
+        for (int g0 = 0; g0 < a.groups; g0 += kTokenLanes) {
+            const int g = g0 + sub;
+            const unsigned s = g < a.groups ? score[g] : 0u;
+            int rank = 0;  // groups that go before this lane's
+            for (int o = 0; o < a.groups; ++o) {
+                const unsigned so = score[o];
+                rank += (so > s || (so == s && o < g)) ? 1 : 0;
+            }
+            const unsigned long long b = __ballot(g < a.groups && rank < a.top_groups);
+            kept |= ((b >> (threadIdx.x & 48)) & 0xFFFFull) << g0;
+        }
+    }
+
+    K best[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) no_key(best[i]);
+    float next[kList];
+    list_load<VEC>(l, a.E, 0, sub, next);
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+        for (int i = 0; i < kList; ++i) v[i] = next[i];
+        if (c + 1 < chunks) list_load<VEC>(l, a.E, c + 1, sub, next);
+        bool in = true;
+        if constexpr (GROUPS)
+            in = (kept >> (((unsigned)min(c * kChunk + sub * kList, a.E - kList) * magic) >> 20)) & 1ull;
+        K key[kList];
+#pragma unroll
+        for (int i = 0; i < kList; ++i) {
+            const int e = list_expert<VEC>(c, sub, i);
+            const float b = BIAS ? a.bias[min(e, a.E - 1)] : 0.0f;
+            pack_key(key[i], score_order<SIGMOID, BIAS>(v[i], b, sm), (unsigned)e);
+            if (e >= a.E || !in) no_key(key[i]);
+        }
+        sort8(key);
+        if (c == 0) {
+#pragma unroll
+            for (int i = 0; i < kList; ++i) best[i] = key[i];
+        } else {
+            merge8(best, key);
+        }
+    }
+    merge_lanes<kDppQuadSwap1>(best);
+    merge_lanes<kDppQuadSwap2>(best);
+    merge_lanes<kDppHalfMirror>(best);
+    merge_lanes<kDppMirror>(best);
+
+    K mine = best[0];  // lane j < k: the j-th choice
+#pragma unroll
+    for (int i = 1; i < kList; ++i)
+        if (sub == i) mine = best[i];
+    const bool chosen = sub < a.k;
+    const int e = key_expert(mine);
+    float p = 0.0f;
+    if (chosen) {
+        // the score that was ordered, or the logit below a bias
+        const float s = BIAS ? load_logit(l + e) : value_of(key_order(mine));
+        if constexpr (!SIGMOID)
+            p = softmax_term(s, BIAS || !a.renormalize ? sm.m : value_of(key_order(best[0])));
+        else
+            p = BIAS ? (s == s ? sigmoid(s) : 0.0f) : (s > 0.0f ? s : 0.0f);
+    }
+    const float sum = a.renormalize ? token_sum(p) : sm.sum;
+    if (chosen && token < a.T) {
+        const size_t o = (size_t)t * a.k + sub;
+        if (a.renormalize || !SIGMOID) p = sum > 0.0f ? p / sum : 0.0f;
+        a.weights[o] = p * a.factor;
+        a.ids[o] = e;
+    }
+}
+
+// ---------------------------------------------------------------- choice by choice
+
+// One wave holds a token: C keys per lane, expert c * 64 + lane.  Each choice
+// is a chain of integer DPP maxima over the wave, and among equal keys the
+// smallest index is a second chain.
 template <typename TL, int C, bool SIGMOID>
 __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     extern __shared__ unsigned route_lds[];  // groups > 1: E keys per wave
@@ -136,9 +444,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
         }
         unsigned score = b1;
         if (SIGMOID && size > 1) {
-            const float f1 = __uint_as_float((b1 & 0x80000000u) ? b1 ^ 0x80000000u : ~b1);
-            const float f2 = __uint_as_float((b2 & 0x80000000u) ? b2 ^ 0x80000000u : ~b2);
-            score = order_of(f1 + f2);
+            score = order_of(value_of(b1) + value_of(b2));
         }
         int rank = 0;  // groups that go before this lane's
         for (int o = 0; o < a.groups; ++o) {
@@ -204,8 +510,42 @@ int go(const RouteArgs &a, bool sigmoid, hipStream_t stream) {
     return (int)hipGetLastError();
 }
 
+template <typename TL, typename K, bool SIGMOID, bool BIAS>
+int lists(const RouteArgs &a, bool vec, hipStream_t stream) {
+    constexpr int tokens = 256 / kTokenLanes;
+    const dim3 grid((unsigned)((a.T + tokens - 1) / tokens)), block(256);
+    if (a.groups > 1) {
+        const size_t lds = (size_t)tokens * (2 * (a.E / kList) + SKG_ROUTE_MAX_GROUPS) * 4;
+        hipLaunchKernelGGL((route_lists_kernel<TL, K, SIGMOID, BIAS, true, true>), grid, block, lds, stream, a);
+    } else if (vec) {
+        hipLaunchKernelGGL((route_lists_kernel<TL, K, SIGMOID, BIAS, true, false>), grid, block, 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((route_lists_kernel<TL, K, SIGMOID, BIAS, false, false>), grid, block, 0, stream, a);
+    }
+    return (int)hipGetLastError();
+}
+
 template <typename TL>
 int pick(const RouteArgs &a, bool sigmoid, hipStream_t stream) {
+    // whole 16-byte vectors of logits in every row
+    const bool vec = a.E % kList == 0 && ((uintptr_t)a.logits & 15) == 0;
+    const bool grouped = a.groups > 1;
+    // Choice by choice against lists, in us at 1, 512, 4096 and 16384 tokens:
+    // 384 bf16 logits, 8 chosen       4.6 5.1 7.1 19.2    3.6 3.9 4.1  8.2
+    // 256 fp32, sigmoid and bias      4.3 4.9 6.6 17.7    4.6 4.9 5.2 14.2
+    // the same in 8 groups            5.4 6.2 8.4 22.5    6.7 7.2 7.7 16.2
+    // 256 fp32, softmax's division    4.1 4.8 6.5 17.1    5.2 5.6 5.8 11.9
+    // so lists that read the logits twice are for many tokens only.
+    const bool twice = grouped || (!sigmoid && (a.bias || !a.renormalize));
+    if (a.k <= kList && (!grouped || (vec && a.E / a.groups % kList == 0)) && (!twice || a.T >= 2048)) {
+        if (sigmoid)
+            return a.bias ? lists<TL, double, true, true>(a, vec, stream)
+                          : lists<TL, double, true, false>(a, vec, stream);
+        if (a.bias) return lists<TL, double, false, true>(a, vec, stream);
+        // the logits themselves are the keys
+        typedef typename std::conditional<sizeof(TL) == 2, unsigned, double>::type K;
+        return lists<TL, K, false, false>(a, vec, stream);
+    }
     const int c = (a.E + 63) / 64;
     if (c <= 1) return go<TL, 1>(a, sigmoid, stream);
     if (c <= 2) return go<TL, 2>(a, sigmoid, stream);
