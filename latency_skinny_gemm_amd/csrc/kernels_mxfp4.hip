@@ -32,7 +32,6 @@ struct TileArgs {
     int row_tiles;          // dense
 };
 
-
 // Larger of two over lanes l, l ^ 16, l ^ 32, l ^ 48 (the four lanes that
 // hold one output row).
 __device__ __forceinline__ unsigned row_max(unsigned v) {
@@ -90,9 +89,11 @@ constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
 // under the products of the steps before.  That pays where a SIMD holds one
 // wave (dense, 512 x 4096 x 7168: 24.9 -> 21.3 us) and loses, for the registers
 // it takes, where it holds two or more (experts: 283 -> 324 us).
-template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
-    mxfp4_tile_kernel(TileArgs a) {
+//
+// CACHE: what the weights' loads ask of the caches.
+template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD, int CACHE>
+__device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own, const int ct,
+                                           const int rt) {
     constexpr int RB = FX == kMxE4m3 ? 128 : 64;   // bytes of a row and step
     constexpr int CPR = RB / 16;                   // pieces of a row and step
     constexpr int ROWS = MT * 16;
@@ -107,16 +108,6 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 
     const int t = threadIdx.x, lane = t & 63, fr = lane & 15, fg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    // The work list goes expert by expert (dense: one), in it column tile by
-    // column tile, the row tiles of a column tile side by side: those share
-    // their weights, and all of an expert's share its rows of x.
-    const int tiles = MODE == kDense ? a.row_tiles : a.count[0];
-    const int at = xcd_order(blockIdx.x, a.col_tiles * tiles);
-    if (at < 0) return;
-    MoeTile own{0, 0, a.M, 0};
-    if constexpr (MODE != kDense) own = a.tiles[at / a.col_tiles];
-    const int nt = (own.rows + ROWS - 1) / ROWS, local = at - own.first * a.col_tiles;
-    const int ct = local / nt, rt = local - ct * nt;
     const int row0 = own.row + rt * ROWS, rows = min(ROWS, own.rows - rt * ROWS);
     const int KS = mxfp4_steps(a.K), KC = mxfp4_chunks(a.K);
     const int KP = (KS + SL - 1) / SL * SL;              // steps gone through, whole rounds of the ring
@@ -152,7 +143,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
         if (slot % 4 == 0)
             lds_load4(wr[b], wscales + (chunk & (WC - 1)) * (4 * NBW * 256) + b * 256,
                       st < KS ? (unsigned)KS * 1024u + (unsigned)(st / 4) * 256u + lane * 4u : kOOB);
-        w[slot][b] = load16<kCacheDefault>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
+        w[slot][b] = load16<CACHE>(wr[b], st < KS ? (unsigned)st * 1024u + lane * 16u : kOOB);
     };
     // the weights' first round goes out before the rows are known
 #pragma unroll
@@ -369,6 +360,30 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
             }
         }
     }
+}
+
+// Weights that one row tile alone reads pass the caches by: 12 % of the time of
+// 40 tokens (64 experts of 4096 x 1408, 8 a token: 113 -> 99 us) and 10 % of 512
+// tokens' (128 of 2880 x 2880, 4 a token: 328 -> 293).  For those that tiles
+// share the same loads cost 12 %: chosen tile by tile.
+template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+    mxfp4_tile_kernel(TileArgs a) {
+    constexpr int ROWS = MT * 16;
+    // The work list goes expert by expert (dense: one), in it column tile by
+    // column tile, the row tiles of a column tile side by side: those share
+    // their weights, and all of an expert's share its rows of x.
+    const int tiles = MODE == kDense ? a.row_tiles : a.count[0];
+    const int at = xcd_order(blockIdx.x, a.col_tiles * tiles);
+    if (at < 0) return;
+    MoeTile own{0, 0, a.M, 0};
+    if constexpr (MODE != kDense) own = a.tiles[at / a.col_tiles];
+    const int nt = (own.rows + ROWS - 1) / ROWS, local = at - own.first * a.col_tiles;
+    const int ct = local / nt, rt = local - ct * nt;
+    if (nt == 1)
+        mxfp4_tile<MT, NBW, FX, MODE, SL, AHEAD, kCacheStream>(a, own, ct, rt);
+    else
+        mxfp4_tile<MT, NBW, FX, MODE, SL, AHEAD, kCacheDefault>(a, own, ct, rt);
 }
 
 namespace {

@@ -219,11 +219,15 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
             }
             // s < 0: nothing (loads past the views' ends return 0)
             const unsigned so = s < 0 ? kOOB : (unsigned)s;
+            // A dense product reads its weights once (2112 x 7168 from memory:
+            // 7.3 -> 6.9 us); pairs may share an expert's (16 pairs, 64 experts:
+            // 33 us, 35 past the caches).
+            constexpr int CACHE = MODE == kRowsDense ? kCacheStream : kCacheDefault;
 #pragma unroll
             for (int b = 0; b < R; ++b) {
                 const uint8_t *g = Wu + (size_t)group_of(b) * gb;
                 const Rsrc wr = make_rsrc(g, (unsigned)gb);
-                w[i][b] = load16<kCacheDefault>(wr, s < 0 ? kOOB : so * 1024u + lane * 16u);
+                w[i][b] = load16<CACHE>(wr, s < 0 ? kOOB : so * 1024u + lane * 16u);
                 ws[i][b] = __builtin_amdgcn_raw_buffer_load_b32(
                     wr, s < 0 ? kOOB : (unsigned)KS * 1024u + so / 4u * 256u + lane * 4u, 0, kCacheDefault);
             }
