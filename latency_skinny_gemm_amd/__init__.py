@@ -159,7 +159,7 @@ def _one_device(*ts):
 def _launch(dev, stream, fn, *args):
     """fn(*args, stream) with `dev` current (the library keeps its workspaces
     per current device) on `stream`, else dev's current stream."""
-    if torch.cuda.current_device() != dev.index:
+    if torch._C._cuda_getDevice() != dev.index:
         with torch.cuda.device(dev):
             return _launch(dev, stream, fn, *args)
     if stream is None:
@@ -174,10 +174,20 @@ def _empty(shape, dtype, device, stream):
     """A new output tensor, allocated for the stream the call runs on (so the
     caching allocator does not hand its memory to other work on another
     stream while the call may still write it)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None)
+    if len(shape) == 2:  # 1.3 us of host time; torch.empty takes 1.7
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(x, dtype, stream):
+    """_empty of contiguous x's shape and device: 1.2 us of host time."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(x, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(x, dtype=dtype)
 
 
 def _ptr(t):

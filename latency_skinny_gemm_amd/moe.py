@@ -132,7 +132,7 @@ def quant_mx(x, format="e4m3", stream=None):
         raise ValueError("x must be [..., K] with K a multiple of 32")
     lead, K = x.shape[:-1], x.shape[-1]
     if fmt == MX_E4M3:
-        q = _c._empty(x.shape, torch.float8_e4m3fn, x.device, stream)
+        q = _c._empty_like(x, torch.float8_e4m3fn, stream)
     else:
         q = _c._empty((*lead, K // 2), torch.uint8, x.device, stream)
     e = _c._empty((*lead, K // 32), torch.uint8, x.device, stream)
@@ -181,14 +181,14 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out_format="bf16", scale=None, r
     if residual is not None:
         _tensor("residual", residual, _BF16, tuple(x.shape))
         if residual_out is None:
-            residual_out = _c._empty(x.shape, torch.bfloat16, dev, stream)
+            residual_out = _c._empty_like(x, torch.bfloat16, stream)
         else:
             _tensor("residual_out", residual_out, _BF16, tuple(x.shape))
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if fmt == NORM_MX and K % 32:
         raise ValueError("MX output needs K a multiple of 32")
-    y = _c._empty(x.shape, torch.bfloat16 if fmt == NORM_BF16 else torch.float8_e4m3fn, dev, stream)
+    y = _c._empty_like(x, torch.bfloat16 if fmt == NORM_BF16 else torch.float8_e4m3fn, stream)
     e = _c._empty((*x.shape[:-1], K // 32), torch.uint8, dev, stream) if fmt == NORM_MX else None
     M = _rows(x.shape[:-1])
     p = _c._addr
