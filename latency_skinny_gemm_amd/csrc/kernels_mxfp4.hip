@@ -51,11 +51,12 @@ __device__ __forceinline__ int xcd_order(int b, int n) {
 
 }  // namespace
 
-// The key that piece c of row r is stored under: the rows that share a
-// 256-byte window of the banks get different ones.
+// The key that piece c of row r is stored under.  Measured on fragment reads of
+// 64- and 128-byte rows: r / 2 leaves no bank conflict in either, r / 4 or none
+// costs 4 clocks a read in the shorter, none 12 in the longer.
 template <int CPR>
 __device__ __forceinline__ int piece_key(int r) {
-    return (r / (16 / CPR)) & (CPR - 1);
+    return (r / 2) & (CPR - 1);
 }
 
 // Chunks of K (512 each) whose row scales a tile keeps in LDS at a time: whole
@@ -65,6 +66,9 @@ __host__ __device__ constexpr int tile_scale_most(int SL) { return 16 / (SL / 4)
 __host__ __device__ constexpr int tile_scale_chunks(int n, int SL) {
     return n >= tile_scale_most(SL) ? tile_scale_most(SL) : (n + SL / 4 - 1) / (SL / 4) * (SL / 4);
 }
+// Pieces of 16 bytes from row to row there: an odd number, or the 16 rows of a
+// read meet in the banks (4 clocks a read at 14 pieces, 28 at 16).
+__host__ __device__ constexpr int tile_scale_pieces(int chunks) { return chunks | 1; }
 constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
 // Chunks of weight scales in LDS: those of the steps in flight and one more,
 // as a power of two.
@@ -73,7 +77,7 @@ constexpr int tile_wscale_bytes(int NBW, int SL) { return tile_wchunks(SL) * 4 *
 // chunks: as tile_scale_chunks.  Scale loads fill whole KB.
 constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
     return (size_t)SL * tile_slot_bytes(MT, FX) + 1024 + tile_wscale_bytes(NBW, SL) +
-           ((size_t)MT * 256 * chunks + 1023) / 1024 * 1024;
+           ((size_t)MT * 256 * tile_scale_pieces(chunks) + 1023) / 1024 * 1024;
 }
 
 // A workgroup of four waves computes MT * 16 rows x (4 waves * NBW * 16)
@@ -180,7 +184,7 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
     // bytes in their place might be NaN scales)
     int sstride = 0;
     auto load_scales = [&](int c0) {
-        const int nc = tile_scale_chunks(KC - c0, SL);
+        const int nc = tile_scale_pieces(tile_scale_chunks(KC - c0, SL));
         sstride = nc * 16;
         for (int b = wave * 64; b < ROWS * nc; b += 256) {
             const int r = (b + lane) / nc, q = (b + lane) - r * nc;
