@@ -6,6 +6,10 @@
 // squares costs one reduction.  The 8-bit outputs are made from the same
 // fp32 values: static e4m3, or MX codes whose 32-value blocks are the four
 // neighbouring lanes of a quad.
+//
+// Many rows are bound by HBM: 8192 x 7168 with a residual to MX moves 411 MB in
+// 77 us, 5.3 TB/s (a copy on this card: 4.7).  One row takes 3.4 us: a launch,
+// a load, the reduction's barrier and a store, one after another.
 #include "device_common.h"
 #include "internal.h"
 #include "moe_internal.h"
@@ -57,7 +61,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int row, size_t ro
 
 }  // namespace
 
-// TPR lanes per row (64: one wave, four rows a workgroup; else the whole
+// TPR lanes per row (64: one wave, four rows a workgroup; else a whole
 // workgroup), V vectors of 8 values per lane held in registers; V == 0: rows
 // longer than the registers hold, read a second time for the output.
 template <int OUT, int TPR, int V>
@@ -115,12 +119,22 @@ int go(const NormArgs &a, hipStream_t stream) {
     return (int)hipGetLastError();
 }
 
+// One vector of 8 values a lane up to 8192 values (in us, with residual, to MX,
+// at 1, 1024 and 8192 rows; beside it half the lanes with two each):
+//   2880 values   2.9  6.6 34.1    3.7  7.1 32.5
+//   4096          2.9  8.3 41.1    3.9  8.4 41.0
+//   7168          3.4 12.3 79.7    3.9 12.2 76.8
+// so the shorter chain wins for few rows everywhere, and for many rows two
+// vectors only where a row needs more than 512 lanes.
 template <int OUT>
 int pick(const NormArgs &a, hipStream_t stream) {
     const int k8 = a.K / 8;
-    if (k8 <= 128) return go<OUT, 64, 2>(a, stream);
-    if (k8 <= 1024) return k8 <= 512 ? go<OUT, 256, 2>(a, stream) : go<OUT, 256, 4>(a, stream);
+    if (k8 <= 64) return go<OUT, 64, 1>(a, stream);
+    if (k8 <= 256) return go<OUT, 256, 1>(a, stream);
+    if (k8 <= 512) return go<OUT, 512, 1>(a, stream);
+    if (k8 <= 1024) return a.M <= 1024 ? go<OUT, 1024, 1>(a, stream) : go<OUT, 512, 2>(a, stream);
     if (k8 <= 2048) return go<OUT, 1024, 2>(a, stream);
+    // longer rows are read twice: 16384 values, 4096 rows: 103 us against 88
     return go<OUT, 1024, 0>(a, stream);
 }
 

@@ -111,7 +111,7 @@ def test_dequant_every_scale(skg):
 # ------------------------------------------------------------ norm
 
 NORM_SIZES = [(1, 32), (3, 96), (5, 1024), (2, 1056), (1, 7168), (67, 2880), (3, 8224), (2, 16384),
-              (2, 16416), (1, 65536)]
+              (2, 16416), (1, 65536), (1026, 4160)]
 
 
 def _norm_close(skg, out, y, fmt, scale):
