@@ -196,7 +196,8 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
     Mxfp4Args a{(const uint8_t *)x, (int)code_bytes(x_format, K), (const uint8_t *)x_e8m0, K / 32, x_format,
                 (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
-    const bool few = M <= mx_rows_max(x_format);
+    const bool few = M <= (x_e8m0 ? kMxRowsMaxCodes : mx_rows_max(x_format)) &&
+                     M * mxfp4_row_lds_bytes(x_format, K) <= kMxRowMaxLds;
     if (few && (x_e8m0 || M <= kMxRowsMaxBf16)) return status(launch_mxfp4_rows(a, stream));
     float *ws = nullptr;
     unsigned *tk = nullptr;

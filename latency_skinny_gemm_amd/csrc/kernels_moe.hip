@@ -186,7 +186,8 @@ static bool moe_unsorted(const MoeArgs &a) {
     const double shared = E * (1.0 - pow(1.0 - 1.0 / E, P));        // experts that P pairs meet
     const double expert_us = 3.0 * a.H * a.I * 17 / 32 * 1e-6;      // at 1 TB/s
     return P * expert_us / 5.0 - shared * expert_us / 5.9 < 12.0 &&
-           mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds;
+           mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds &&
+           a.k * mxfp4_row_lds_bytes(a.fmt, a.I) <= kMxRowMaxLds;
 }
 
 // Measured at the same sizes from 1 to 1024 tokens: 16 and 32 rows differ by a

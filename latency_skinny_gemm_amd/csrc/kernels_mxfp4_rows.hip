@@ -6,9 +6,16 @@
 // take the 128-wide steps w, w + NW, ..., each wave has the loads of U steps in
 // flight at once, and the only exchange is one sum over the waves through LDS
 // at the end, in wave order: no second launch, no partials in memory, the same
-// bits every time.  bf16 rows are quantised in the registers that feed the
-// matrix instruction (mx_quant_*: about 60 instructions a step, hidden under
-// the weights' latency), which saves the launch that would do it.
+// bits every time.  The rows are brought to LDS by the workgroup, bf16 ones
+// quantised on the way, while the weights are in flight: that saves the launch
+// that would do it.
+//
+// Measured, weights from memory: one row of 7168 by 2112 columns 4.1 us (8.0 MB
+// of weights, 2 TB/s; a launch and one load after another make most of it),
+// 16 rows 9.3 (the rows' quantising), 16 rows of e2m1 codes 5.4.  Experts of
+// 2880 x 2880, one token's four: 8.7 us gate and up (35 MB, 4.1 TB/s) and 5.9
+// down (18 MB, 3.0).  Fragments loaded straight to registers, without LDS:
+// 6.9, 9.9, 6.7, 10.1 and 5.6 us.
 #include "device_common.h"
 #include "internal.h"
 #include "lds_limit.h"
@@ -66,57 +73,15 @@ __device__ __forceinline__ unsigned codes8_e2m1(u32x4 v, float s) {
     return r;
 }
 
-// One step of one row block as the matrix instruction takes it: the codes a
-// lane holds and the scale byte of its 32-block.
-struct Frag {
-    i32x8 q;
-    int e;
-};
-
-// What a lane loads of bf16 rows for one step: 32 values.
-//   e2m1: K 32g .. 32g + 31, block g itself;
-//   e4m3: K 16g .. 16g + 15 and 64 + 16g .., halves of blocks g / 2 and
-//         2 + g / 2 (v[0..1] and v[2..3]).
-template <int FX>
-__device__ __forceinline__ Frag quantise_frag(const u32x4 (&v)[4], int fg) {
-    Frag f;
-    if constexpr (FX == kMxE2m1) {
-        const unsigned a = fold16(pk_max(pk_max(amax8(v[0]), amax8(v[1])), pk_max(amax8(v[2]), amax8(v[3]))));
-        f.e = mx_exponent16<FX>(a);
-        const float s = scale_of(f.e);
-        f.q = i32x8{(int)codes8_e2m1(v[0], s), (int)codes8_e2m1(v[1], s), (int)codes8_e2m1(v[2], s),
-                    (int)codes8_e2m1(v[3], s), 0, 0, 0, 0};
-    } else {
-        // both halves' candidates in one register, then the other half of
-        // each block from lane l ^ 16
-        const unsigned lo = fold16(pk_max(amax8(v[0]), amax8(v[1])));
-        const unsigned hi = fold16(pk_max(amax8(v[2]), amax8(v[3])));
-        unsigned a = lo | hi << 16;
-        const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-        a = pk_max(x[0], x[1]);
-        const int e0 = mx_exponent16<FX>(a & 0xFFFFu), e1 = mx_exponent16<FX>(a >> 16);
-        const float s0 = scale_of(e0), s1 = scale_of(e1);
-        const uint2 c0 = codes8_e4m3(v[0], s0), c1 = codes8_e4m3(v[1], s0);
-        const uint2 c2 = codes8_e4m3(v[2], s1), c3 = codes8_e4m3(v[3], s1);
-        f.q = i32x8{(int)c0.x, (int)c0.y, (int)c1.x, (int)c1.y, (int)c2.x, (int)c2.y, (int)c3.x, (int)c3.y};
-        // lane group g supplies block g's byte: 0 and 3 have it, 1 and 2 take
-        // it from lane l ^ 32 (groups 3 and 0)
-        const unsigned both = (unsigned)e0 | (unsigned)e1 << 16;
-        const auto y = __builtin_amdgcn_permlane32_swap(both, both, false, false);
-        const unsigned other = fg < 2 ? y[1] : y[0];
-        f.e = fg == 0 ? e0 : fg == 3 ? e1 : fg == 1 ? (int)(other & 0xFFFFu) : (int)(other >> 16);
-    }
-    return f;
-}
-
-// Byte offset of the i-th 16-byte piece of a lane's 32 bf16 values in a step.
-template <int FX>
-__device__ __forceinline__ unsigned bf16_piece(int fg, int i) {
-    return FX == kMxE2m1 ? (unsigned)(fg * 64 + i * 16)
-                         : (unsigned)((i >> 1) * 128 + fg * 32 + (i & 1) * 16);
-}
-
 enum { kRowsDense = 0, kRowsGateUp = 1, kRowsDown = 2 };
+
+// A value that is the same in the whole wave and that nothing here writes.  By
+// the scalar unit: a vector load in front of the weights' would be waited for
+// with everything older, loads return in order.
+template <typename T>
+__device__ __forceinline__ T scalar_load(const T *p) {
+    return *(const __attribute__((address_space(4))) T *)(uintptr_t)p;
+}
 
 struct RowArgs {
     const uint8_t *x;        // bf16 rows, or codes
@@ -131,7 +96,18 @@ struct RowArgs {
     const int *ids;          // experts
     const float *weights;
     int top, E;
+    // set by go(): waves' loads per row of codes (or bf16) and of scale bytes,
+    // and what divides by them and by the steps of K
+    int row_loads, scale_loads;
+    unsigned by_row_loads, by_scale_loads, by_steps;
 };
+
+// n / d by a multiplication, for n * d < 2^31: a division takes some 20 vector
+// instructions, and what a wave does before its first load is latency.
+constexpr unsigned divider(unsigned d) { return (0x80000000u + d - 1) / d; }
+__device__ __forceinline__ int divide(int n, unsigned by) {
+    return (int)(((unsigned long long)(unsigned)n * by) >> 31);
+}
 
 }  // namespace
 
@@ -139,12 +115,13 @@ struct RowArgs {
 // Gate-up (R = 4, one row): workgroup (pair, 32 columns of h).
 // Down (one row a unit): workgroup (token, R groups); the units are the steps
 // of all the token's choices.
-template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U>
+// XB: 16-byte pieces of the rows that a thread has in flight.
+template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U, int XB>
 __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     constexpr bool ONE = MODE != kRowsDense;  // one row: only lanes of row 0 hold data
     constexpr int ROWS = ONE ? 1 : MT * 16;
     __shared__ float part[NW][ROWS][R * 16];
-    extern __shared__ __attribute__((aligned(16))) uint8_t row_lds[];  // gate-up: the row's codes and scales
+    extern __shared__ __attribute__((aligned(16))) uint8_t row_lds[];  // the rows' codes, then their scales
     const int t = threadIdx.x, lane = t & 63, fr = lane & 15, fg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int KS = mxfp4_steps(a.K);
@@ -188,34 +165,92 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     const unsigned xrows = MODE == kRowsGateUp ? 1u : MODE == kRowsDown ? (unsigned)a.top : (unsigned)a.M;
     const Rsrc xr = make_rsrc(a.x + x0 * a.xs, (xrows - 1) * a.xs + rowb);
     const Rsrc er = make_rsrc(BF16 ? nullptr : a.xe + x0 * a.es, BF16 ? 0u : xrows * a.es);
-    constexpr bool LDS_ROW = MODE == kRowsGateUp;
-    constexpr int XV = BF16 ? 4 : FX == kMxE4m3 ? 2 : 1;  // 16-byte pieces of a lane and step
-    constexpr int XM = LDS_ROW ? 0 : MT;                  // blocks whose rows come straight to registers
-    constexpr unsigned CB = FX == kMxE4m3 ? 128u : 64u;   // bytes of a row's codes in a step
+    constexpr unsigned CB = FX == kMxE4m3 ? 128u : 64u;  // bytes of a row's codes in a step
+
+    // The rows go to LDS once, as codes in whole steps (zeros past K) and their
+    // scale bytes: straight to registers they would be fragments of 16 rows,
+    // and a lane that is out of range costs what one with data does.  A wave's
+    // load is 64 pieces of one row: 8 bf16 values (a block is a quad of lanes)
+    // or 16 bytes of codes each; or 64 scale bytes.
+    const int xp = KS * (BF16 ? 16 : (int)CB / 16);  // pieces of a row
+    const int rs = KS * (int)CB + kRowLdsPad;
+    const int xn = (int)xrows * a.row_loads, sn = BF16 ? 0 : (int)xrows * a.scale_loads;
+    uint8_t *const row_sc = row_lds + (size_t)xrows * rs;
+    u32x4 xv[XB];
+    uint8_t sv[XB];
+    auto load_rows = [&](int v0) {
+#pragma unroll
+        for (int v = 0; v < XB; ++v) {
+            const int q = wave + (v0 + v) * NW;
+            if (q < xn) {
+                const int r = divide(q, a.by_row_loads), c = (q - r * a.row_loads) * 64 + lane;
+                xv[v] = load16<kCacheDefault>(xr, (unsigned)c * 16u < rowb ? (unsigned)r * a.xs + (unsigned)c * 16u : kOOB);
+            }
+            if (q < sn) {
+                const int r = divide(q, a.by_scale_loads), c = (q - r * a.scale_loads) * 64 + lane;
+                sv[v] = __builtin_amdgcn_raw_buffer_load_b8(
+                    er, (unsigned)c < kb ? (unsigned)r * a.es + (unsigned)c : kOOB, 0, kCacheDefault);
+            }
+        }
+    };
+    auto store_rows = [&](int v0) {
+#pragma unroll
+        for (int v = 0; v < XB; ++v) {
+            const int q = wave + (v0 + v) * NW;
+            if (q < xn) {
+                const int r = divide(q, a.by_row_loads), c = (q - r * a.row_loads) * 64 + lane;
+                if constexpr (BF16) {
+                    const int e = mx_exponent16<FX>(quad_max(fold16(amax8(xv[v]))));
+                    if (c < xp) {
+                        if constexpr (FX == kMxE4m3)
+                            *reinterpret_cast<uint2 *>(row_lds + r * rs + c * 8) = codes8_e4m3(xv[v], scale_of(e));
+                        else
+                            *reinterpret_cast<unsigned *>(row_lds + r * rs + c * 4) = codes8_e2m1(xv[v], scale_of(e));
+                        if ((c & 3) == 0) row_sc[r * (KS * 4) + c / 4] = (uint8_t)e;
+                    }
+                } else {
+                    if (c < xp) *reinterpret_cast<u32x4 *>(row_lds + r * rs + c * 16) = xv[v];
+                }
+            }
+            if (q < sn) {
+                const int r = divide(q, a.by_scale_loads), c = (q - r * a.scale_loads) * 64 + lane;
+                if (c < KS * 4) row_sc[r * (KS * 4) + c] = sv[v];
+            }
+        }
+    };
+    load_rows(0);  // before the weights: loads return in order
 
     const int batches = (units + NW * U - 1) / (NW * U);  // the same for every wave
     for (int it = 0; it < batches; ++it) {
         const int u0 = it * NW * U + wave;
-        u32x4 w[U][R], x[U][XM > 0 ? XM : 1][XV];
-        unsigned ws[U][R], xs[U][XM > 0 ? XM : 1];
+        u32x4 w[U][R];
+        unsigned ws[U][R];
         float wt[U];
+        int expert[U];  // down: of the unit's choice; -1: none that is held here
+        if constexpr (MODE == kRowsDown) {
+            int id[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const size_t p = (size_t)row * a.top + divide(min(u0 + i * NW, units - 1), a.by_steps);
+                id[i] = scalar_load(a.ids + p);
+                wt[i] = scalar_load(a.weights + p);
+            }
+            // all together: one by one each would be waited for
+            static_assert(MODE != kRowsDown || U == 6, "the operands below");
+            asm volatile("" : "+s"(id[0]), "+s"(id[1]), "+s"(id[2]), "+s"(id[3]), "+s"(id[4]), "+s"(id[5]),
+                              "+s"(wt[0]), "+s"(wt[1]), "+s"(wt[2]), "+s"(wt[3]), "+s"(wt[4]), "+s"(wt[5]));
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                expert[i] = u0 + i * NW < units && (unsigned)id[i] < (unsigned)a.E ? id[i] : -1;
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int u = u0 + i * NW;
-            const bool live = u < units;
-            int s = u, j = 0;
+            int s = u < units ? u : -1;
             const uint8_t *Wu = We;
             if constexpr (MODE == kRowsDown) {
-                j = u / KS;
-                s = u - j * KS;
-                const size_t p = (size_t)row * a.top + (live ? j : 0);
-                const int e = a.ids[p];
-                const bool in = live && (unsigned)e < (unsigned)a.E;
-                wt[i] = in ? a.weights[p] : 0.0f;
-                Wu += in ? (size_t)e * ng * gb : 0;
-                if (!in) s = -1;
-            } else {
-                if (!live) s = -1;
+                s = expert[i] >= 0 ? u - divide(u, a.by_steps) * KS : -1;
+                Wu += (size_t)max(expert[i], 0) * ng * gb;
             }
             // s < 0: nothing (loads past the views' ends return 0)
             const unsigned so = s < 0 ? kOOB : (unsigned)s;
@@ -231,71 +266,35 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                 ws[i][b] = __builtin_amdgcn_raw_buffer_load_b32(
                     wr, s < 0 ? kOOB : (unsigned)KS * 1024u + so / 4u * 256u + lane * 4u, 0, kCacheDefault);
             }
-#pragma unroll
-            for (int m = 0; m < XM; ++m) {
-                const int r = ONE ? j : m * 16 + fr;
-                const bool has = s >= 0 && (ONE ? fr == 0 : r < a.M);
-                const unsigned stepb = BF16 ? 256u : CB;
-#pragma unroll
-                for (int v = 0; v < XV; ++v) {
-                    const unsigned in = so * stepb + (BF16 ? bf16_piece<FX>(fg, v)
-                                                           : (unsigned)(v * 64 + fg * 16));
-                    x[i][m][v] = load16<kCacheDefault>(xr, has && in < rowb ? (unsigned)r * a.xs + in : kOOB);
-                }
-                if constexpr (!BF16) {
-                    const unsigned blk = so * 4u + fg;
-                    xs[i][m] = __builtin_amdgcn_raw_buffer_load_b8(
-                        er, has && blk < kb ? (unsigned)r * a.es + blk : kOOB, 0, kCacheDefault);
-                }
-            }
         }
         // every load of the batch goes out before the first product; steps past
         // the end hold zeros, which add nothing
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (LDS_ROW) {
-            // The one row, quantised once by the workgroup while the weights
-            // are on their way: 8 values a thread, a block per quad; codes to
-            // the end of the last step (zeros past K), then the scale bytes.
-            if (it == 0) {
-                uint8_t *const rs = row_lds + (size_t)KS * CB;
-                for (int i = t; i < KS * 16; i += NW * 64) {
-                    const u32x4 v = load16<kCacheDefault>(xr, (unsigned)i * 16u < rowb ? (unsigned)i * 16u : kOOB);
-                    const unsigned am = quad_max(fold16(amax8(v)));
-                    const int e = mx_exponent16<FX>(am);
-                    if constexpr (FX == kMxE4m3)
-                        *reinterpret_cast<uint2 *>(row_lds + i * 8) = codes8_e4m3(v, scale_of(e));
-                    else
-                        *reinterpret_cast<unsigned *>(row_lds + i * 4) = codes8_e2m1(v, scale_of(e));
-                    if ((i & 3) == 0) rs[i / 4] = (uint8_t)e;
-                }
-                __syncthreads();
+        if (it == 0) {  // while the weights are on their way
+            store_rows(0);
+            for (int v0 = XB; v0 * NW < max(xn, sn); v0 += XB) {
+                load_rows(v0);
+                store_rows(v0);
             }
+            wait_vmcnt_lds<63>();  // the writes to LDS alone
+            barrier_nofence();
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int u = u0 + i * NW;
-            const int s = MODE == kRowsDown ? u % KS : u;
+            const int j = MODE == kRowsDown ? divide(min(u, units - 1), a.by_steps) : 0;
+            const int s = u - j * KS, sl = min(s, KS - 1);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                Frag f;
-                if constexpr (LDS_ROW) {
-                    // every lane row holds the one row; only column 0 of the
-                    // result is used
-                    const int sl = min(s, KS - 1);
-                    const uint8_t *rp = row_lds + sl * CB + fg * 16;
-                    const u32x4 p = *reinterpret_cast<const u32x4 *>(rp);
-                    const u32x4 q = *reinterpret_cast<const u32x4 *>(rp + (FX == kMxE4m3 ? 64 : 0));
-                    f.q = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
-                                        : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
-                    f.e = row_lds[(size_t)KS * CB + sl * 4 + fg];
-                } else if constexpr (BF16) {
-                    f = quantise_frag<FX>(x[i][m], fg);
-                } else {
-                    const u32x4 p = x[i][m][0], q = x[i][m][XV - 1];
-                    f.q = XV == 2 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
-                                  : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
-                    f.e = (int)xs[i][m];
-                }
+                // lanes past the last row hold it again; their columns of the
+                // result are not used
+                const int rl = MODE == kRowsDown ? j : min(m * 16 + fr, (int)xrows - 1);
+                const uint8_t *rp = row_lds + rl * rs + sl * CB + fg * 16;
+                const u32x4 p = *reinterpret_cast<const u32x4 *>(rp);
+                const u32x4 x1 = *reinterpret_cast<const u32x4 *>(rp + (FX == kMxE4m3 ? 64 : 0));
+                const i32x8 xq = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w}
+                                               : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+                const int xe = row_sc[rl * (KS * 4) + sl * 4 + fg];
 #pragma unroll
                 for (int b = 0; b < R; ++b) {
                     const u32x4 q = w[i][b];
@@ -303,12 +302,12 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                     const int sc = (int)(ws[i][b] >> (8 * (s & 3)));
                     if constexpr (MODE == kRowsDown) {
                         const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, f.q, f32x4{0.f, 0.f, 0.f, 0.f}, kMxE2m1, FX, 0, sc, 0, f.e);
+                            wf, xq, f32x4{0.f, 0.f, 0.f, 0.f}, kMxE2m1, FX, 0, sc, 0, xe);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[m][b][c] = __builtin_fmaf(wt[i], d[c], acc[m][b][c]);
+                        for (int c = 0; c < 4; ++c) acc[m][b][c] = __builtin_fmaf(wt[i], expert[i] >= 0 ? d[c] : 0.0f, acc[m][b][c]);
                     } else {
                         acc[m][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, f.q, acc[m][b], kMxE2m1, FX, 0, sc, 0, f.e);
+                            wf, xq, acc[m][b], kMxE2m1, FX, 0, sc, 0, xe);
                     }
                 }
             }
@@ -363,37 +362,56 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
 
 namespace {
 
-template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U>
-int go(const RowArgs &a, size_t grid, hipStream_t stream) {
-    size_t lds = 0;
-    if (MODE == kRowsGateUp) {
-        lds = mxfp4_row_lds_bytes(FX, a.K);
-        static std::atomic<unsigned long long> lds_set{0};
-        const hipError_t e = allow_dynamic_lds(
-            reinterpret_cast<const void *>(&mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U>),
-            kMxRowMaxLds, lds_set);
-        if (e != hipSuccess) return (int)e;
-    }
-    hipLaunchKernelGGL((mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U>), dim3((unsigned)grid),
+template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U, int XB>
+int go(RowArgs a, size_t grid, hipStream_t stream) {
+    const int rows = MODE == kRowsGateUp ? 1 : MODE == kRowsDown ? a.top : a.M;
+    const size_t lds = rows * mxfp4_row_lds_bytes(FX, a.K);
+    const int KS = mxfp4_steps(a.K);
+    a.row_loads = (KS * (BF16 ? 16 : FX == kMxE4m3 ? 8 : 4) + 63) / 64;
+    a.scale_loads = (KS * 4 + 63) / 64;
+    a.by_row_loads = divider((unsigned)a.row_loads);
+    a.by_scale_loads = divider((unsigned)a.scale_loads);
+    a.by_steps = divider((unsigned)KS);
+    static std::atomic<unsigned long long> lds_set{0};
+    const hipError_t e = allow_dynamic_lds(
+        reinterpret_cast<const void *>(&mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U, XB>),
+        kMxRowMaxLds, lds_set);
+    if (e != hipSuccess) return (int)e;
+    hipLaunchKernelGGL((mxfp4_rows_kernel<MODE, MT, R, FX, BF16, NW, U, XB>), dim3((unsigned)grid),
                        dim3(NW * 64), lds, stream, a);
     return (int)hipGetLastError();
 }
 
 // Waves that share the steps: enough that a wave has at most U of them, up to 16.
-template <int MODE, int MT, int R, int FX, bool BF16, int U>
-int waves(const RowArgs &a, int units, size_t grid, hipStream_t stream) {
-    if (units <= 4 * U) return go<MODE, MT, R, FX, BF16, 4, U>(a, grid, stream);
-    if (units <= 8 * U) return go<MODE, MT, R, FX, BF16, 8, U>(a, grid, stream);
-    return go<MODE, MT, R, FX, BF16, 16, U>(a, grid, stream);
+inline int waves_of(int units, int U) { return units <= 4 * U ? 4 : units <= 8 * U ? 8 : 16; }
+
+template <int MODE, int MT, int R, int FX, bool BF16, int U, int XB>
+int waves(const RowArgs &a, int nw, size_t grid, hipStream_t stream) {
+    if (nw == 4) return go<MODE, MT, R, FX, BF16, 4, U, XB>(a, grid, stream);
+    if (nw == 8) return go<MODE, MT, R, FX, BF16, 8, U, XB>(a, grid, stream);
+    return go<MODE, MT, R, FX, BF16, 16, U, XB>(a, grid, stream);
+}
+
+// XB as many as a wave has loads of rows, up to 4: what is not needed costs its
+// instructions before the weights' loads (one row of 7168: 4.1 us with one,
+// 4.3 with four, 4.8 with eight), and a second round waits for the weights (four
+// rows: 5.5, 4.8).
+template <int FX, bool BF16>
+int dense16(const RowArgs &a, int KS, size_t grid, hipStream_t stream) {
+    const int nw = waves_of(KS, 4), pieces = KS * (BF16 ? 16 : FX == kMxE4m3 ? 8 : 4);
+    const int loads = a.M * ((max(pieces, BF16 ? 0 : KS * 4) + 63) / 64);
+    if (loads <= nw) return waves<kRowsDense, 1, 1, FX, BF16, 4, 1>(a, nw, grid, stream);
+    if (loads <= 2 * nw) return waves<kRowsDense, 1, 1, FX, BF16, 4, 2>(a, nw, grid, stream);
+    return waves<kRowsDense, 1, 1, FX, BF16, 4, 4>(a, nw, grid, stream);
 }
 
 template <int FX>
 int dense(const RowArgs &a, bool bf16, hipStream_t stream) {
     const size_t grid = (size_t)mxfp4_groups(a.N);
     const int KS = mxfp4_steps(a.K);
-    if (bf16) return waves<kRowsDense, 1, 1, FX, true, 4>(a, KS, grid, stream);
-    if (a.M <= 16) return waves<kRowsDense, 1, 1, FX, false, 4>(a, KS, grid, stream);
-    return waves<kRowsDense, 2, 1, FX, false, 4>(a, KS, grid, stream);
+    if (bf16) return dense16<FX, true>(a, KS, grid, stream);
+    if (a.M <= 16) return dense16<FX, false>(a, KS, grid, stream);
+    return waves<kRowsDense, 2, 1, FX, false, 4, 4>(a, waves_of(KS, 4), grid, stream);
 }
 
 }  // namespace
@@ -430,7 +448,7 @@ int moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream) {
     a.weights = m.weights;
     a.top = m.k;
     a.E = m.E;
-    int e = go<kRowsGateUp, 1, 4, FX, true, 8, 3>(a, (size_t)m.T * m.k * (m.I / 32), stream);
+    int e = go<kRowsGateUp, 1, 4, FX, true, 8, 3, 1>(a, (size_t)m.T * m.k * (m.I / 32), stream);
     if (e != (int)hipSuccess) return e;
     a.x = h;
     a.xs = (unsigned)mx_code_stride(m.fmt, m.I);
@@ -441,8 +459,8 @@ int moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream) {
     a.out_f32 = 0;
     a.N = m.H;
     a.K = m.I;
-    return waves<kRowsDown, 1, 1, FX, false, 6>(a, m.k * mxfp4_steps(m.I),
-                                                (size_t)m.T * mxfp4_groups(m.H), stream);
+    return waves<kRowsDown, 1, 1, FX, false, 6, 1>(a, waves_of(m.k * mxfp4_steps(m.I), 6),
+                                                   (size_t)m.T * mxfp4_groups(m.H), stream);
 }
 }  // namespace
 

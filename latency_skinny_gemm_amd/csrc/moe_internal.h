@@ -64,12 +64,16 @@ struct Mxfp4Args {
 int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
 // Few rows: codes, or up to 16 bf16 rows quantised on the way (above, every
 // workgroup quantising all of them costs more than a launch that does it once:
-// 37 x 1111 x 2880 took 12.2 us against 7.3 + 2.4).
+// 4096 x 7168 to e2m1 takes 8.3 us at 12 rows, 9.6 at 16, and 9.1 at 17 with the
+// launch).
 constexpr int kMxRowsMaxBf16 = 16;
-// Codes: every workgroup takes in all rows, so the tile kernel overtakes it
-// sooner with the wider ones (N = 4096, K = 7168: 12.3 against 13.4 us at 17
-// rows and 15.9 against 13.4 at 32 in e4m3, 12.7 against 13.2 at 32 in e2m1).
-constexpr int mx_rows_max(int fmt) { return fmt == SKG_MX_E4M3 ? 20 : 32; }
+// Codes: every workgroup takes in all rows, so the tile kernel overtakes it.
+// Given by the caller, not before 32 rows (2880 x 1111: 6.9 us in e4m3 and 6.3
+// in e2m1 there, tiles 7.9 and 7.8); quantised by a launch just before, sooner
+// (2880 x 1111, e4m3: 7.8 at 20, 8.9 at 24, tiles 8.3; 2048 x 8192, e2m1: 8.9 at
+// 28, 9.7 at 32, tiles 9.1).
+constexpr int kMxRowsMaxCodes = 32;
+constexpr int mx_rows_max(int fmt) { return fmt == SKG_MX_E4M3 ? 20 : 28; }
 int launch_mxfp4_rows(const Mxfp4Args &a, hipStream_t stream);
 
 // ---------------------------------------------------------------- experts
@@ -111,10 +115,12 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
 int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const uint8_t *he,
                     float *y, int rows, int tiles, hipStream_t stream);
 // LDS of a row's codes and scale bytes, in whole steps, and the most of it.
+// The pad puts the same piece of neighbouring rows into different banks.
+constexpr int kRowLdsPad = 64;
 constexpr size_t mxfp4_row_lds_bytes(int fmt, int K) {
-    return (size_t)mxfp4_steps(K) * ((fmt == SKG_MX_E4M3 ? 128 : 64) + 4);
+    return (size_t)mxfp4_steps(K) * ((fmt == SKG_MX_E4M3 ? 128 : 64) + 4) + kRowLdsPad;
 }
-constexpr size_t kMxRowMaxLds = 128 * 1024;
+constexpr size_t kMxRowMaxLds = 124 * 1024;
 // Few pairs, unsorted: h and he have a row per pair; combines as well.
 int launch_moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream);
 // Bytes of workspace the experts need.

@@ -376,7 +376,9 @@ GEMM_SIZES = [(1, 1, 32), (1, 16, 128), (2, 15, 64), (3, 17, 96), (15, 33, 160),
               (1, 2112, 7168), (5, 576, 7168), (16, 1111, 2880), (32, 48, 1024), (33, 128, 2880), (64, 65, 320),
               (65, 256, 2016), (128, 130, 640), (129, 96, 1024), (200, 31, 5984), (512, 272, 288), (512, 16, 32),
               # every tile of the products above 32 rows, and K past the 8192 whose scales a tile holds at once
-              (21, 40, 352), (40, 33, 8480), (512, 600, 96), (500, 1100, 160), (512, 2100, 544), (490, 2180, 8736)]
+              (21, 40, 352), (40, 33, 8480), (512, 600, 96), (500, 1100, 160), (512, 2100, 544), (490, 2180, 8736),
+              # few rows: several rounds of loads, and rows too long for them
+              (2, 33, 30016), (16, 40, 6368), (20, 24, 4640), (30, 50, 4320), (16, 40, 9248), (31, 20, 9248)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -393,7 +395,11 @@ def test_gemm_mxfp4(skg, M, N, K, fmt):
     f32 = skg.gemm_mxfp4(x.to(DEV), h, x_format=fmt, out_dtype=torch.float32)
     assert torch.equal(f32.bfloat16(), out)  # one rounding
     xq, xe = skg.quant_mx(x.to(DEV), fmt)
-    assert torch.equal(skg.gemm_mxfp4(xq, h, xe=xe, x_format=fmt), out)  # codes or bf16: the same bits
+    codes = skg.gemm_mxfp4(xq, h, xe=xe, x_format=fmt)
+    if 16 < M <= 32:  # may take another kernel, with another order of its sums
+        _product_close(codes, want, K)
+    else:
+        assert torch.equal(codes, out)  # codes or bf16: the same bits
     assert torch.equal(skg.gemm_mxfp4(x.to(DEV), h, x_format=fmt), out)  # the same bits again
 
 
@@ -515,7 +521,9 @@ def _check_experts(skg, m, x, ids, w, fmt):
                                        (1, 4, 6, 2880, 1440), (9, 2, 130, 64, 64), (70, 64, 64, 64, 32),
                                        # enough bytes to be sorted: tiles of 16, 32 and 64 rows
                                        (64, 4, 64, 448, 448), (200, 4, 40, 288, 224), (300, 4, 8, 160, 224),
-                                       (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (80, 2, 2, 8480, 64)])
+                                       (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (80, 2, 2, 8480, 64),
+                                       # unsorted, rows of several rounds of loads
+                                       (1, 8, 8, 96, 4128), (1, 2, 2, 8480, 64)])
 def test_experts(skg, T, k, E, H, I, fmt):
     m = Experts(skg, E, H, I)
     ids, w = _choices(T, T, k, E)
