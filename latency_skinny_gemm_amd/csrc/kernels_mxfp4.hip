@@ -72,7 +72,7 @@ __host__ __device__ constexpr int tile_scale_pieces(int chunks) { return chunks 
 constexpr int tile_slot_bytes(int MT, int FX) { return MT * (FX == kMxE4m3 ? 2048 : 1024); }
 // Chunks of weight scales in LDS: those of the steps in flight and one more,
 // as a power of two.
-constexpr int tile_wchunks(int SL) { return SL == 4 ? 2 : SL <= 12 ? 4 : 8; }
+constexpr int tile_wchunks(int SL) { return SL == 4 ? 2 : 4; }
 constexpr int tile_wscale_bytes(int NBW, int SL) { return tile_wchunks(SL) * 4 * NBW * 256; }
 // chunks: as tile_scale_chunks.  Scale loads fill whole KB.
 constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
@@ -88,6 +88,13 @@ constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
 // leaves all younger steps' loads in flight.  The rows' scale bytes are loaded
 // once for 8192 K.  A 16-byte piece c of row r sits at c ^ piece_key(r), so that
 // the 16 rows of a fragment read hit all banks once.
+//
+// What bounds it.  Experts, 40 tokens (64 of 4096 x 1408, 8 a token, half of them
+// held, e2m1): HBM; 54 us for the 332 MB of gate and up, 6.1 TB/s, 27 us for the
+// 172 MB of down.  2048 tokens (128 of 2880 x 2880, 4 a token, e4m3): 282 us and
+// 159 us; 4.0 and 3.6 TB/s of weights, the matrix pipes 37 % busy, 15 bytes a clock
+// into each CU with the rows: nothing alone, all of it together.  Dense,
+// 512 x 4096 x 7168 in e2m1: 19 us, 17 bytes a clock into each CU.
 //
 // AHEAD > 0 takes that many steps a barrier and reads their fragments from LDS
 // under the products of the steps before.  That pays where a SIMD holds one
@@ -423,7 +430,7 @@ int pick(const TileArgs &a, int rows, int tiles, hipStream_t stream) {
 // The smallest tile whose workgroups are at most one a CU.  A CU takes in
 // 14-17 bytes a clock of these operands however many workgroups it holds and
 // however deep their rings are, so a workgroup's time follows its bytes a step:
-// at K = 7168 13.4, 15.0, 19.9 and 29 us (quantising included) for tiles of
+// at K = 7168 12.3, 15.0, 19.2 and 30 us (quantising included) for tiles of
 // 16 x 64, 32 x 64, 32 x 128 and 64 x 128 while they fit, and twice that in a
 // second round (M = 128, N = 4096: 19.0, 15.7, 19.8, 29).
 template <int FX>
