@@ -20,7 +20,7 @@ struct PrepArgs {
     uint8_t *xq, *xe;
     unsigned n8, k8, q_stride, e_stride;
     const int *ids;
-    int P, E, tile_rows;
+    int P, E, tile_rows, tall;
     int *pairs;
     MoeTile *tiles;
     int *count;
@@ -85,15 +85,15 @@ __device__ __forceinline__ void sort_pairs(const PrepArgs &a, int *hist) {
     __syncthreads();
     int3 v{0, 0, 0};  // rows and tiles of the experts before e, tiles of all
     for (int i = t; i < a.E; i += kPrepThreads) {
-        const int c = hist[i], ct = (c + a.tile_rows - 1) / a.tile_rows;
+        const int c = hist[i], h = moe_tile_height(c, a.tile_rows, a.tall), ct = (c + h - 1) / h;
         v.x += i < e ? c : 0;
         v.y += i < e ? ct : 0;
         v.z += ct;
     }
     v = block_sum(v, sums);
     if (e == 0 && t == 0) a.count[0] = v.z;
-    const int n = hist[e];
-    for (int i = t; i * a.tile_rows < n; i += kPrepThreads) a.tiles[v.y + i] = MoeTile{e, v.x, n, v.y};
+    const int n = hist[e], height = moe_tile_height(n, a.tile_rows, a.tall);
+    for (int i = t; i * height < n; i += kPrepThreads) a.tiles[v.y + i] = MoeTile{e, v.x, n, v.y};
     int at = v.x;
     for (int w = 0; w < wave; ++w) at += mine[w];
     for (int p = p0; p < p1; p += 64 * kIdsInFlight) {
@@ -204,6 +204,16 @@ int moe_tile_rows(int T, int k, int E) {
     return avg <= 4 ? 16 : avg <= 24 ? 32 : 64;
 }
 
+// Whether the tiles of some experts may be taller than 64 rows: with enough of
+// them that fewer, longer workgroups still fill the card.  2048 and 4096 tokens
+// of 128 experts of 2880 x 2880, 4 a token: 460 -> 451 and 637 -> 620 us (e2m1 581
+// -> 546); 512 of 64 of 4096 x 1408, 8 a token: 162 -> 157, but 256: 130 -> 131;
+// 1024 of 32 of 2880 x 1440: 104 -> 114.
+static int moe_tall(const MoeArgs &a, int rows) {
+    const long tiles = (long)a.T * a.k / 64 + a.E / 2;
+    return rows == 64 && tiles * ((a.I + 127) / 128) >= 4 * kNumCusMI355X;
+}
+
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
     return moe_space(T, k, H, I, E, fmt).bytes;
 }
@@ -215,11 +225,11 @@ int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const int P = a.T * a.k, rows = moe_tile_rows(a.T, a.k, a.E);
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),
-                         (const int *)(b + s.pairs)};
+                         (const int *)(b + s.pairs), moe_tall(a, rows)};
     const unsigned n8 = (unsigned)((size_t)a.T * a.H / 8);
     const PrepArgs prep{a.x, b + s.xq, b + s.xe, n8, (unsigned)a.H / 8,
                         (unsigned)mx_code_stride(a.fmt, a.H), (unsigned)mx_scale_stride(a.H),
-                        a.ids, P, a.E, rows, (int *)(b + s.pairs), (MoeTile *)(b + s.tiles),
+                        a.ids, P, a.E, rows, lists.tall, (int *)(b + s.pairs), (MoeTile *)(b + s.tiles),
                         (int *)(b + s.count)};
     const dim3 grid((unsigned)a.E + (n8 + kPrepThreads - 1) / kPrepThreads);
     if (a.fmt == kMxE4m3)

@@ -28,6 +28,7 @@ struct TileArgs {
     const int *count;       // grouped: tiles in use
     const int *pairs;       // grouped: sorted row -> pair
     int top;                // grouped: pairs per token
+    int tall;               // grouped: as MoeLists
     int col_tiles;          // workgroups side by side in a row tile
     int row_tiles;          // dense
 };
@@ -217,30 +218,35 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
     // before their products, in two sets.
     constexpr int U = AHEAD ? AHEAD : 1;  // steps a barrier
     constexpr int FS = AHEAD ? 2 * U : 1;
-    u32x4 xf[FS][MT][FX == kMxE4m3 ? 2 : 1];
-    unsigned xsc[FS][MT], wsc[FS][NBW];
+    // blocks of 16 rows whose fragments are held at once: with all six of a tall
+    // tile in e4m3 66 registers spill
+    constexpr int MG = MT > 4 && FX == kMxE4m3 ? 2 : MT;
+    static_assert(MG == MT || !AHEAD, "fragments ahead are of all rows");
+    u32x4 xf[FS][MG][FX == kMxE4m3 ? 2 : 1];
+    unsigned xsc[FS][MG], wsc[FS][NBW];
     // slot s; chunk: of the scale bytes in LDS; wchunk: of all chunks so far
-    auto read_frags = [&](int f, int s, int chunk, int wchunk) {
+    auto read_frags = [&](int f, int s, int chunk, int wchunk, int m0 = 0) {
         const unsigned char *base = lds_raw + s * SLOT;
 #pragma unroll
-        for (int b = 0; b < NBW; ++b)
+        for (int b = 0; m0 == 0 && b < NBW; ++b)
             wsc[f][b] = *reinterpret_cast<const unsigned *>(wscales + (wchunk & (WC - 1)) * (4 * NBW * 256) + b * 256 + lane * 4);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const unsigned char *rp = base + (m * 16 + fr) * RB;
-            xsc[f][m] = *reinterpret_cast<const unsigned *>(scales + (m * 16 + fr) * sstride + chunk * 16 + (s % 4) * 4);
+        for (int m = 0; m < MG; ++m) {
+            const int r = (m0 + m) * 16 + fr;
+            const unsigned char *rp = base + r * RB;
+            xsc[f][m] = *reinterpret_cast<const unsigned *>(scales + r * sstride + chunk * 16 + (s % 4) * 4);
             xf[f][m][0] = *reinterpret_cast<const u32x4 *>(rp + ((fg ^ piece_key<CPR>(fr)) * 16));
             if constexpr (FX == kMxE4m3)
                 xf[f][m][1] = *reinterpret_cast<const u32x4 *>(rp + (((4 + fg) ^ piece_key<CPR>(fr)) * 16));
         }
     };
-    auto multiply = [&](int f, int s, int m, int b) {
+    auto multiply = [&](int f, int s, int m, int b, int m0) {
         const u32x4 p = xf[f][m][0], q = xf[f][m][FX == kMxE4m3 ? 1 : 0], v = w[s][b];
         const i32x8 x8 = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
                                        : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
         const i32x8 w8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
         const int sx = (int)(xsc[f][m] >> (8 * fg)), sw = (int)wsc[f][b];
-        f32x4 &d = acc[m][b];
+        f32x4 &d = acc[m0 + m][b];
         if (s % 4 == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 0, sw, 0, sx);
         if (s % 4 == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 1, sw, 0, sx);
         if (s % 4 == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 2, sw, 0, sx);
@@ -276,19 +282,22 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
             } else {
                 if (s0 == 0) issue_x(SL - 1, cb + SL - 1);
                 else issue_x(s0 - 1, nb + s0 - 1);
-                read_frags(0, s0, (cb + s0) / 4 % SC, (cb + s0) / 4);
             }
             // A group's products, then the loads into the registers they leave:
             // free to move, the loads would go first, into as many more.
 #pragma unroll
             for (int s = s0; s < s0 + U; ++s)
 #pragma unroll
-                for (int b = 0; b < NBW; ++b) {
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int m0 = 0; m0 < MT; m0 += MG) {
+                    if constexpr (!AHEAD) read_frags(0, s, (cb + s) / 4 % SC, (cb + s) / 4, m0);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) multiply(s % FS, s, m, b);
-                    __builtin_amdgcn_sched_barrier(0);
-                    issue_w(s, nb + s, (nb + s) / 4, b);
+                    for (int b = 0; b < NBW; ++b) {
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int m = 0; m < MG; ++m) multiply(s % FS, s, m, b, m0);
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (m0 + MG == MT) issue_w(s, nb + s, (nb + s) / 4, b);
+                    }
                 }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -377,10 +386,12 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
 // 40 tokens (64 experts of 4096 x 1408, 8 a token: 113 -> 99 us) and 10 % of 512
 // tokens' (128 of 2880 x 2880, 4 a token: 328 -> 293).  For those that tiles
 // share the same loads cost 12 %: chosen tile by tile.
+//
+// Grouped tiles of 64 rows are 96 high for the experts of which that makes fewer
+// (moe_tile_height).
 template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     mxfp4_tile_kernel(TileArgs a) {
-    constexpr int ROWS = MT * 16;
     // The work list goes expert by expert (dense: one), in it column tile by
     // column tile, the row tiles of a column tile side by side: those share
     // their weights, and all of an expert's share its rows of x.
@@ -389,8 +400,18 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     if (at < 0) return;
     MoeTile own{0, 0, a.M, 0};
     if constexpr (MODE != kDense) own = a.tiles[at / a.col_tiles];
-    const int nt = (own.rows + ROWS - 1) / ROWS, local = at - own.first * a.col_tiles;
+    const int height = MODE == kDense ? MT * 16 : moe_tile_height(own.rows, MT * 16, a.tall);
+    const int nt = (own.rows + height - 1) / height, local = at - own.first * a.col_tiles;
     const int ct = local / nt, rt = local - ct * nt;
+    if constexpr (MODE != kDense && MT == 4) {
+        if (height > MT * 16) {
+            if (nt == 1)
+                mxfp4_tile<6, NBW, FX, MODE, SL, AHEAD, kCacheStream>(a, own, ct, rt);
+            else
+                mxfp4_tile<6, NBW, FX, MODE, SL, AHEAD, kCacheDefault>(a, own, ct, rt);
+            return;
+        }
+    }
     if (nt == 1)
         mxfp4_tile<MT, NBW, FX, MODE, SL, AHEAD, kCacheStream>(a, own, ct, rt);
     else
@@ -402,8 +423,9 @@ namespace {
 // tiles: row tiles (grouped products: a bound on them).
 template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 int go(TileArgs a, int tiles, hipStream_t stream) {
-    const size_t bytes = tile_lds_bytes(MT, NBW, FX, SL, tile_scale_chunks(mxfp4_chunks(a.K), SL));
-    constexpr size_t most = tile_lds_bytes(MT, NBW, FX, SL, tile_scale_most(SL));
+    constexpr int TALL = MODE != kDense && MT == 4 ? 6 : MT;
+    const size_t bytes = tile_lds_bytes(TALL, NBW, FX, SL, tile_scale_chunks(mxfp4_chunks(a.K), SL));
+    constexpr size_t most = tile_lds_bytes(TALL, NBW, FX, SL, tile_scale_most(SL));
     static_assert(most <= 160 * 1024 - 256, "LDS of a workgroup");
     static std::atomic<unsigned long long> lds_set{0};
     const hipError_t e = allow_dynamic_lds(
@@ -479,6 +501,7 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
     a.count = s.count;
     a.pairs = s.pairs;
     a.top = m.k;
+    a.tall = s.tall;
     return m.fmt == kMxE4m3 ? pick<kGateUp, kMxE4m3, 4, 4>(a, rows, tiles, stream)
                             : pick<kGateUp, kMxE2m1, 4, 4>(a, rows, tiles, stream);
 }
@@ -498,6 +521,7 @@ int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const
     a.count = s.count;
     a.pairs = s.pairs;
     a.top = m.k;
+    a.tall = s.tall;
     // Wide column tiles halve what the rows cost (2048 tokens: 170 -> 161 us);
     // with few rows more, narrower workgroups stream better (40: 32 -> 30 us).
     return m.fmt == kMxE4m3 ? pick<kDown, kMxE4m3, 4, 2>(a, rows, tiles, stream)

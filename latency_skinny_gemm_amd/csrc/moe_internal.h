@@ -89,6 +89,14 @@ struct MoeTile {
 };
 // Rows a tile may hold, by the average number of pairs an expert gets.
 int moe_tile_rows(int T, int k, int E);
+// The height of the tiles of an expert with n rows: 96 (tall) instead of 64 where
+// that makes fewer of them, and so fewer readings of its weights.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+constexpr int moe_tile_height(int n, int rows, int tall) {
+    return tall && (n + 95) / 96 < (n + 63) / 64 ? 96 : rows;
+}
 // The most tiles of that height the pairs can make.
 constexpr int moe_max_tiles(long P, int E, int rows) {
     return (int)((P < E ? P : E) + P / rows);
@@ -108,8 +116,9 @@ struct MoeLists {
     const MoeTile *tiles;
     const int *count;  // tiles in use
     const int *pairs;  // sorted row -> pair t * k + j
+    int tall;          // tiles of 64 rows may be 96 high
 };
-// rows: height of the tiles (16, 32, 64 or 128); tiles: bound on their number.
+// rows: height of the tiles (16, 32 or 64); tiles: bound on their number.
 int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, const uint8_t *xe,
                        uint8_t *h, uint8_t *he, int rows, int tiles, hipStream_t stream);
 int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const uint8_t *he,

@@ -123,8 +123,32 @@ def route(l, k, scores, bias, groups, top_groups, renormalize, factor):
     return key, kept, ids, w * factor
 
 
-def experts(x, ids, weights, w13, w2, fmt):
-    """x [T, H], w13 [E, 2I, H], w2 [E, H, I] fp64 values."""
+def _undecided(v, fmt, near):
+    """Hidden values whose code, or whose block's scale, lies within `near` of
+    its value of the next one: (slice, the values it would then stand for)."""
+    largest, table = (E4M3_LARGEST, E4M3_VALUES[:-1]) if fmt == "e4m3" else (E2M1_LARGEST, E2M1_VALUES)
+    codes, e = quantise(v, fmt)
+    scaled = np.ldexp(np.abs(v), 127 - np.repeat(e, 32))
+    mids = (table[1:] + table[:-1]) / 2
+    k = np.clip(np.searchsorted(mids, scaled), 0, len(mids) - 1)
+    k = np.where((k > 0) & (np.abs(scaled - mids[k - 1]) < np.abs(scaled - mids[k])), k - 1, k)
+    for i in np.nonzero(np.abs(scaled - mids[k]) <= near * scaled)[0]:
+        here = codes[i] % len(values(fmt))
+        other = np.ldexp(table[k[i] + 1 if here == k[i] else k[i]], int(e[i // 32]) - 127)
+        yield slice(i, i + 1), np.copysign([other], v[i])
+    top = np.repeat(np.abs(v).reshape(-1, 32).max(-1), 32)
+    for f in (1 - near, 1 + near):
+        o = quantise(top * f, fmt)[1]
+        for b in np.nonzero((o != e) & (top[::32] > 0))[0]:
+            at = slice(32 * b, 32 * b + 32)
+            q = np.clip(np.ldexp(v[at], 127 - int(o[b])), -largest, largest)
+            yield at, dequantise(_nearest(q, table), o[b:b + 1], fmt)
+
+
+def experts(x, ids, weights, w13, w2, fmt, either=None):
+    """x [T, H], w13 [E, 2I, H], w2 [E, H, I] fp64 values.  either: a list that
+    takes (t, change of out[t]) for the hidden values and scales that lie within
+    2^-13 of a tie, where the precision of the products' sums decides."""
     xq = rounded(x, fmt)
     out = np.zeros_like(xq)
     for t in range(x.shape[0]):
@@ -133,8 +157,12 @@ def experts(x, ids, weights, w13, w2, fmt):
             if not 0 <= e < w13.shape[0]:
                 continue
             g, u = np.split(w13[e] @ xq[t], 2)
-            h = rounded(g / (1.0 + np.exp(-g)) * u, fmt)
+            v = g / (1.0 + np.exp(-g)) * u
+            h = rounded(v, fmt)
             out[t] += weights[t, j] * (w2[e] @ h)
+            if either is not None:
+                either += [(t, weights[t, j] * (w2[e][:, at] @ (alt - h[at])))
+                           for at, alt in _undecided(v, fmt, 2.0 ** -13)]
     return out
 
 

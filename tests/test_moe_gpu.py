@@ -20,6 +20,9 @@ Tolerances, derived:
   about 2^-14 of its largest term, so fewer than one code in 100 lies that near a
   tie; a flip moves a value by at most 2^-2 (e2m1) of it, so the sum by about
   sqrt(1/100) * 2^-2 * rms = 0.025 rms; twice that is allowed.
+  That is a bound on many flips; a single one of a value far above the rest, or
+  of a block's scale, is accounted for itself: the reference has both codes
+  where a value lies within 2^-13 of a tie.
 """
 import importlib.util
 import math
@@ -503,8 +506,12 @@ def _choices(seed, T, k, E):
 
 def _check_experts(skg, m, x, ids, w, fmt):
     out = skg.moe_mxfp4(x.to(DEV), ids.to(DEV), w.to(DEV), m.w13, m.w2, x_format=fmt)
-    want = ref.experts(ref.f64(x), ids.numpy(), ref.f64(w), m.v13, m.v2, fmt)
+    either = []
+    want = ref.experts(ref.f64(x), ids.numpy(), ref.f64(w), m.v13, m.v2, fmt, either)
     got = ref.f64(out)
+    for t, change in either:  # where the sums' last bits decide: whichever was taken
+        if np.linalg.norm(got[t] - want[t] - change) < np.linalg.norm(got[t] - want[t]):
+            want[t] += change
     rms = math.sqrt(np.mean(want ** 2)) if want.size else 0.0
     assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 0.05 * rms)
     # most values are far closer than the worst allowed
@@ -522,6 +529,8 @@ def _check_experts(skg, m, x, ids, w, fmt):
                                        # enough bytes to be sorted: tiles of 16, 32 and 64 rows
                                        (64, 4, 64, 448, 448), (200, 4, 40, 288, 224), (300, 4, 8, 160, 224),
                                        (600, 8, 12, 96, 96), (500, 64, 64, 64, 32), (80, 2, 2, 8480, 64),
+                                       # enough of them for tiles of 96 rows, one or more to an expert
+                                       (2500, 2, 100, 32, 1024), (896, 8, 32, 32, 1024),
                                        # unsorted, rows of several rounds of loads
                                        (1, 8, 8, 96, 4128), (1, 2, 2, 8480, 64)])
 def test_experts(skg, T, k, E, H, I, fmt):
