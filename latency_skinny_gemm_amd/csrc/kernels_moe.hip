@@ -184,14 +184,15 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
 // Whether each pair reads its expert's weights for itself (two launches)
 // instead of sorting (four).  Sorting saves the weights of the experts that
 // several pairs share, and its tiles stream at 5.9 TB/s against 5.0, for about
-// 12 us more.  Both sides measured from 1 to 32 tokens at (E, k, H, I) =
-// (128, 4, 2880, 2880), (32, 4, 2880, 1440) and (256, 8, 2048, 512): they cross
-// at 16-24, 16-24 and 96-128 pairs, where this does.
+// 14 us more.  Both sides measured from 1 to 20 tokens at (E, k, H, I) =
+// (128, 4, 2880, 2880), (32, 4, 2880, 1440) and (256, 8, 2048, 512): 1 token 17,
+// 11 and 10 us against 32, 26 and 22; they cross at 20-24, 24-32 and 112-128
+// pairs, where this does.
 static bool moe_unsorted(const MoeArgs &a) {
     const double P = (double)a.T * a.k, E = a.E;
     const double shared = E * (1.0 - pow(1.0 - 1.0 / E, P));        // experts that P pairs meet
     const double expert_us = 3.0 * a.H * a.I * 17 / 32 * 1e-6;      // at 1 TB/s
-    return P * expert_us / 5.0 - shared * expert_us / 5.9 < 12.0 &&
+    return P * expert_us / 5.0 - shared * expert_us / 5.9 < 14.0 &&
            mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds &&
            a.k * mxfp4_row_lds_bytes(a.fmt, a.I) <= kMxRowMaxLds;
 }

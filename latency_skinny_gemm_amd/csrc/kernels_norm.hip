@@ -7,8 +7,14 @@
 // fp32 values: static e4m3, or MX codes whose 32-value blocks are the four
 // neighbouring lanes of a quad.
 //
+// The factor of a row errs coherently in all its codes, and each rounding of a
+// value moves it across more ties.  So the waves' sums are added in fp64, the
+// factor is carried in two fp32 numbers, and a value goes to its 8-bit code as if
+// it had not been rounded before.  Forty drawn calls had 5 codes other than the
+// exact ones so, against 40 by rounding every step.
+//
 // Many rows are bound by HBM: 8192 x 7168 with a residual to MX moves 411 MB in
-// 77 us, 5.3 TB/s (a copy on this card: 4.7).  One row takes 3.4 us: a launch,
+// 79 us, 5.2 TB/s (a copy on this card: 4.7).  One row takes 3.6 us: a launch,
 // a load, the reduction's barrier and a store, one after another.
 #include "device_common.h"
 #include "internal.h"
@@ -25,8 +31,53 @@ struct NormArgs {
     uint8_t *y, *e8;
     uint16_t *residual_out;
     float eps;
+    double inv_k;
     int M, K;
 };
+
+// A factor as the sum of two fp32 numbers.
+struct Factor {
+    float hi, lo;
+};
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const unsigned long long u = (unsigned long long)__double_as_longlong(v);
+    const unsigned lo = dpp_u32<CTRL>((unsigned)u), hi = dpp_u32<CTRL>((unsigned)(u >> 32));
+    return __longlong_as_double((long long)((unsigned long long)hi << 32 | lo));
+}
+// Sum over 16 lanes, the same in each.
+__device__ __forceinline__ double row16_sum(double v) {
+    v += dpp_f64<kDppQuadSwap1>(v);
+    v += dpp_f64<kDppQuadSwap2>(v);
+    v += dpp_f64<kDppHalfMirror>(v);
+    return v + dpp_f64<kDppMirror>(v);
+}
+
+// 1 / sqrt(m): the hardware's (1 ulp) and what it leaves, from 1 - m hi^2 with
+// exact products.  Where that is no number (m 0, infinite or NaN) hi stands alone.
+__device__ __forceinline__ Factor rsqrt_factor(double m) {
+    const float mh = (float)m, ml = (float)(m - (double)mh), c = __builtin_amdgcn_rsqf(mh);
+    const float t = c * c, te = __builtin_fmaf(c, c, -t);
+    const float d = __builtin_fmaf(-mh, te, __builtin_fmaf(-ml, t, __builtin_fmaf(-mh, t, 1.0f)));
+    const float lo = 0.5f * c * d;
+    return {c, fabsf(lo) <= fabsf(c) * 1e-3f ? lo : 0.0f};
+}
+// f / v, likewise.
+__device__ __forceinline__ Factor divided(Factor f, float v) {
+    const float q = 1.0f / v, ql = __builtin_fmaf(-q, v, 1.0f) * q, hi = f.hi * q;
+    const float lo = __builtin_fmaf(f.hi, q, -hi) + __builtin_fmaf(f.hi, ql, f.lo * q);
+    return {hi, fabsf(lo) <= fabsf(hi) * 1e-3f ? lo : 0.0f};
+}
+
+// y + rest, |rest| up to half a step of y, as the odd one of the two fp32 numbers
+// around it: a tie between codes, an even number, is then met only by y itself,
+// so that the code is that of the sum.  y infinite, NaN or 0: as it is.
+__device__ __forceinline__ float to_odd(float y, float rest) {
+    const unsigned b = __float_as_uint(y);
+    const int step = ((int)(__float_as_uint(rest) ^ b) >> 31) | 1;  // away from 0, or towards it
+    return (b & 1u) == 0 && rest != 0.0f && fabsf(rest) < fabsf(y) ? __uint_as_float(b + (unsigned)step) : y;
+}
 
 // The eight fp32 sums of vector i of a row, and bf16 of them to residual_out.
 __device__ __forceinline__ void norm_load(const NormArgs &a, size_t row0, int i, float (&s)[8]) {
@@ -41,17 +92,38 @@ __device__ __forceinline__ void norm_load(const NormArgs &a, size_t row0, int i,
 
 template <int OUT>
 __device__ __forceinline__ void norm_store(const NormArgs &a, int row, size_t row0, int i,
-                                           const float (&s)[8], float inv, float qinv) {
+                                           const float (&s)[8], Factor c) {
     float w[8], y[8];
     bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.weight + (size_t)i * 8), w);
+    // s * (hi + lo) * w, in effect rounded once; what is left of it in `rest`
+    auto value = [&](int j, float *rest) {
+        const float p = s[j] * c.hi, e = __builtin_fmaf(s[j], c.lo, __builtin_fmaf(s[j], c.hi, -p)) * w[j];
+        const float v = __builtin_fmaf(p, w[j], e);
+        if (rest) *rest = __builtin_fmaf(p, w[j], -v) + e;
+        return v;
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = s[j] * inv * w[j];
+    for (int j = 0; j < 8; ++j) y[j] = value(j, nullptr);
+    if constexpr (OUT != SKG_NORM_BF16) {
+        // ties between codes end in 19 zeros
+        unsigned low = ~0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) low = min(low, __float_as_uint(y[j]) << 13);
+        if (low == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float rest;
+                const float v = value(j, &rest);
+                y[j] = to_odd(v, rest);
+            }
+        }
+    }
     const size_t at = row0 + (size_t)i * 8;
     if constexpr (OUT == SKG_NORM_BF16) {
         *reinterpret_cast<u32x4 *>(a.y + at * 2) = f32x8_to_bf16(y);
     } else if constexpr (OUT == SKG_NORM_E4M3) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = quant_clamp(y[j] * qinv);
+        for (int j = 0; j < 8; ++j) y[j] = quant_clamp(y[j]);
         *reinterpret_cast<uint2 *>(a.y + at) = mx_codes8_e4m3(y, 1.0f);
     } else {
         const int e = mx_store8<kMxE4m3>(y, a.y, at);
@@ -87,16 +159,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(sv[j], sv[j], sq);
     }
     sq = wave_sum(sq);
+    double total = sq;
     if constexpr (TPR > 64) {
         __shared__ float part[TPR / 64];
         if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = sq;
         __syncthreads();
-        sq = 0.0f;
-#pragma unroll
-        for (int w = 0; w < TPR / 64; ++w) sq += part[w];
+        // every lane of a row of 16 adds the same up to 16 partial sums
+        total = (threadIdx.x & 15) < TPR / 64 ? (double)part[threadIdx.x & 15] : 0.0;
+        total = row16_sum(total);
     }
-    const float inv = 1.0f / sqrtf(sq / (float)a.K + a.eps);
-    const float qinv = OUT == SKG_NORM_E4M3 ? 1.0f / a.scale[0] : 1.0f;
+    Factor c = rsqrt_factor(__builtin_fma(total, a.inv_k, (double)a.eps));
+    if constexpr (OUT == SKG_NORM_E4M3) c = divided(c, a.scale[0]);
 #pragma unroll
     for (int v = 0; v < nv; ++v) {
         const int i = t + v * TPR;
@@ -105,7 +178,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         if constexpr (V == 0) norm_load(a, row0, i, sv);
         if (a.residual_out)
             *reinterpret_cast<u32x4 *>(a.residual_out + row0 + (size_t)i * 8) = f32x8_to_bf16(sv);
-        norm_store<OUT>(a, row, row0, i, sv, inv, qinv);
+        norm_store<OUT>(a, row, row0, i, sv, c);
     }
 }
 
@@ -144,7 +217,7 @@ int launch_rmsnorm(const void *x, const void *residual, const void *weight, floa
                    int out_format, const float *scale, void *y, void *e8, void *residual_out,
                    int M, int K, hipStream_t stream) {
     const NormArgs a{(const uint16_t *)x, (const uint16_t *)residual, (const uint16_t *)weight,
-                     scale, (uint8_t *)y, (uint8_t *)e8, (uint16_t *)residual_out, eps, M, K};
+                     scale, (uint8_t *)y, (uint8_t *)e8, (uint16_t *)residual_out, eps, 1.0 / K, M, K};
     switch (out_format) {
     case SKG_NORM_BF16: return pick<SKG_NORM_BF16>(a, stream);
     case SKG_NORM_E4M3: return pick<SKG_NORM_E4M3>(a, stream);
