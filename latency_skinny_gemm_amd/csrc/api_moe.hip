@@ -2,6 +2,8 @@
 // host before any HIP call, workspace, launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
 #include "moe_internal.h"
 #include "mx_common.h"
@@ -55,6 +57,64 @@ int check_linear(int M, int N, int K) {
     if (M > SKG_MAX_M || N >= 1 << 20 || K >= 1 << 20 || K < 32 || K % 32 != 0)
         return SKG_ERR_UNSUPPORTED;
     return SKG_OK;
+}
+
+// How a product is done: by blocks of few rows (how many; bf16 rows quantised on
+// the way or by a launch before), or by tiles (0).
+struct Mxfp4Way {
+    int blocks;
+    bool quantise_first;
+};
+
+// Time in us of the blocks that suit M rows best.  A workgroup brings its rows
+// and 16 columns of weights to a CU, 16 rows and more in two row blocks of the
+// matrix instruction; a CU's workgroups follow each other, from 32 steps of K on
+// (16 waves) without overlap.  Fits 300 points of M = 2-512, N = 256-16384,
+// K = 2048-7168 to some 15 %.
+double rows_time(int M, int N, int K, int format, bool codes, int *blocks) {
+    // a column group's blocks share an XCD: 32 CUs for every eighth group
+    const int groups = (mxfp4_groups(N) + 7) / 8, cus = kNumCusMI355X / 8;
+    const size_t fit = kMxRowMaxLds / mxfp4_row_lds_bytes(format, K);
+    const int most = (int)std::min<size_t>(codes ? kMxRowsCodes : kMxRowsBf16, fit);
+    if (most < 1) return 1e30;
+    const bool alone = mxfp4_steps(K) > 32;
+    const double weights = 3.5e-4 * K;
+    const double row = !codes ? 0.07 + 4.1e-5 * K : format == SKG_MX_E4M3 ? 0.05 + 2e-5 * K : 0.05 + 0.6e-5 * K;
+    const int least = (M + most - 1) / most;  // blocks
+    double best = 1e30;
+    for (int i = 0; i < 3; ++i) {
+        const long cu = i < 2 ? i + 1 : ((long)least * groups + cus - 1) / cus;
+        const int b = (int)std::min<long>(M, cu * cus / groups);
+        if (b < least) continue;
+        const int r = (M + b - 1) / b;
+        const double us = (alone ? cu : 1) * 1.5 + cu * (weights + row * r + (r > 16 ? 1.3 : 0.0));
+        if (us < best) {
+            best = us;
+            *blocks = (M + r - 1) / r;
+        }
+    }
+    return best;
+}
+
+// Measured (us, e4m3 from bf16, weights from memory; blocks, tiles):
+//   16 x 576 x 7168    4.9  12.7      17 x 4096 x 7168   10.6  13.5
+//   37 x 1111 x 2880   5.9   8.5      24 x 4096 x 7168   14.5  13.6
+//   128 x 256 x 2880   4.7   8.4      64 x 2112 x 7168   20.9  12.5
+//   64 x 576 x 7168    7.8  12.2      16 x 16384 x 4096  30    11.9
+Mxfp4Way mxfp4_way(int M, int N, int K, int format, bool codes) {
+    Mxfp4Way way{0, false};
+    double best = mxfp4_tile_time(M, N, K);
+    int blocks = 0;
+    double us = rows_time(M, N, K, format, codes, &blocks);
+    if (us < best) {
+        best = us;
+        way = {blocks, false};
+    }
+    if (!codes) {
+        us = rows_time(M, N, K, format, true, &blocks) + 2.3;  // the launch before
+        if (us < best) way = {blocks, true};
+    }
+    return way;
 }
 
 int check_moe(int T, int k, int H, int I, int E) {
@@ -196,9 +256,8 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
     Mxfp4Args a{(const uint8_t *)x, (int)code_bytes(x_format, K), (const uint8_t *)x_e8m0, K / 32, x_format,
                 (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
-    const bool few = M <= (x_e8m0 ? kMxRowsMaxCodes : mx_rows_max(x_format)) &&
-                     M * mxfp4_row_lds_bytes(x_format, K) <= kMxRowMaxLds;
-    if (few && (x_e8m0 || M <= kMxRowsMaxBf16)) return status(launch_mxfp4_rows(a, stream));
+    const Mxfp4Way way = mxfp4_way(M, N, K, x_format, x_e8m0 != nullptr);
+    if (way.blocks && !way.quantise_first) return status(launch_mxfp4_rows(a, way.blocks, stream));
     float *ws = nullptr;
     unsigned *tk = nullptr;
     rc = acquire(stream, floats_of(linear_workspace_bytes((size_t)M, K)), 0, &ws, &tk);
@@ -215,7 +274,7 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     if (e != (int)hipSuccess) return SKG_ERR_HIP;
     a.xe = scales;
     a.es = mx_scale_stride(K);
-    return status(few ? launch_mxfp4_rows(a, stream) : launch_mxfp4(a, stream));
+    return status(way.blocks ? launch_mxfp4_rows(a, way.blocks, stream) : launch_mxfp4(a, stream));
 }
 
 extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weights,

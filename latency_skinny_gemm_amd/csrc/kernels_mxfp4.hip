@@ -468,6 +468,16 @@ int dense(const TileArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// As dense() picks them.
+double mxfp4_tile_time(int M, int N, int K) {
+    const long c64 = (N + 63) / 64, c128 = (N + 127) / 128, r16 = (M + 15) / 16, r32 = (M + 31) / 32;
+    const double us = 5.3 + 9.5e-4 * K;
+    if (r16 * c64 <= kNumCusMI355X) return us;
+    if (r32 * c64 <= kNumCusMI355X) return 1.25 * us;
+    if (r32 * c128 <= kNumCusMI355X) return 1.6 * us;
+    return 2.5 * us * (double)(((M + 63) / 64 * c128 + kNumCusMI355X - 1) / kNumCusMI355X);
+}
+
 int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
     TileArgs a{};
     a.x = p.x;

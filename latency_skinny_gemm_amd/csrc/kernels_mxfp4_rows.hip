@@ -8,11 +8,13 @@
 // at the end, in wave order: no second launch, no partials in memory, the same
 // bits every time.  The rows are brought to LDS by the workgroup, bf16 ones
 // quantised on the way, while the weights are in flight: that saves the launch
-// that would do it.
+// that would do it.  More rows go in blocks to more workgroups, while there are
+// CUs without one: what a workgroup waits for grows with its rows.
 //
 // Measured, weights from memory: one row of 7168 by 2112 columns 4.1 us (8.0 MB
 // of weights, 2 TB/s; a launch and one load after another make most of it),
-// 16 rows 9.3 (the rows' quantising), 16 rows of e2m1 codes 5.4.  Experts of
+// 16 rows 9.5 (the rows' quantising), 16 rows of e2m1 codes 5.4; 16 rows by 576
+// columns 4.9, in four blocks (in one 8.9).  Experts of
 // 2880 x 2880, one token's four: 8.7 us gate and up (35 MB, 4.1 TB/s) and 5.9
 // down (18 MB, 3.0).  Fragments loaded straight to registers, without LDS:
 // 6.9, 9.9, 6.7, 10.1 and 5.6 us.
@@ -96,6 +98,7 @@ struct RowArgs {
     const int *ids;          // experts
     const float *weights;
     int top, E;
+    int blocks, block_rows;  // dense: blocks of rows, and rows of all but the last
     // set by go(): waves' loads per row of codes (or bf16) and of scale bytes,
     // and what divides by them and by the steps of K
     int row_loads, scale_loads;
@@ -130,7 +133,12 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
 
     int j0, row = 0, units = KS;  // first group, (pair or token), steps to share
     if constexpr (MODE == kRowsDense) {
-        j0 = blockIdx.x * R;
+        // the blocks of a column group side by side on one XCD (workgroup b runs on
+        // XCD b % 8): they read the same weights
+        const int i = blockIdx.x >> 3, g = i / a.blocks;
+        j0 = (g * 8 + (int)(blockIdx.x & 7)) * R;
+        row = (i - g * a.blocks) * a.block_rows;
+        if (j0 >= ng || row >= a.M) return;
     } else if constexpr (MODE == kRowsGateUp) {
         const int cols = a.N / 32;
         row = blockIdx.x / cols;
@@ -161,8 +169,8 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
         for (int b = 0; b < R; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // the rows: a view that ends with the last one
-    const size_t x0 = MODE == kRowsGateUp ? (size_t)(row / a.top) : MODE == kRowsDown ? (size_t)row * a.top : 0;
-    const unsigned xrows = MODE == kRowsGateUp ? 1u : MODE == kRowsDown ? (unsigned)a.top : (unsigned)a.M;
+    const size_t x0 = MODE == kRowsGateUp ? (size_t)(row / a.top) : MODE == kRowsDown ? (size_t)row * a.top : (size_t)row;
+    const unsigned xrows = MODE == kRowsGateUp ? 1u : MODE == kRowsDown ? (unsigned)a.top : (unsigned)min(a.block_rows, a.M - row);
     const Rsrc xr = make_rsrc(a.x + x0 * a.xs, (xrows - 1) * a.xs + rowb);
     const Rsrc er = make_rsrc(BF16 ? nullptr : a.xe + x0 * a.es, BF16 ? 0u : xrows * a.es);
     constexpr unsigned CB = FX == kMxE4m3 ? 128u : 64u;  // bytes of a row's codes in a step
@@ -352,10 +360,10 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
     } else {
         for (int i = t; i < ROWS * R * 16; i += NW * 64) {
             const int r = i / (R * 16), c = i % (R * 16), n = j0 * 16 + c;
-            if (n >= a.N || (!ONE && r >= a.M)) continue;
+            if (n >= a.N || (!ONE && r >= (int)xrows)) continue;
             float v = sum(r, c);
             if (MODE == kRowsDense && a.bias) v += bf16_to_f32(a.bias[n]);
-            store_out(a.out, (size_t)(ONE ? row : r) * a.N + n, v, a.out_f32);
+            store_out(a.out, (size_t)(ONE ? row : row + r) * a.N + n, v, a.out_f32);
         }
     }
 }
@@ -364,7 +372,7 @@ namespace {
 
 template <int MODE, int MT, int R, int FX, bool BF16, int NW, int U, int XB>
 int go(RowArgs a, size_t grid, hipStream_t stream) {
-    const int rows = MODE == kRowsGateUp ? 1 : MODE == kRowsDown ? a.top : a.M;
+    const int rows = MODE == kRowsGateUp ? 1 : MODE == kRowsDown ? a.top : a.block_rows;
     const size_t lds = rows * mxfp4_row_lds_bytes(FX, a.K);
     const int KS = mxfp4_steps(a.K);
     a.row_loads = (KS * (BF16 ? 16 : FX == kMxE4m3 ? 8 : 4) + 63) / 64;
@@ -399,7 +407,7 @@ int waves(const RowArgs &a, int nw, size_t grid, hipStream_t stream) {
 template <int FX, bool BF16>
 int dense16(const RowArgs &a, int KS, size_t grid, hipStream_t stream) {
     const int nw = waves_of(KS, 4), pieces = KS * (BF16 ? 16 : FX == kMxE4m3 ? 8 : 4);
-    const int loads = a.M * ((max(pieces, BF16 ? 0 : KS * 4) + 63) / 64);
+    const int loads = a.block_rows * ((max(pieces, BF16 ? 0 : KS * 4) + 63) / 64);
     if (loads <= nw) return waves<kRowsDense, 1, 1, FX, BF16, 4, 1>(a, nw, grid, stream);
     if (loads <= 2 * nw) return waves<kRowsDense, 1, 1, FX, BF16, 4, 2>(a, nw, grid, stream);
     return waves<kRowsDense, 1, 1, FX, BF16, 4, 4>(a, nw, grid, stream);
@@ -407,16 +415,16 @@ int dense16(const RowArgs &a, int KS, size_t grid, hipStream_t stream) {
 
 template <int FX>
 int dense(const RowArgs &a, bool bf16, hipStream_t stream) {
-    const size_t grid = (size_t)mxfp4_groups(a.N);
+    const size_t grid = (size_t)((mxfp4_groups(a.N) + 7) / 8 * 8) * a.blocks;
     const int KS = mxfp4_steps(a.K);
     if (bf16) return dense16<FX, true>(a, KS, grid, stream);
-    if (a.M <= 16) return dense16<FX, false>(a, KS, grid, stream);
+    if (a.block_rows <= 16) return dense16<FX, false>(a, KS, grid, stream);
     return waves<kRowsDense, 2, 1, FX, false, 4, 4>(a, waves_of(KS, 4), grid, stream);
 }
 
 }  // namespace
 
-int launch_mxfp4_rows(const Mxfp4Args &p, hipStream_t stream) {
+int launch_mxfp4_rows(const Mxfp4Args &p, int blocks, hipStream_t stream) {
     RowArgs a{};
     a.x = p.x;
     a.xs = (unsigned)(p.xe ? p.xs : p.K * 2);
@@ -429,6 +437,8 @@ int launch_mxfp4_rows(const Mxfp4Args &p, hipStream_t stream) {
     a.M = p.M;
     a.N = p.N;
     a.K = p.K;
+    a.blocks = blocks;
+    a.block_rows = (p.M + blocks - 1) / blocks;
     return p.fmt == kMxE4m3 ? dense<kMxE4m3>(a, p.xe == nullptr, stream)
                             : dense<kMxE2m1>(a, p.xe == nullptr, stream);
 }

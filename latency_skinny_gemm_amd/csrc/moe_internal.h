@@ -62,19 +62,12 @@ struct Mxfp4Args {
 };
 // Codes with padded scale rows, any number of rows.
 int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
-// Few rows: codes, or up to 16 bf16 rows quantised on the way (above, every
-// workgroup quantising all of them costs more than a launch that does it once:
-// 4096 x 7168 to e2m1 takes 8.3 us at 12 rows, 9.6 at 16, and 9.1 at 17 with the
-// launch).
-constexpr int kMxRowsMaxBf16 = 16;
-// Codes: every workgroup takes in all rows, so the tile kernel overtakes it.
-// Given by the caller, not before 32 rows (2880 x 1111: 6.9 us in e4m3 and 6.3
-// in e2m1 there, tiles 7.9 and 7.8); quantised by a launch just before, sooner
-// (2880 x 1111, e4m3: 7.8 at 20, 8.9 at 24, tiles 8.3; 2048 x 8192, e2m1: 8.9 at
-// 28, 9.7 at 32, tiles 9.1).
-constexpr int kMxRowsMaxCodes = 32;
-constexpr int mx_rows_max(int fmt) { return fmt == SKG_MX_E4M3 ? 20 : 28; }
-int launch_mxfp4_rows(const Mxfp4Args &a, hipStream_t stream);
+// Blocks of few rows, a workgroup each for 16 columns: codes, or bf16 rows
+// quantised on the way.
+constexpr int kMxRowsBf16 = 16, kMxRowsCodes = 32;
+int launch_mxfp4_rows(const Mxfp4Args &a, int blocks, hipStream_t stream);
+// Time in us of the tiles, quantising included.
+double mxfp4_tile_time(int M, int N, int K);
 
 // ---------------------------------------------------------------- experts
 // Pairs (token, choice) sorted by expert, and the row tiles of the grouped
