@@ -248,8 +248,10 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
             asm volatile("" : "+s"(id[0]), "+s"(id[1]), "+s"(id[2]), "+s"(id[3]), "+s"(id[4]), "+s"(id[5]),
                               "+s"(wt[0]), "+s"(wt[1]), "+s"(wt[2]), "+s"(wt[3]), "+s"(wt[4]), "+s"(wt[5]));
 #pragma unroll
-            for (int i = 0; i < U; ++i)
+            for (int i = 0; i < U; ++i) {
                 expert[i] = u0 + i * NW < units && (unsigned)id[i] < (unsigned)a.E ? id[i] : -1;
+                if (expert[i] < 0) wt[i] = 0.0f;  // whatever stands there, infinite or NaN too
+            }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {

@@ -561,6 +561,27 @@ def test_experts_skewed_and_absent(skg, T, fmt):
     assert torch.all(out == 0)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,E,H,I", [(1, 6, 96, 64), (5, 6, 96, 64), (2000, 6, 96, 64), (72, 72, 480, 480)])
+def test_experts_weights_of_absent_choices_do_not_count(skg, T, E, H, I, fmt):
+    """The weight of a choice whose id lies outside [0, E) may be anything: with
+    NaN and infinities there, the same bits as with zeros, in calls that each
+    pair takes for itself and in sorted ones; zeros where a token has none left."""
+    k = 4
+    m = Experts(skg, E, H, I)
+    x = _randn(T, T, H).bfloat16()
+    ids, w = _choices(3, T, k, E)
+    ids[:, 1] = -1
+    ids[::2, 3] = E
+    ids[0] = -1
+    away = (ids < 0) | (ids >= E)
+    zeros = skg.moe_mxfp4(x.to(DEV), ids.to(DEV), torch.where(away, 0.0, w).to(DEV), m.w13, m.w2, x_format=fmt)
+    for bad in (math.nan, math.inf, -math.inf):
+        got = skg.moe_mxfp4(x.to(DEV), ids.to(DEV), torch.where(away, bad, w).to(DEV), m.w13, m.w2, x_format=fmt)
+        assert torch.isfinite(got).all() and torch.equal(got, zeros)
+        assert torch.all(got[0] == 0)
+
+
 @pytest.mark.parametrize("T", [3, 90, 3000])
 def test_experts_row_does_not_depend_on_its_neighbours(skg, T):
     """Other tokens' values and choices (their number the same): the same bits,
