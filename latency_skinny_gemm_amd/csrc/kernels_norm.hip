@@ -70,6 +70,12 @@ __device__ __forceinline__ Factor divided(Factor f, float v) {
     return {hi, fabsf(lo) <= fabsf(hi) * 1e-3f ? lo : 0.0f};
 }
 
+// a / v to 2 ulp for any v: the hardware's reciprocal takes no subnormals and makes none.
+__device__ __forceinline__ float quotient(float a, float v) {
+    const float m = fabsf(v) < 0x1p-100f ? 0x1p50f : fabsf(v) > 0x1p100f ? 0x1p-50f : 1.0f;
+    return a * m * __builtin_amdgcn_rcpf(v * m * m) * m;
+}
+
 // y + rest, |rest| up to half a step of y, as the odd one of the two fp32 numbers
 // around it: a tie between codes, an even number, is then met only by y itself,
 // so that the code is that of the sum.  y infinite, NaN or 0: as it is.
@@ -79,7 +85,7 @@ __device__ __forceinline__ float to_odd(float y, float rest) {
     return (b & 1u) == 0 && rest != 0.0f && fabsf(rest) < fabsf(y) ? __uint_as_float(b + (unsigned)step) : y;
 }
 
-// The eight fp32 sums of vector i of a row, and bf16 of them to residual_out.
+// The eight fp32 sums of vector i of a row.
 __device__ __forceinline__ void norm_load(const NormArgs &a, size_t row0, int i, float (&s)[8]) {
     bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.x + row0 + (size_t)i * 8), s);
     if (a.residual) {
@@ -90,9 +96,11 @@ __device__ __forceinline__ void norm_load(const NormArgs &a, size_t row0, int i,
     }
 }
 
+// Vector i of a row's output.  c: the row's factor, over the scale for e4m3;
+// plain: the factor alone, in one number.
 template <int OUT>
-__device__ __forceinline__ void norm_store(const NormArgs &a, int row, size_t row0, int i,
-                                           const float (&s)[8], Factor c) {
+__device__ __forceinline__ void norm_store(const NormArgs &a, size_t row0, int i,
+                                           const float (&s)[8], Factor c, float plain) {
     float w[8], y[8];
     bf16x8_to_f32(*reinterpret_cast<const u32x4 *>(a.weight + (size_t)i * 8), w);
     // s * (hi + lo) * w, in effect rounded once; what is left of it in `rest`
@@ -104,16 +112,30 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, int row, size_t ro
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = value(j, nullptr);
-    if constexpr (OUT != SKG_NORM_BF16) {
-        // ties between codes end in 19 zeros
+    // Past fp32's range (a scale near 0, an infinite weight) what is left over is
+    // infinite too, and their sum NaN: such values by the formula as it stands.
+    // Ties between codes end in 19 zeros, and so do infinities and that NaN.
+    bool again;
+    if constexpr (OUT == SKG_NORM_BF16) {
+        float finite = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) finite = __builtin_fmaf(y[j], 0.0f, finite);
+        again = finite != 0.0f;
+    } else {
         unsigned low = ~0u;
 #pragma unroll
         for (int j = 0; j < 8; ++j) low = min(low, __float_as_uint(y[j]) << 13);
-        if (low == 0) {
+        again = low == 0;
+    }
+    if (__builtin_expect(again, 0)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float rest;
-                const float v = value(j, &rest);
+        for (int j = 0; j < 8; ++j) {
+            float rest;
+            const float v = value(j, &rest);
+            if (!(fabsf(v) < __builtin_inff())) {
+                y[j] = s[j] * plain * w[j];
+                if constexpr (OUT == SKG_NORM_E4M3) y[j] = quotient(y[j], a.scale[0]);
+            } else if constexpr (OUT != SKG_NORM_BF16) {
                 y[j] = to_odd(v, rest);
             }
         }
@@ -169,6 +191,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         total = row16_sum(total);
     }
     Factor c = rsqrt_factor(__builtin_fma(total, a.inv_k, (double)a.eps));
+    const float plain = c.hi;
     if constexpr (OUT == SKG_NORM_E4M3) c = divided(c, a.scale[0]);
 #pragma unroll
     for (int v = 0; v < nv; ++v) {
@@ -178,7 +201,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         if constexpr (V == 0) norm_load(a, row0, i, sv);
         if (a.residual_out)
             *reinterpret_cast<u32x4 *>(a.residual_out + row0 + (size_t)i * 8) = f32x8_to_bf16(sv);
-        norm_store<OUT>(a, row, row0, i, sv, c);
+        norm_store<OUT>(a, row0, i, sv, c, plain);
     }
 }
 
