@@ -54,6 +54,13 @@ __device__ __forceinline__ double row16_sum(double v) {
     return v + dpp_f64<kDppMirror>(v);
 }
 
+// Sum over the wave's 64 lanes, the same in each.
+__device__ __forceinline__ double wave_sum64(double v) {
+    v = row16_sum(v);
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
 // 1 / sqrt(m): the hardware's (1 ulp) and what it leaves, from 1 - m hi^2 with
 // exact products.  Where that is no number (m 0, infinite or NaN) hi stands alone.
 __device__ __forceinline__ Factor rsqrt_factor(double m) {
@@ -159,7 +166,7 @@ __device__ __forceinline__ void norm_store(const NormArgs &a, size_t row0, int i
 // workgroup), V vectors of 8 values per lane held in registers; V == 0: rows
 // longer than the registers hold, read a second time for the output.
 template <int OUT, int TPR, int V>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 8) rmsnorm_kernel(NormArgs a) {
     constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
     const int t = threadIdx.x % TPR;
     const int row = blockIdx.x * ROWS + threadIdx.x / TPR;
@@ -190,7 +197,39 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         total = (threadIdx.x & 15) < TPR / 64 ? (double)part[threadIdx.x & 15] : 0.0;
         total = row16_sum(total);
     }
-    Factor c = rsqrt_factor(__builtin_fma(total, a.inv_k, (double)a.eps));
+    double mean = __builtin_fma(total, a.inv_k, (double)a.eps);
+    // Squares past either end of fp32 (values above 2^60, or rows of tiny ones with
+    // an eps as tiny): the sum again in fp64, and the row moved by the power of two
+    // that leaves its mean square near one.  The same in all of a row's lanes.
+    float move = 1.0f;
+    if (__builtin_expect(!(mean >= 0x1p-70 && total <= 0x1p120), 0)) {
+        double wide = 0.0;
+#pragma unroll
+        for (int v = 0; v < nv; ++v) {
+            const int i = t + v * TPR;
+            float(&sv)[8] = s[V > 0 ? v : 0];
+            if constexpr (V == 0) {
+                if (i >= k8) continue;
+                norm_load(a, row0, i, sv);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wide = __builtin_fma((double)sv[j], (double)sv[j], wide);
+        }
+        wide = wave_sum64(wide);
+        if constexpr (TPR > 64) {
+            __shared__ double wide_part[TPR / 64];
+            if ((threadIdx.x & 63) == 0) wide_part[threadIdx.x / 64] = wide;
+            __syncthreads();
+            wide = row16_sum((threadIdx.x & 15) < TPR / 64 ? wide_part[threadIdx.x & 15] : 0.0);
+        }
+        mean = __builtin_fma(wide, a.inv_k, (double)a.eps);
+        if (mean > 0.0 && mean <= 0x1p300) {  // else 0, infinite or NaN, as it is
+            const int n = min(max(-(ilogb(mean) / 2), -120), 120);
+            move = ldexpf(1.0f, n);
+            mean = ldexp(mean, 2 * n);
+        }
+    }
+    Factor c = rsqrt_factor(mean);
     const float plain = c.hi;
     if constexpr (OUT == SKG_NORM_E4M3) c = divided(c, a.scale[0]);
 #pragma unroll
@@ -201,6 +240,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rmsnorm_kernel(NormArgs
         if constexpr (V == 0) norm_load(a, row0, i, sv);
         if (a.residual_out)
             *reinterpret_cast<u32x4 *>(a.residual_out + row0 + (size_t)i * 8) = f32x8_to_bf16(sv);
+        if (__builtin_expect(move != 1.0f, 0))
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sv[j] *= move;
         norm_store<OUT>(a, row0, i, sv, c, plain);
     }
 }

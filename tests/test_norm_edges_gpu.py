@@ -183,3 +183,47 @@ def test_mx_codes_next_to_ties(skg, K):
         assert np.array_equal(_codes(out.e8m0), e), seed
         assert np.array_equal(_codes(out.y)[0, sure], want[0, sure]), seed
     assert other >= 5
+
+
+# ------------------------------------------------------------ squares past fp32's range
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "mx"])
+@pytest.mark.parametrize("K", LENGTHS)
+@pytest.mark.parametrize("residual", [False, True])
+def test_rows_whose_squares_leave_fp32(skg, K, residual, fmt):
+    """eps 0: rows down to bf16's subnormals and up to its largest values have
+    the norm of their shape, whatever their size."""
+    powers = [-131, -126, -110, -70, -63, -50, -34, 0, 59, 61, 63, 64, 90, 125]
+    size = torch.exp2(torch.tensor(powers, dtype=torch.float64))[:, None]
+    x = (_randn(K, len(powers), K).clamp(-3, 3).double() * size).bfloat16()
+    r = (0.5 * _randn(K + 2, len(powers), K).clamp(-1, 1).double() * size).bfloat16() if residual else None
+    w = (1 + 0.3 * _randn(K + 1, K)).bfloat16()
+    scale = torch.tensor([0.0123], device=DEV) if fmt == "e4m3" else None
+    out = skg.rmsnorm(x.to(DEV), w.to(DEV), residual=None if r is None else r.to(DEV), eps=0.0, out_format=fmt, scale=scale)
+    y = ref.norm(x, r, w, 0.0)[1]
+    if residual:
+        assert torch.equal(out.residual.cpu(), (x.float() + r.float()).bfloat16())
+    if fmt == "mx":
+        e = _codes(out.e8m0)
+        want_e = ref.quantise(y, "e4m3")[1]
+        near = np.abs(np.log2(np.abs(y).reshape(*want_e.shape, 32).max(-1) / 448.0) % 1.0 - 0.5) > 0.5 - 2.0 ** -14
+        assert np.all((e == want_e) | (near & (np.abs(e - want_e) <= 1)))
+        f = np.exp2(np.repeat(e, 32, -1) - 127.0)
+        got, t = _e4m3(_codes(out.y)), y / f
+    elif fmt == "e4m3":
+        got, t = _e4m3(_codes(out.y)), np.clip(y / float(np.float32(0.0123)), -448, 448)
+    else:
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -126))) - 7)
+        assert np.all(np.abs(ref.f64(out.y) - y) <= step / 2 + 2.0 ** -16 * np.abs(y))
+        return
+    step = np.exp2(np.floor(np.log2(np.maximum(np.abs(t), 2.0 ** -6))) - 3)
+    assert np.all(np.abs(got - t) <= step / 2 + 2.0 ** -15 * np.abs(t))
+
+
+def test_a_row_of_zeros_and_one_infinite_stay_as_the_formula_has_them(skg):
+    for K in LENGTHS:
+        x = torch.zeros(3, K, dtype=torch.bfloat16)
+        x[1, 5], x[2, 6] = math.inf, math.nan
+        y = skg.rmsnorm(x.to(DEV), torch.ones(K, dtype=torch.bfloat16, device=DEV), eps=0.0).y.cpu()
+        assert torch.isnan(y[0]).all() and torch.isnan(y[1, 5]) and torch.isnan(y[2]).all()
+        assert torch.all(y[1, :5] == 0) and torch.all(y[1, 6:] == 0)
