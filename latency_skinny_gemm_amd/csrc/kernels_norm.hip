@@ -16,6 +16,8 @@
 // Many rows are bound by HBM: 8192 x 7168 with a residual to MX moves 411 MB in
 // 79 us, 5.2 TB/s (a copy on this card: 4.7).  One row takes 3.6 us: a launch,
 // a load, the reduction's barrier and a store, one after another.
+#include <algorithm>
+
 #include "device_common.h"
 #include "internal.h"
 #include "moe_internal.h"
@@ -281,13 +283,21 @@ int pick(const NormArgs &a, hipStream_t stream) {
 int launch_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
                    int out_format, const float *scale, void *y, void *e8, void *residual_out,
                    int M, int K, hipStream_t stream) {
-    const NormArgs a{(const uint16_t *)x, (const uint16_t *)residual, (const uint16_t *)weight,
-                     scale, (uint8_t *)y, (uint8_t *)e8, (uint16_t *)residual_out, eps, 1.0 / K, M, K};
-    switch (out_format) {
-    case SKG_NORM_BF16: return pick<SKG_NORM_BF16>(a, stream);
-    case SKG_NORM_E4M3: return pick<SKG_NORM_E4M3>(a, stream);
-    default: return pick<SKG_NORM_MX>(a, stream);
+    // a grid has fewer than 2^32 work-items: 2^21 rows of up to 1024 lanes at a time
+    constexpr int kMostRows = 1 << 21;
+    for (size_t m0 = 0; m0 < (size_t)M; m0 += kMostRows) {
+        const size_t at = m0 * K;
+        auto rows = [&](const void *p) { return p ? (const uint16_t *)p + at : nullptr; };
+        const NormArgs a{rows(x), rows(residual), (const uint16_t *)weight, scale,
+                         (uint8_t *)y + (out_format == SKG_NORM_BF16 ? 2 * at : at),
+                         e8 ? (uint8_t *)e8 + at / 32 : nullptr, const_cast<uint16_t *>(rows(residual_out)),
+                         eps, 1.0 / K, (int)std::min<size_t>(M - m0, kMostRows), K};
+        const int e = out_format == SKG_NORM_BF16   ? pick<SKG_NORM_BF16>(a, stream)
+                      : out_format == SKG_NORM_E4M3 ? pick<SKG_NORM_E4M3>(a, stream)
+                                                    : pick<SKG_NORM_MX>(a, stream);
+        if (e != (int)hipSuccess) return e;
     }
+    return (int)hipSuccess;
 }
 
 }  // namespace skg

@@ -8,6 +8,7 @@
 // vector instructions, not by memory: 16384 tokens of 384 bf16 logits take
 // 8.2 us where their 14 MB would take 3; up to 512 tokens they take what a
 // launch and the chain of dependent steps take, 3 to 5 us.
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.h"
@@ -559,10 +560,17 @@ int pick(const RouteArgs &a, bool sigmoid, hipStream_t stream) {
 
 int launch_route(const void *logits, int dtype, const float *bias, const skinny_route_options &o,
                  float *weights, int *ids, int T, int E, hipStream_t stream) {
-    const RouteArgs a{logits, bias, weights, ids, T, E, o.k, o.groups, o.top_groups,
-                      o.renormalize, o.factor};
-    const bool sig = o.scores == SKG_SCORE_SIGMOID;
-    return dtype == SKG_DTYPE_F32 ? pick<float>(a, sig, stream) : pick<uint16_t>(a, sig, stream);
+    const bool sig = o.scores == SKG_SCORE_SIGMOID, f32 = dtype == SKG_DTYPE_F32;
+    // a grid has fewer than 2^32 work-items: 2^21 tokens of up to 64 lanes at a time
+    constexpr int kMostTokens = 1 << 21;
+    for (size_t t0 = 0; t0 < (size_t)T; t0 += kMostTokens) {
+        const RouteArgs a{(const uint8_t *)logits + t0 * E * (f32 ? 4 : 2), bias, weights + t0 * o.k, ids + t0 * o.k,
+                          (int)std::min<size_t>(T - t0, kMostTokens), E, o.k, o.groups, o.top_groups,
+                          o.renormalize, o.factor};
+        const int e = f32 ? pick<float>(a, sig, stream) : pick<uint16_t>(a, sig, stream);
+        if (e != (int)hipSuccess) return e;
+    }
+    return (int)hipSuccess;
 }
 
 }  // namespace skg

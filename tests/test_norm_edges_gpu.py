@@ -227,3 +227,25 @@ def test_a_row_of_zeros_and_one_infinite_stay_as_the_formula_has_them(skg):
         y = skg.rmsnorm(x.to(DEV), torch.ones(K, dtype=torch.bfloat16, device=DEV), eps=0.0).y.cpu()
         assert torch.isnan(y[0]).all() and torch.isnan(y[1, 5]) and torch.isnan(y[2]).all()
         assert torch.all(y[1, :5] == 0) and torch.all(y[1, 6:] == 0)
+
+
+# ------------------------------------------------------------ more rows than one grid holds
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "mx"])
+def test_more_rows_than_a_grid_holds(skg, fmt):
+    """2^26 rows of a wave each are 2^32 work-items: the same 2^20 rows over and
+    over, with the same result over and over."""
+    K, times = 32, 64
+    x, w = _randn(1, 1 << 20, K).bfloat16().to(DEV), (1 + 0.3 * _randn(2, K)).bfloat16().to(DEV)
+    r = (2 * _randn(3, 1 << 20, K)).bfloat16().to(DEV)
+    o = dict(out_format=fmt, scale=torch.tensor([0.01], device=DEV) if fmt == "e4m3" else None)
+    one = skg.rmsnorm(x, w, residual=r, **o)
+    many = skg.rmsnorm(torch.cat([x.repeat(times, 1), x[:3]]), w, residual=torch.cat([r.repeat(times, 1), r[:3]]), **o)
+    for a, b in zip(many, one):
+        if b is None:
+            assert a is None
+            continue
+        a, b = a.view(torch.uint8), b.view(torch.uint8)
+        assert torch.equal(a[-3:], b[:3])
+        for i in range(times):
+            assert torch.equal(a[i << 20:(i + 1) << 20], b), i
