@@ -183,36 +183,39 @@ MoeSpace moe_space(int T, int k, int H, int I, int E, int fmt) {
 
 // Whether each pair reads its expert's weights for itself (two launches)
 // instead of sorting (four).  Sorting saves the weights of the experts that
-// several pairs share, and its tiles stream at 5.9 TB/s against 5.0, for about
-// 14 us more.  Both sides measured from 1 to 20 tokens at (E, k, H, I) =
-// (128, 4, 2880, 2880), (32, 4, 2880, 1440) and (256, 8, 2048, 512): 1 token 17,
-// 11 and 10 us against 32, 26 and 22; they cross at 20-24, 24-32 and 112-128
-// pairs, where this does.
+// several pairs share, and its tiles stream at 5.9 TB/s against 5.0 (4.5 in e4m3,
+// whose rows are taken apart pair by pair), for about 14 us more.  Both sides measured
+// from 1 to 20 tokens at (E, k, H, I) = (128, 4, 2880, 2880), (32, 4, 2880, 1440) and
+// (256, 8, 2048, 512): 1 token of the first 16.4 us against 30.7 (e2m1 14.5, 27.7);
+// they cross at 16-20, 20-24 and 112-120 pairs (20, 24 and 128-160), where this does.
 static bool moe_unsorted(const MoeArgs &a) {
     const double P = (double)a.T * a.k, E = a.E;
     const double shared = E * (1.0 - pow(1.0 - 1.0 / E, P));        // experts that P pairs meet
     const double expert_us = 3.0 * a.H * a.I * 17 / 32 * 1e-6;      // at 1 TB/s
-    return P * expert_us / 5.0 - shared * expert_us / 5.9 < 14.0 &&
+    return P * expert_us / (a.fmt == kMxE4m3 ? 4.5 : 5.0) - shared * expert_us / 5.9 < 14.0 &&
            mxfp4_row_lds_bytes(a.fmt, a.H) <= kMxRowMaxLds &&
            a.k * mxfp4_row_lds_bytes(a.fmt, a.I) <= kMxRowMaxLds;
 }
 
-// Measured at the same sizes from 1 to 1024 tokens: 16 and 32 rows differ by a
-// few per cent up to 4 pairs an expert, 32 wins by 3-7 % to 16, and 64 from
-// about 32 on (128 experts: 394 against 379 us there).
-int moe_tile_rows(int T, int k, int E) {
+// Measured at the same sizes from 1 to 1024 tokens of e2m1: 16 and 32 rows differ
+// by a few per cent up to 4 pairs an expert, 32 wins by 3-7 % to 16, and 64 from
+// about 32 on (128 experts: 394 against 379 us there).  e4m3, in us at 16, 32 and
+// 64 rows: 5 pairs an expert (32 of 2880 x 1440) 47, 51, 69; 12 50, 54, 74; 16 (128
+// of 2880 x 2880) 342, 307, 356; 64 647, 537, 585; 128 1074, 869, 916; 512 513, 415,
+// 416; 2048 1987, 1636, 1586.
+int moe_tile_rows(int T, int k, int E, int fmt) {
     const long avg = (long)T * k / E;
+    if (fmt == kMxE4m3) return avg <= 14 ? 16 : avg <= 640 ? 32 : 64;
     return avg <= 4 ? 16 : avg <= 24 ? 32 : 64;
 }
 
-// Whether the tiles of some experts may be taller than 64 rows: with enough of
-// them that fewer, longer workgroups still fill the card.  2048 and 4096 tokens
-// of 128 experts of 2880 x 2880, 4 a token: 460 -> 451 and 637 -> 620 us (e2m1 581
-// -> 546); 512 of 64 of 4096 x 1408, 8 a token: 162 -> 157, but 256: 130 -> 131;
-// 1024 of 32 of 2880 x 1440: 104 -> 114.
+// Whether the tiles of some experts may be taller than 64 rows: in e2m1, with
+// enough of them that fewer, longer workgroups still fill the card.  4096 tokens of
+// 128 experts of 2880 x 2880, 4 a token: 581 -> 546 us; 512 of 64 of 4096 x 1408, 8 a
+// token: 162 -> 157, but 256: 130 -> 131; 1024 of 32 of 2880 x 1440: 104 -> 114.
 static int moe_tall(const MoeArgs &a, int rows) {
     const long tiles = (long)a.T * a.k / 64 + a.E / 2;
-    return rows == 64 && tiles * ((a.I + 127) / 128) >= 4 * kNumCusMI355X;
+    return a.fmt == kMxE2m1 && rows == 64 && tiles * ((a.I + 127) / 128) >= 4 * kNumCusMI355X;
 }
 
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
@@ -223,7 +226,7 @@ int launch_moe(const MoeArgs &a, void *workspace, hipStream_t stream) {
     const MoeSpace s = moe_space(a.T, a.k, a.H, a.I, a.E, a.fmt);
     uint8_t *b = (uint8_t *)workspace;
     if (moe_unsorted(a)) return launch_moe_rows(a, b + s.h, b + s.he, stream);
-    const int P = a.T * a.k, rows = moe_tile_rows(a.T, a.k, a.E);
+    const int P = a.T * a.k, rows = moe_tile_rows(a.T, a.k, a.E, a.fmt);
     const int tiles = moe_max_tiles(P, a.E, rows);
     const MoeLists lists{(const MoeTile *)(b + s.tiles), (const int *)(b + s.count),
                          (const int *)(b + s.pairs), moe_tall(a, rows)};

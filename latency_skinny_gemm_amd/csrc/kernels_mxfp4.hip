@@ -218,21 +218,17 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
     // before their products, in two sets.
     constexpr int U = AHEAD ? AHEAD : 1;  // steps a barrier
     constexpr int FS = AHEAD ? 2 * U : 1;
-    // blocks of 16 rows whose fragments are held at once: with all six of a tall
-    // tile in e4m3 66 registers spill
-    constexpr int MG = MT > 4 && FX == kMxE4m3 ? 2 : MT;
-    static_assert(MG == MT || !AHEAD, "fragments ahead are of all rows");
-    u32x4 xf[FS][MG][FX == kMxE4m3 ? 2 : 1];
-    unsigned xsc[FS][MG], wsc[FS][NBW];
+    u32x4 xf[FS][MT][FX == kMxE4m3 ? 2 : 1];
+    unsigned xsc[FS][MT], wsc[FS][NBW];
     // slot s; chunk: of the scale bytes in LDS; wchunk: of all chunks so far
-    auto read_frags = [&](int f, int s, int chunk, int wchunk, int m0 = 0) {
+    auto read_frags = [&](int f, int s, int chunk, int wchunk) {
         const unsigned char *base = lds_raw + s * SLOT;
 #pragma unroll
-        for (int b = 0; m0 == 0 && b < NBW; ++b)
+        for (int b = 0; b < NBW; ++b)
             wsc[f][b] = *reinterpret_cast<const unsigned *>(wscales + (wchunk & (WC - 1)) * (4 * NBW * 256) + b * 256 + lane * 4);
 #pragma unroll
-        for (int m = 0; m < MG; ++m) {
-            const int r = (m0 + m) * 16 + fr;
+        for (int m = 0; m < MT; ++m) {
+            const int r = m * 16 + fr;
             const unsigned char *rp = base + r * RB;
             xsc[f][m] = *reinterpret_cast<const unsigned *>(scales + r * sstride + chunk * 16 + (s % 4) * 4);
             xf[f][m][0] = *reinterpret_cast<const u32x4 *>(rp + ((fg ^ piece_key<CPR>(fr)) * 16));
@@ -240,13 +236,11 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
                 xf[f][m][1] = *reinterpret_cast<const u32x4 *>(rp + (((4 + fg) ^ piece_key<CPR>(fr)) * 16));
         }
     };
-    auto multiply = [&](int f, int s, int m, int b, int m0) {
-        const u32x4 p = xf[f][m][0], q = xf[f][m][FX == kMxE4m3 ? 1 : 0], v = w[s][b];
-        const i32x8 x8 = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)q.x, (int)q.y, (int)q.z, (int)q.w}
-                                       : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+    auto multiply = [&](const i32x8 &x8, int f, int s, int m, int b) {
+        const u32x4 v = w[s][b];
         const i32x8 w8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
         const int sx = (int)(xsc[f][m] >> (8 * fg)), sw = (int)wsc[f][b];
-        f32x4 &d = acc[m0 + m][b];
+        f32x4 &d = acc[m][b];
         if (s % 4 == 0) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 0, sw, 0, sx);
         if (s % 4 == 1) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 1, sw, 0, sx);
         if (s % 4 == 2) d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x8, d, kMxE2m1, FX, 2, sw, 0, sx);
@@ -286,19 +280,40 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
             // A group's products, then the loads into the registers they leave:
             // free to move, the loads would go first, into as many more.
 #pragma unroll
-            for (int s = s0; s < s0 + U; ++s)
+            for (int s = s0; s < s0 + U; ++s) {
+                if constexpr (!AHEAD) read_frags(0, s, (cb + s) / 4 % SC, (cb + s) / 4);
+                if constexpr (FX == kMxE4m3) {
+                    // a row block's parts at a time: those of all are too many registers
 #pragma unroll
-                for (int m0 = 0; m0 < MT; m0 += MG) {
-                    if constexpr (!AHEAD) read_frags(0, s, (cb + s) / 4 % SC, (cb + s) / 4, m0);
+                    for (int m = 0; m < MT; ++m) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        i32x8 large, small;
+                        mx_parts8(xf[s % FS][m][0], xf[s % FS][m][1], large, small);
+#pragma unroll
+                        for (int b = 0; b < NBW; ++b) multiply(small, s % FS, s, m, b);
+#pragma unroll
+                        for (int b = 0; b < NBW; ++b) {
+                            multiply(large, s % FS, s, m, b);
+                            if (m == MT - 1) {
+                                __builtin_amdgcn_sched_barrier(0);
+                                issue_w(s, nb + s, (nb + s) / 4, b);
+                            }
+                        }
+                    }
+                } else {
 #pragma unroll
                     for (int b = 0; b < NBW; ++b) {
                         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int m = 0; m < MG; ++m) multiply(s % FS, s, m, b, m0);
+                        for (int m = 0; m < MT; ++m) {
+                            const u32x4 p = xf[s % FS][m][0];
+                            multiply(i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0}, s % FS, s, m, b);
+                        }
                         __builtin_amdgcn_sched_barrier(0);
-                        if (m0 + MG == MT) issue_w(s, nb + s, (nb + s) / 4, b);
+                        issue_w(s, nb + s, (nb + s) / 4, b);
                     }
                 }
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         // The sums are "used" here: with their next use behind a branch, the
@@ -403,7 +418,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     const int height = MODE == kDense ? MT * 16 : moe_tile_height(own.rows, MT * 16, a.tall);
     const int nt = (own.rows + height - 1) / height, local = at - own.first * a.col_tiles;
     const int ct = local / nt, rt = local - ct * nt;
-    if constexpr (MODE != kDense && MT == 4) {
+    if constexpr (MODE != kDense && MT == 4 && FX == kMxE2m1) {
         if (height > MT * 16) {
             if (nt == 1)
                 mxfp4_tile<6, NBW, FX, MODE, SL, AHEAD, kCacheStream>(a, own, ct, rt);
@@ -423,7 +438,7 @@ namespace {
 // tiles: row tiles (grouped products: a bound on them).
 template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 int go(TileArgs a, int tiles, hipStream_t stream) {
-    constexpr int TALL = MODE != kDense && MT == 4 ? 6 : MT;
+    constexpr int TALL = MODE != kDense && MT == 4 && FX == kMxE2m1 ? 6 : MT;
     const size_t bytes = tile_lds_bytes(TALL, NBW, FX, SL, tile_scale_chunks(mxfp4_chunks(a.K), SL));
     constexpr size_t most = tile_lds_bytes(TALL, NBW, FX, SL, tile_scale_most(SL));
     static_assert(most <= 160 * 1024 - 256, "LDS of a workgroup");
@@ -441,41 +456,77 @@ int go(TileArgs a, int tiles, hipStream_t stream) {
     return (int)hipGetLastError();
 }
 
-// rows: 16, 32 or 64 a tile.  NB: column groups a wave for 64 rows, and for fewer.
-template <int MODE, int FX, int NB64, int NB>
+// rows: 16, 32 or 64 a tile.  NB16, NB32, NB64: column groups a wave for each.
+template <int MODE, int FX, int NB16, int NB32, int NB64>
 int pick(const TileArgs &a, int rows, int tiles, hipStream_t stream) {
-    if (rows <= 16) return go<1, NB, FX, MODE, 4, 0>(a, tiles, stream);
-    if (rows <= 32) return go<2, NB, FX, MODE, 4, 0>(a, tiles, stream);
+    if (rows <= 16) return go<1, NB16, FX, MODE, 4, 0>(a, tiles, stream);
+    if (rows <= 32) return go<2, NB32, FX, MODE, 4, 0>(a, tiles, stream);
     return go<4, NB64, FX, MODE, 4, 0>(a, tiles, stream);
 }
 
-// The smallest tile whose workgroups are at most one a CU.  A CU takes in
-// 14-17 bytes a clock of these operands however many workgroups it holds and
-// however deep their rings are, so a workgroup's time follows its bytes a step:
-// at K = 7168 12.3, 15.0, 19.2 and 30 us (quantising included) for tiles of
-// 16 x 64, 32 x 64, 32 x 128 and 64 x 128 while they fit, and twice that in a
-// second round (M = 128, N = 4096: 19.0, 15.7, 19.8, 29).
+// Rows of e2m1: the smallest tile whose workgroups are at most one a CU.  A CU
+// takes in 14-17 bytes a clock of these operands however many workgroups it holds
+// and however deep their rings are, so a workgroup's time follows its bytes a step.
+//
+// Rows of e4m3: taking the rows' parts costs a wave as much as its products, and
+// fewer rows by more columns a wave have fewer of them.  Below one workgroup a CU
+// steps ahead pay; above it workgroups that alternate on a CU do, up to three.
+// Measured (us, quantising included; 16 x 64, 16 x 128 ahead, 16 x 128, 32 x 128,
+// 32 x 256; K = 7168, below 2880):
+//   64 x 4096    18.4  19.3  20.9  27.9  37.4     128 x 4096   23.7  20.6  21.6  28.7  37.7
+//   256 x 4096   36.3  28.9  28.0  30.2  39.1     512 x 4096   65.7  50.4  45.9  40.2  41.2
+//   128 x 2880   12.6  11.9  12.1  16.0  21.4     512 x 2880   27.0  20.9  19.7  21.8  23.1
+// 512 x 8192 x 4096: 75.7, 53.5, 49.9, 43.0 and 39.6.  Tiles of 64 rows: 49.5 at
+// 512 x 4096.
+enum { kTile16x64, kTile16x128, kTile16x128Ring, kTile32x128Ring, kTile32x256Ring, kTile32x64, kTile32x128, kTile64x128 };
+
+int dense_tile(int M, int N, int fmt) {
+    const long c64 = (N + 63) / 64, c128 = (N + 127) / 128;
+    const long r16 = (M + 15) / 16, r32 = (M + 31) / 32;
+    constexpr long cus = kNumCusMI355X;
+    if (r16 * c64 <= cus) return kTile16x64;
+    if (fmt == kMxE4m3)
+        return r16 * c128 <= cus       ? kTile16x128
+               : r16 * c128 <= 3 * cus ? kTile16x128Ring
+               : r32 * c128 <= 3 * cus ? kTile32x128Ring
+                                       : kTile32x256Ring;
+    return r32 * c64 <= cus ? kTile32x64 : r32 * c128 <= cus ? kTile32x128 : kTile64x128;
+}
+
 template <int FX>
 int dense(const TileArgs &a, hipStream_t stream) {
-    const long c64 = (a.N + 63) / 64, c128 = (a.N + 127) / 128;
-    const int r16 = (a.M + 15) / 16, r32 = (a.M + 31) / 32, r64 = (a.M + 63) / 64;
-    if (r16 * c64 <= kNumCusMI355X) return go<1, 1, FX, kDense, 8, 2>(a, r16, stream);
-    if (r32 * c64 <= kNumCusMI355X) return go<2, 1, FX, kDense, 8, 2>(a, r32, stream);
-    if (r32 * c128 <= kNumCusMI355X) return go<2, 2, FX, kDense, 8, 2>(a, r32, stream);
-    // two steps a barrier spill with e4m3 fragments of 64 rows
-    return go<4, 2, FX, kDense, 8, FX == kMxE4m3 ? 1 : 2>(a, r64, stream);
+    const int r16 = (a.M + 15) / 16, r32 = (a.M + 31) / 32, tile = dense_tile(a.M, a.N, FX);
+    if (tile == kTile16x64) return go<1, 1, FX, kDense, 8, 2>(a, r16, stream);
+    if constexpr (FX == kMxE4m3) {
+        if (tile == kTile16x128) return go<1, 2, FX, kDense, 8, 2>(a, r16, stream);
+        if (tile == kTile16x128Ring) return go<1, 2, FX, kDense, 4, 0>(a, r16, stream);
+        if (tile == kTile32x128Ring) return go<2, 2, FX, kDense, 4, 0>(a, r32, stream);
+        return go<2, 4, FX, kDense, 4, 0>(a, r32, stream);
+    } else {
+        if (tile == kTile32x64) return go<2, 1, FX, kDense, 8, 2>(a, r32, stream);
+        if (tile == kTile32x128) return go<2, 2, FX, kDense, 8, 2>(a, r32, stream);
+        return go<4, 2, FX, kDense, 8, 2>(a, (a.M + 63) / 64, stream);
+    }
 }
 
 }  // namespace
 
-// As dense() picks them.
-double mxfp4_tile_time(int M, int N, int K) {
-    const long c64 = (N + 63) / 64, c128 = (N + 127) / 128, r16 = (M + 15) / 16, r32 = (M + 31) / 32;
-    const double us = 5.3 + 9.5e-4 * K;
-    if (r16 * c64 <= kNumCusMI355X) return us;
-    if (r32 * c64 <= kNumCusMI355X) return 1.25 * us;
-    if (r32 * c128 <= kNumCusMI355X) return 1.6 * us;
-    return 2.5 * us * (double)(((M + 63) / 64 * c128 + kNumCusMI355X - 1) / kNumCusMI355X);
+// Of the tile that dense() picks: straight lines in K through 392 points a format.
+double mxfp4_tile_time(int M, int N, int K, int fmt) {
+    const long c128 = (N + 127) / 128;
+    switch (dense_tile(M, N, fmt)) {
+    case kTile16x64: return fmt == kMxE4m3 ? 5.2 + 1.65e-3 * K : 5.2 + 1.03e-3 * K;
+    case kTile16x128: return 6.3 + 1.97e-3 * K;
+    case kTile16x128Ring: return (M + 15) / 16 * c128 <= 2 * kNumCusMI355X ? 6.1 + 3.0e-3 * K : 7.6 + 4.1e-3 * K;
+    case kTile32x128Ring: return 8.2 + 4.9e-3 * K;
+    case kTile32x256Ring: return 14 + 6.6e-3 * K;
+    case kTile32x64: return 6.6 + 1.2e-3 * K;
+    case kTile32x128: return 7.0 + 1.64e-3 * K;
+    default: {
+        const double rounds = (double)(((M + 63) / 64 * c128 + kNumCusMI355X - 1) / kNumCusMI355X);
+        return 5.0 + 5e-4 * K + rounds * (4.6 + 1.41e-3 * K);
+    }
+    }
 }
 
 int launch_mxfp4(const Mxfp4Args &p, hipStream_t stream) {
@@ -512,8 +563,8 @@ int launch_moe_gate_up(const MoeArgs &m, const MoeLists &s, const uint8_t *xq, c
     a.pairs = s.pairs;
     a.top = m.k;
     a.tall = s.tall;
-    return m.fmt == kMxE4m3 ? pick<kGateUp, kMxE4m3, 4, 4>(a, rows, tiles, stream)
-                            : pick<kGateUp, kMxE2m1, 4, 4>(a, rows, tiles, stream);
+    return m.fmt == kMxE4m3 ? pick<kGateUp, kMxE4m3, 4, 4, 4>(a, rows, tiles, stream)
+                            : pick<kGateUp, kMxE2m1, 4, 4, 4>(a, rows, tiles, stream);
 }
 
 int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const uint8_t *he,
@@ -532,10 +583,11 @@ int launch_moe_down(const MoeArgs &m, const MoeLists &s, const uint8_t *h, const
     a.pairs = s.pairs;
     a.top = m.k;
     a.tall = s.tall;
-    // Wide column tiles halve what the rows cost (2048 tokens: 170 -> 161 us);
-    // with few rows more, narrower workgroups stream better (40: 32 -> 30 us).
-    return m.fmt == kMxE4m3 ? pick<kDown, kMxE4m3, 4, 2>(a, rows, tiles, stream)
-                            : pick<kDown, kMxE2m1, 4, 2>(a, rows, tiles, stream);
+    // Wide column tiles halve what the rows cost (e2m1, 2048 tokens: 170 -> 161 us;
+    // e4m3, both products of 1024 tokens of 32 experts of 2880 x 1440: 133 -> 128);
+    // with few rows more, narrower workgroups stream better (40: 32 -> 30).
+    return m.fmt == kMxE4m3 ? pick<kDown, kMxE4m3, 2, 4, 4>(a, rows, tiles, stream)
+                            : pick<kDown, kMxE2m1, 2, 2, 4>(a, rows, tiles, stream);
 }
 
 }  // namespace skg

@@ -302,22 +302,25 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                 const uint8_t *rp = row_lds + rl * rs + sl * CB + fg * 16;
                 const u32x4 p = *reinterpret_cast<const u32x4 *>(rp);
                 const u32x4 x1 = *reinterpret_cast<const u32x4 *>(rp + (FX == kMxE4m3 ? 64 : 0));
-                const i32x8 xq = FX == kMxE4m3 ? i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w}
-                                               : i32x8{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0};
+                i32x8 xq{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0}, xs;
+                if constexpr (FX == kMxE4m3) mx_parts8(p, x1, xq, xs);
                 const int xe = row_sc[rl * (KS * 4) + sl * 4 + fg];
+                auto multiply = [&](const i32x8 &wf, int sc, f32x4 d) {
+                    if constexpr (FX == kMxE4m3)
+                        d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xs, d, kMxE2m1, FX, 0, sc, 0, xe);
+                    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xq, d, kMxE2m1, FX, 0, sc, 0, xe);
+                };
 #pragma unroll
                 for (int b = 0; b < R; ++b) {
                     const u32x4 q = w[i][b];
                     const i32x8 wf{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
                     const int sc = (int)(ws[i][b] >> (8 * (s & 3)));
                     if constexpr (MODE == kRowsDown) {
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, xq, f32x4{0.f, 0.f, 0.f, 0.f}, kMxE2m1, FX, 0, sc, 0, xe);
+                        const f32x4 d = multiply(wf, sc, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                         for (int c = 0; c < 4; ++c) acc[m][b][c] = __builtin_fmaf(wt[i], expert[i] >= 0 ? d[c] : 0.0f, acc[m][b][c]);
                     } else {
-                        acc[m][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            wf, xq, acc[m][b], kMxE2m1, FX, 0, sc, 0, xe);
+                        acc[m][b] = multiply(wf, sc, acc[m][b]);
                     }
                 }
             }

@@ -67,7 +67,7 @@ int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
 constexpr int kMxRowsBf16 = 16, kMxRowsCodes = 32;
 int launch_mxfp4_rows(const Mxfp4Args &a, int blocks, hipStream_t stream);
 // Time in us of the tiles, quantising included.
-double mxfp4_tile_time(int M, int N, int K);
+double mxfp4_tile_time(int M, int N, int K, int fmt);
 
 // ---------------------------------------------------------------- experts
 // Pairs (token, choice) sorted by expert, and the row tiles of the grouped
@@ -81,7 +81,7 @@ struct MoeTile {
     int first;
 };
 // Rows a tile may hold, by the average number of pairs an expert gets.
-int moe_tile_rows(int T, int k, int E);
+int moe_tile_rows(int T, int k, int E, int fmt);
 // The height of the tiles of an expert with n rows: 96 (tall) instead of 64 where
 // that makes fewer of them, and so fewer readings of its weights.
 #ifdef __HIPCC__
