@@ -256,7 +256,11 @@ int skinny_gemm_bf16_planned(const void *x, const void *W, const void *bias, voi
  * M*K e4m3 codes.  max_K = 0 reserves no such room (enough for every other
  * entry point).  Allocates (hipMalloc) and zeroes the tile counters; call it
  * before graph capture.  Outside capture a call that needs more grows the
- * workspace itself; during capture it returns SKG_ERR_WORKSPACE instead.
+ * workspace itself; during capture it returns SKG_ERR_WORKSPACE instead.  A
+ * workspace grows by half its size at least, and what it replaces stays
+ * allocated until skinny_gemm_release_all (a graph may still use it): at most
+ * 4.5 times the largest request in all, and no more than the largest one if that
+ * is reserved first.
  * SKG_ERR_INVALID_ARG if max_M, max_N or max_S is below 1, max_M exceeds
  * SKG_MAX_M, max_S exceeds 256, max_K is negative, or max_K * 1024 bytes
  * reaches 2 GiB. */

@@ -146,7 +146,8 @@ int skinny_moe_mxfp4(const void *x, const int *ids, const float *weights, const 
 /* Workspace of `stream` for skinny_gemm_mxfp4 calls of up to max_M x max_K
  * (M, K; any N) and skinny_moe_mxfp4 calls of up to (max_T, k, H, I, E); either set of
  * sizes may be 0.  As skinny_gemm_reserve: before graph capture, and a larger
- * call outside capture grows it by itself. */
+ * call outside capture grows it by itself, as told there.  The experts take about
+ * T * (k * (4 * H + I) + H) bytes of it; a server reserves for its longest prompt. */
 int skinny_moe_reserve(int max_M, int max_K, int max_T, int k, int H, int I, int E,
                        hipStream_t stream);
 

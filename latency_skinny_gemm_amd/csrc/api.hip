@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <vector>
@@ -90,13 +91,22 @@ long stream_owner(hipStream_t stream) {
 // on the null stream, which a non-blocking stream does not wait for, so the
 // first kernel could read uninitialised counters and no workgroup of a tile
 // would see itself arrive last.
+//
+// A graph may still use what is replaced here, so that stays allocated.  A new
+// buffer is half as large again as the old one at least: requests that creep up
+// then leave no more than twice the last buffer behind, not one for every size.
 int grow(Workspace &w, size_t floats, size_t tickets, hipStream_t stream) {
     if (floats > w.ws_floats) {
         float *p = nullptr;
-        if (hipMalloc((void **)&p, floats * sizeof(float)) != hipSuccess) return SKG_ERR_HIP;
+        size_t size = std::max(floats, w.ws_floats + w.ws_floats / 2);
+        if (hipMalloc((void **)&p, size * sizeof(float)) != hipSuccess) {
+            (void)hipGetLastError();  // no room for more than was asked for
+            size = floats;
+            if (hipMalloc((void **)&p, size * sizeof(float)) != hipSuccess) return SKG_ERR_HIP;
+        }
         if (w.ws) g_retired.push_back(Retired{w.device, w.ws});
         w.ws = p;
-        w.ws_floats = floats;
+        w.ws_floats = size;
         g_generation.fetch_add(1, std::memory_order_acq_rel);
     }
     if (tickets > w.n_tickets) {
