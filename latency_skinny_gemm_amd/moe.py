@@ -120,7 +120,15 @@ def _codes(name, q, e8m0, fmt):
     return lead, K
 
 
-_rows = math.prod
+def _count(n):
+    """n, refused past 31 bits: ctypes would pass its low half on."""
+    if n >> 31:
+        _c._check(_c.ERR_UNSUPPORTED, f"a size of {n}")
+    return n
+
+
+def _rows(lead):
+    return _count(math.prod(lead))
 
 
 def quant_mx(x, format="e4m3", stream=None):
@@ -210,6 +218,7 @@ def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=1, renorm
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
+    _count(max(T, k, groups, top_groups))
     if bias is not None:
         _tensor("bias", bias, _F32, (E,))
     o = RouteOptions(sc, k, groups, top_groups, 1 if renormalize else 0, factor)
@@ -231,6 +240,7 @@ def mxfp4_pack(q, e8m0, stream=None):
     if len(lead) not in (1, 2):
         raise ValueError("q must be [N, K/2] or [E, N, K/2]")
     E, N = (None, lead[0]) if len(lead) == 1 else lead
+    _count(max(lead))
     L = _c._load()
     n = L.skinny_mxfp4_packed_bytes(E or 1, N, K)
     if n == 0:
@@ -257,7 +267,7 @@ def gemm_mxfp4(x, w, xe=None, x_format="e4m3", bias=None, out_dtype=torch.bfloat
         K = x.shape[1]
     else:
         _, K = _codes("x", x, xe, fmt)
-    M, N = x.shape[0], w.N
+    M, N = _count(x.shape[0]), w.N
     if K != w.K:
         raise ValueError(f"x has K={K}, w has K={w.K}")
     if bias is not None:
@@ -294,6 +304,7 @@ def moe_mxfp4(x, ids, weights, w13, w2, x_format="e4m3", out=None, stream=None):
         if not isinstance(w, MxfpWeights) or w.E is None:
             raise TypeError(f"{name} must be mxfp4_pack of [E, N, K] weights")
     (T, H), k, I, E = x.shape, ids.shape[1], w2.K, w2.E
+    _count(max(T, k))
     if w13.E != E or w13.N != 2 * I or w13.K != H or w2.N != H:
         raise ValueError(f"w13 must be [E, 2I, H] and w2 [E, H, I] with H={H}, got {w13} and {w2}")
     if out is None:
