@@ -299,6 +299,26 @@ extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weig
     return status(launch_moe(a, ws, stream));
 }
 
+// For the tests: the way a product takes (its blocks of rows, 0 for tiles, with
+// their rows, whether they are quantised before, and the tile), and the experts'.
+extern "C" int skg_mxfp4_way(int M, int N, int K, int format, int codes, int *rows, int *first, int *tile) {
+    const Mxfp4Way way = mxfp4_way(M, N, K, format, codes != 0);
+    *rows = way.blocks ? (M + way.blocks - 1) / way.blocks : 0;
+    *first = way.quantise_first;
+    *tile = dense_tile(M, N, format);
+    return way.blocks;
+}
+extern "C" int skg_moe_way(int T, int k, int H, int I, int E, int format) {
+    MoeArgs a{};
+    a.fmt = format;
+    a.T = T;
+    a.k = k;
+    a.H = H;
+    a.I = I;
+    a.E = E;
+    return moe_way(a);
+}
+
 extern "C" int skinny_moe_reserve(int max_M, int max_K, int max_T, int k, int H, int I, int E,
                                   hipStream_t stream) {
     int rc = check_linear(max_M, 0, max_K ? max_K : 32);

@@ -218,6 +218,12 @@ static int moe_tall(const MoeArgs &a, int rows) {
     return a.fmt == kMxE2m1 && rows == 64 && tiles * ((a.I + 127) / 128) >= 4 * kNumCusMI355X;
 }
 
+int moe_way(const MoeArgs &a) {
+    if (moe_unsorted(a)) return 0;
+    const int rows = moe_tile_rows(a.T, a.k, a.E, a.fmt);
+    return moe_tall(a, rows) ? 96 : rows;
+}
+
 size_t moe_workspace_bytes(int T, int k, int H, int I, int E, int fmt) {
     return moe_space(T, k, H, I, E, fmt).bytes;
 }

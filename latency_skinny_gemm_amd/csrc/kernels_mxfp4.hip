@@ -478,7 +478,9 @@ int pick(const TileArgs &a, int rows, int tiles, hipStream_t stream) {
 //   128 x 2880   12.6  11.9  12.1  16.0  21.4     512 x 2880   27.0  20.9  19.7  21.8  23.1
 // 512 x 8192 x 4096: 75.7, 53.5, 49.9, 43.0 and 39.6.  Tiles of 64 rows: 49.5 at
 // 512 x 4096.
-enum { kTile16x64, kTile16x128, kTile16x128Ring, kTile32x128Ring, kTile32x256Ring, kTile32x64, kTile32x128, kTile64x128 };
+enum DenseTile { kTile16x64, kTile16x128, kTile16x128Ring, kTile32x128Ring, kTile32x256Ring, kTile32x64, kTile32x128, kTile64x128 };
+
+}  // namespace
 
 int dense_tile(int M, int N, int fmt) {
     const long c64 = (N + 63) / 64, c128 = (N + 127) / 128;
@@ -492,6 +494,8 @@ int dense_tile(int M, int N, int fmt) {
                                        : kTile32x256Ring;
     return r32 * c64 <= cus ? kTile32x64 : r32 * c128 <= cus ? kTile32x128 : kTile64x128;
 }
+
+namespace {
 
 template <int FX>
 int dense(const TileArgs &a, hipStream_t stream) {

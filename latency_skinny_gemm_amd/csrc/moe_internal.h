@@ -66,6 +66,8 @@ int launch_mxfp4(const Mxfp4Args &a, hipStream_t stream);
 // quantised on the way.
 constexpr int kMxRowsBf16 = 16, kMxRowsCodes = 32;
 int launch_mxfp4_rows(const Mxfp4Args &a, int blocks, hipStream_t stream);
+// The tile that a product of this size takes, as dense() lists them.
+int dense_tile(int M, int N, int fmt);
 // Time in us of the tiles, quantising included.
 double mxfp4_tile_time(int M, int N, int K, int fmt);
 
@@ -123,6 +125,8 @@ constexpr size_t mxfp4_row_lds_bytes(int fmt, int K) {
     return (size_t)mxfp4_steps(K) * ((fmt == SKG_MX_E4M3 ? 128 : 64) + 4) + kRowLdsPad;
 }
 constexpr size_t kMxRowMaxLds = 124 * 1024;
+// How a call is done: 0 unsorted, else the height of its tiles (96: some of them).
+int moe_way(const MoeArgs &a);
 // Few pairs, unsorted: h and he have a row per pair; combines as well.
 int launch_moe_rows(const MoeArgs &m, uint8_t *h, uint8_t *he, hipStream_t stream);
 // Bytes of workspace the experts need.
