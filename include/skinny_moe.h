@@ -62,8 +62,8 @@ int skinny_dequant_mx(const void *q, const void *e8m0, int format, void *out, in
 
 /* s = x + residual (fp32; residual NULL: s = x), residual_out = bf16(s),
  * y = s / sqrt(mean_k(s^2) + eps) * weight, in fp32, rounded once to the
- * output's type.  The norm is of the fp32 sum, not of its bf16 rounding.  Rows
- * whose squares leave fp32's range, at either end, have them added up in fp64.
+ * output's type.  The norm is of the fp32 sum, not of its bf16 rounding.  The
+ * squares are added up in fp64, so that rows of any size have their norm.
  * x, residual, residual_out, (bf16 out) [M, K]; weight bf16 [K]; scale: one
  * fp32 (SKG_NORM_E4M3 only, else NULL); e8m0 [M, K/32] (SKG_NORM_MX only,
  * else NULL).  residual and residual_out are given together or not at all, and

@@ -8,10 +8,11 @@
 // neighbouring lanes of a quad.
 //
 // The factor of a row errs coherently in all its codes, and each rounding of a
-// value moves it across more ties.  So the waves' sums are added in fp64, the
-// factor is carried in two fp32 numbers, and a value goes to its 8-bit code as if
-// it had not been rounded before.  Forty drawn calls had 5 codes other than the
-// exact ones so, against 40 by rounding every step.
+// value moves it across more ties.  So the squares are added up in fp64 (no square
+// leaves its range either), the factor is carried in two fp32 numbers, and a value
+// goes to its 8-bit code as if it had not been rounded before.  Forty drawn calls had
+// no code other than the exact one so; with sums in fp32 6, and 39 by rounding
+// every step.  It takes 2-5 % of the time.
 //
 // Many rows are bound by HBM: 8192 x 7168 with a residual to MX moves 411 MB in
 // 79 us, 5.2 TB/s (a copy on this card: 4.7).  One row takes 3.6 us: a launch,
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 8) rmsnorm_kernel(NormA
     const size_t row0 = (size_t)row * a.K;
     constexpr int N = V > 0 ? V : 1;
     float s[N][8];
-    float sq = 0.0f;
+    double sq = 0.0;
     const int nv = V > 0 ? V : (k8 + TPR - 1) / TPR;
 #pragma unroll
     for (int v = 0; v < nv; ++v) {
@@ -187,49 +188,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 8) rmsnorm_kernel(NormA
         for (int j = 0; j < 8; ++j) sv[j] = 0.0f;
         if (i < k8) norm_load(a, row0, i, sv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(sv[j], sv[j], sq);
+        for (int j = 0; j < 8; ++j) sq = __builtin_fma((double)sv[j], (double)sv[j], sq);
     }
-    sq = wave_sum(sq);
-    double total = sq;
+    sq = wave_sum64(sq);
     if constexpr (TPR > 64) {
-        __shared__ float part[TPR / 64];
+        __shared__ double part[TPR / 64];
         if ((threadIdx.x & 63) == 0) part[threadIdx.x / 64] = sq;
         __syncthreads();
         // every lane of a row of 16 adds the same up to 16 partial sums
-        total = (threadIdx.x & 15) < TPR / 64 ? (double)part[threadIdx.x & 15] : 0.0;
-        total = row16_sum(total);
+        sq = row16_sum((threadIdx.x & 15) < TPR / 64 ? part[threadIdx.x & 15] : 0.0);
     }
-    double mean = __builtin_fma(total, a.inv_k, (double)a.eps);
-    // Squares past either end of fp32 (values above 2^60, or rows of tiny ones with
-    // an eps as tiny): the sum again in fp64, and the row moved by the power of two
-    // that leaves its mean square near one.  The same in all of a row's lanes.
+    double mean = __builtin_fma(sq, a.inv_k, (double)a.eps);
+    // Past either end of what the factor's fp32 takes the row is moved by the power
+    // of two that leaves its mean square near one; 0, infinite and NaN stay.
     float move = 1.0f;
-    if (__builtin_expect(!(mean >= 0x1p-70 && total <= 0x1p120), 0)) {
-        double wide = 0.0;
-#pragma unroll
-        for (int v = 0; v < nv; ++v) {
-            const int i = t + v * TPR;
-            float(&sv)[8] = s[V > 0 ? v : 0];
-            if constexpr (V == 0) {
-                if (i >= k8) continue;
-                norm_load(a, row0, i, sv);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) wide = __builtin_fma((double)sv[j], (double)sv[j], wide);
-        }
-        wide = wave_sum64(wide);
-        if constexpr (TPR > 64) {
-            __shared__ double wide_part[TPR / 64];
-            if ((threadIdx.x & 63) == 0) wide_part[threadIdx.x / 64] = wide;
-            __syncthreads();
-            wide = row16_sum((threadIdx.x & 15) < TPR / 64 ? wide_part[threadIdx.x & 15] : 0.0);
-        }
-        mean = __builtin_fma(wide, a.inv_k, (double)a.eps);
-        if (mean > 0.0 && mean <= 0x1p300) {  // else 0, infinite or NaN, as it is
-            const int n = min(max(-(ilogb(mean) / 2), -120), 120);
-            move = ldexpf(1.0f, n);
-            mean = ldexp(mean, 2 * n);
-        }
+    if (__builtin_expect(!(mean >= 0x1p-70 && mean <= 0x1p110), 0) && mean > 0.0 && mean <= 0x1p300) {
+        const int n = min(max(-(ilogb(mean) / 2), -120), 120);
+        move = ldexpf(1.0f, n);
+        mean = ldexp(mean, 2 * n);
     }
     Factor c = rsqrt_factor(mean);
     const float plain = c.hi;
