@@ -56,7 +56,7 @@ __device__ __forceinline__ int3 block_sum(int3 v, int (*lds)[3]) {
 // times from L2, 16 waves with eight loads each in flight.  Pairs whose id is
 // outside [0, E) are left out.
 //
-// 8192 pairs of 128 experts take 8.1 us, with the quantising of 2048 x 2880 in
+// 8192 pairs of 128 experts take 8.5 us, with the quantising of 2048 x 2880 in
 // the same launch, and 320 pairs of 64 experts 4.9: two passes over the ids, one
 // load after another, and the barriers between them.
 __device__ __forceinline__ void sort_pairs(const PrepArgs &a, int *hist) {

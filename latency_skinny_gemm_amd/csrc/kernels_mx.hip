@@ -3,8 +3,9 @@
 // products read their weights in.
 //
 // All three are single passes bound by HBM: 4096 x 7168 to e2m1 takes 15 us
-// (74 MB, 4.9 TB/s) and back 14 us (5.3), where a copy on this card moves 4.7;
-// 64 x 2880 takes 2.2 us, a launch and one trip to memory.  The pieces are 16
+// (74 MB, 4.9 TB/s) and back 14 us (5.4), where a copy on this card moves 4.7;
+// 64 x 2880 takes 2.2 us, a launch and one trip to memory; the layout of 128 x 2880 x
+// 2880 226 us (1.13 GB, 5.0).  The pieces are 16
 // bytes a thread and independent, so there is nothing to share or stage.
 #include "device_common.h"
 #include "internal.h"

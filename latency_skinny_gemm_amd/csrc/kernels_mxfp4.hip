@@ -92,15 +92,16 @@ constexpr size_t tile_lds_bytes(int MT, int NBW, int FX, int SL, int chunks) {
 //
 // What bounds it.  Experts, 40 tokens (64 of 4096 x 1408, 8 a token, half of them
 // held, e2m1): HBM; 54 us for the 332 MB of gate and up, 6.1 TB/s, 27 us for the
-// 172 MB of down.  2048 tokens (128 of 2880 x 2880, 4 a token, e4m3): 282 us and
-// 159 us; 4.0 and 3.6 TB/s of weights, the matrix pipes 37 % busy, 15 bytes a clock
-// into each CU with the rows: nothing alone, all of it together.  Dense,
-// 512 x 4096 x 7168 in e2m1: 19 us, 17 bytes a clock into each CU.
+// 172 MB of down.  2048 tokens (128 of 2880 x 2880, 4 a token, e4m3): 346 us and
+// 192 us; 3.3 and 2.8 TB/s of weights, the matrix pipes half busy with two
+// instructions a product, and the vector instructions that take the rows apart
+// issued between them.  Dense, 512 x 4096 x 7168: in e2m1 19 us, 17 bytes a clock
+// into each CU; in e4m3 36 us, with the parts.
 //
 // AHEAD > 0 takes that many steps a barrier and reads their fragments from LDS
 // under the products of the steps before.  That pays where a SIMD holds one
-// wave (dense, 512 x 4096 x 7168: 24.9 -> 21.3 us) and loses, for the registers
-// it takes, where it holds two or more (experts: 283 -> 324 us).
+// wave (e2m1, 512 x 4096 x 7168: 24.9 -> 21.3 us) and loses, for the registers
+// it takes, where it holds two or more (experts: by 15 %).
 //
 // CACHE: what the weights' loads ask of the caches.
 template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD, int CACHE>
@@ -398,12 +399,12 @@ __device__ __forceinline__ void mxfp4_tile(const TileArgs &a, const MoeTile &own
 }
 
 // Weights that one row tile alone reads pass the caches by: 12 % of the time of
-// 40 tokens (64 experts of 4096 x 1408, 8 a token: 113 -> 99 us) and 10 % of 512
-// tokens' (128 of 2880 x 2880, 4 a token: 328 -> 293).  For those that tiles
-// share the same loads cost 12 %: chosen tile by tile.
+// 40 tokens (64 experts of 4096 x 1408, 8 a token) and 10 % of 512 tokens' (128 of
+// 2880 x 2880, 4 a token).  For those that tiles share the same loads cost 12 %:
+// chosen tile by tile.
 //
-// Grouped tiles of 64 rows are 96 high for the experts of which that makes fewer
-// (moe_tile_height).
+// Grouped tiles of 64 e2m1 rows are 96 high for the experts of which that makes
+// fewer (moe_tile_height).
 template <int MT, int NBW, int FX, int MODE, int SL, int AHEAD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
     mxfp4_tile_kernel(TileArgs a) {

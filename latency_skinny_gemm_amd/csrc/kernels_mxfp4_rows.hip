@@ -11,13 +11,14 @@
 // that would do it.  More rows go in blocks to more workgroups, while there are
 // CUs without one: what a workgroup waits for grows with its rows.
 //
-// Measured, weights from memory: one row of 7168 by 2112 columns 4.1 us (8.0 MB
-// of weights, 2 TB/s; a launch and one load after another make most of it),
-// 16 rows 9.5 (the rows' quantising), 16 rows of e2m1 codes 5.4; 16 rows by 576
-// columns 4.9, in four blocks (in one 8.9).  Experts of
-// 2880 x 2880, one token's four: 8.7 us gate and up (35 MB, 4.1 TB/s) and 5.9
-// down (18 MB, 3.0).  Fragments loaded straight to registers, without LDS:
-// 6.9, 9.9, 6.7, 10.1 and 5.6 us.
+// Measured, weights from memory, bf16 rows to e4m3 (e2m1): one row of 7168 by 2112
+// columns 5.1 us (4.4; 8.0 MB of weights, 1.6 TB/s: a launch and one load after
+// another make most of it, and in e4m3 the rows' two parts), 16 rows 9.8 (7.6; the
+// rows' quantising), 16 rows by 576 columns 5.3 (4.5), in four blocks.  Experts of
+// 2880 x 2880, one token's four, in e4m3: 10.2 us gate and up (35 MB, 3.4 TB/s) and
+// 7.2 down (18 MB, 2.5).  Fragments loaded straight to registers, without LDS, took
+// 1.7 times as long for the one row; the parts of several steps taken before the
+// weights arrive 7 % longer for the token, for the registers.
 #include "device_common.h"
 #include "internal.h"
 #include "lds_limit.h"
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(NW * 64) mxfp4_rows_kernel(RowArgs a) {
                 i32x8 xq{(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0}, xs;
                 if constexpr (FX == kMxE4m3) mx_parts8(p, x1, xq, xs);
                 const int xe = row_sc[rl * (KS * 4) + sl * 4 + fg];
+                // fp32 sums of e4m3 in two instructions (mx_parts)
                 auto multiply = [&](const i32x8 &wf, int sc, f32x4 d) {
                     if constexpr (FX == kMxE4m3)
                         d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xs, d, kMxE2m1, FX, 0, sc, 0, xe);

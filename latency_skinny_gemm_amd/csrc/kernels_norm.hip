@@ -15,8 +15,9 @@
 // every step.  It takes 2-5 % of the time.
 //
 // Many rows are bound by HBM: 8192 x 7168 with a residual to MX moves 411 MB in
-// 79 us, 5.2 TB/s (a copy on this card: 4.7).  One row takes 3.6 us: a launch,
-// a load, the reduction's barrier and a store, one after another.
+// 80 us, 5.1 TB/s, one call after another (89 us in a kernel trace; a copy on this
+// card: 4.7 TB/s).  One row takes 3.9 us: a launch, a load, the reduction's barrier
+// and a store, one after another.
 #include <algorithm>
 
 #include "device_common.h"
@@ -237,9 +238,9 @@ int go(const NormArgs &a, hipStream_t stream) {
 
 // One vector of 8 values a lane up to 8192 values (in us, with residual, to MX,
 // at 1, 1024 and 8192 rows; beside it half the lanes with two each):
-//   2880 values   2.9  6.6 34.1    3.7  7.1 32.5
-//   4096          2.9  8.3 41.1    3.9  8.4 41.0
-//   7168          3.4 12.3 79.7    3.9 12.2 76.8
+//   2880 values   3.0  7.7 37.9    3.9  8.2 35.3
+//   4096          3.2  9.6 44.1    4.2 10.0 43.8
+//   7168          3.7 13.8 87.0    4.5 14.3 80.6
 // so the shorter chain wins for few rows everywhere, and for many rows two
 // vectors only where a row needs more than 512 lanes.
 template <int OUT>
@@ -250,7 +251,7 @@ int pick(const NormArgs &a, hipStream_t stream) {
     if (k8 <= 512) return go<OUT, 512, 1>(a, stream);
     if (k8 <= 1024) return a.M <= 1024 ? go<OUT, 1024, 1>(a, stream) : go<OUT, 512, 2>(a, stream);
     if (k8 <= 2048) return go<OUT, 1024, 2>(a, stream);
-    // longer rows are read twice: 16384 values, 4096 rows: 103 us against 88
+    // longer rows are read twice: 16384 values, 4096 rows: 108 us against 90
     return go<OUT, 1024, 0>(a, stream);
 }
 
