@@ -19,7 +19,10 @@ __all__ = ["SkgPlan", "SkinnyGemmError", "gemm_bf16", "gemm_bf16_planned", "gemm
            "quant_e4m3",
            # the operators around the products (moe.py)
            "NormOut", "MxfpWeights", "rmsnorm", "route", "quant_mx", "dequant_mx", "mxfp4_pack",
-           "gemm_mxfp4", "moe_mxfp4", "reserve_moe"]
+           "gemm_mxfp4", "moe_mxfp4", "reserve_moe",
+           # latent attention (latent.py)
+           "LatentOut", "latent_append", "latent_attention", "latent_attention_expanded", "heads_gemm",
+           "reserve_latent"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libskinny_gemm.so")
@@ -125,6 +128,7 @@ def _load():
     L.skinny_gemm_status_string.argtypes = [I]
     L.skinny_gemm_status_string.restype = ctypes.c_char_p
     moe.declare(L)
+    latent.declare(L)
     _lib = L
     return L
 
@@ -432,3 +436,6 @@ def release_all():
 from . import moe  # noqa: E402  (uses the helpers above)
 from .moe import (MxfpWeights, NormOut, dequant_mx, gemm_mxfp4, moe_mxfp4,  # noqa: E402,F401
                   mxfp4_pack, quant_mx, reserve_moe, rmsnorm, route)
+from . import latent  # noqa: E402  (uses moe's helpers)
+from .latent import (LatentOut, heads_gemm, latent_append, latent_attention,  # noqa: E402,F401
+                     latent_attention_expanded, reserve_latent)

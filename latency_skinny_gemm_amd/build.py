@@ -30,7 +30,8 @@ LIB_HIP = ["api.hip", "kernels_dot.hip", "kernels_splitk.hip", "kernels_tiled.hi
            "kernels_fp8.hip", "kernels_quant.hip", "kernels_fp8_tiled.hip", "kernels_rows.hip",
            "kernels_fp8_rows.hip", "api_moe.hip", "kernels_norm.hip", "kernels_route.hip",
            "kernels_mx.hip", "kernels_mxfp4.hip", "kernels_mxfp4_rows.hip",
-           "kernels_moe.hip"]
+           "kernels_moe.hip", "api_latent.hip", "kernels_latent_append.hip",
+           "kernels_latent_attention.hip", "kernels_latent_expanded.hip", "kernels_heads.hip"]
 LIB_HOST = ["plan.cpp"]
 # Per-file flags.  The tiled kernels keep their accumulators in VGPRs: with the
 # compiler's default AGPR form, the loop-carried accumulators were copied

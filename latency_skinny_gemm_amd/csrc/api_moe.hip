@@ -7,37 +7,14 @@
 #include "internal.h"
 #include "moe_internal.h"
 #include "mx_common.h"
+#include "spans.h"
 
 using namespace skg;
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// A tensor's memory, for the overlap checks (null: none).
-struct Span {
-    const void *p;
-    size_t bytes;
-};
-bool overlap(Span a, Span b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-template <size_t N, size_t L>
-bool any_overlap(const Span (&outs)[N], const Span (&ins)[L]) {
-    for (size_t i = 0; i < N; ++i) {
-        for (size_t j = i + 1; j < N; ++j)
-            if (overlap(outs[i], outs[j])) return true;
-        for (const Span &s : ins)
-            if (overlap(outs[i], s)) return true;
-    }
-    return false;
-}
-
 bool format_ok(int f) { return f == SKG_MX_E4M3 || f == SKG_MX_E2M1; }
 size_t code_bytes(int format, size_t n) { return format == SKG_MX_E4M3 ? n : n / 2; }
-int status(int hip) { return hip == (int)hipSuccess ? SKG_OK : SKG_ERR_HIP; }
 
 int check_mx(int format, int M, int K) {
     if (!format_ok(format) || M < 0 || K < 0) return SKG_ERR_INVALID_ARG;
@@ -141,7 +118,7 @@ extern "C" int skinny_quant_mx(const void *x, void *q, void *e8m0, int format, i
     const size_t n = (size_t)M * K;
     const Span outs[] = {{q, code_bytes(format, n)}, {e8m0, n / 32}}, ins[] = {{x, n * 2}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    return status(launch_quant_mx(x, q, e8m0, format, M, K, false, stream));
+    return hip_status(launch_quant_mx(x, q, e8m0, format, M, K, false, stream));
 }
 
 extern "C" int skinny_dequant_mx(const void *q, const void *e8m0, int format, void *out, int M,
@@ -154,7 +131,7 @@ extern "C" int skinny_dequant_mx(const void *q, const void *e8m0, int format, vo
     const size_t n = (size_t)M * K;
     const Span outs[] = {{out, n * 2}}, ins[] = {{q, code_bytes(format, n)}, {e8m0, n / 32}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    return status(launch_dequant_mx(q, e8m0, format, out, M, K, stream));
+    return hip_status(launch_dequant_mx(q, e8m0, format, out, M, K, stream));
 }
 
 extern "C" int skinny_rmsnorm(const void *x, const void *residual, const void *weight, float eps,
@@ -185,7 +162,7 @@ extern "C" int skinny_rmsnorm(const void *x, const void *residual, const void *w
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
     const Span y_out[] = {outs[0], outs[1]}, whole[] = {{x, 2 * n}, {residual, 2 * n}};
     if (any_overlap(y_out, whole)) return SKG_ERR_INVALID_ARG;
-    return status(launch_rmsnorm(x, residual, weight, eps, out_format, scale, y, e8m0,
+    return hip_status(launch_rmsnorm(x, residual, weight, eps, out_format, scale, y, e8m0,
                                  residual_out, M, K, stream));
 }
 
@@ -210,7 +187,7 @@ extern "C" int skinny_route(const void *logits, int dtype, const float *bias,
     const Span outs[] = {{weights, n}, {ids, n}},
                ins[] = {{logits, (size_t)T * E * la}, {bias, (size_t)E * 4}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    return status(launch_route(logits, dtype, bias, *o, weights, ids, T, E, stream));
+    return hip_status(launch_route(logits, dtype, bias, *o, weights, ids, T, E, stream));
 }
 
 extern "C" size_t skinny_mxfp4_packed_bytes(int E, int N, int K) {
@@ -229,7 +206,7 @@ extern "C" int skinny_mxfp4_pack(const void *q, const void *e8m0, void *packed, 
     const size_t n = (size_t)E * N * K;
     const Span outs[] = {{packed, bytes}}, ins[] = {{q, n / 2}, {e8m0, n / 32}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    return status(launch_mxfp4_pack(q, e8m0, packed, E, N, K, stream));
+    return hip_status(launch_mxfp4_pack(q, e8m0, packed, E, N, K, stream));
 }
 
 extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format,
@@ -254,7 +231,7 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     Mxfp4Args a{(const uint8_t *)x, (int)code_bytes(x_format, K), (const uint8_t *)x_e8m0, K / 32, x_format,
                 (const uint8_t *)packed, (const uint16_t *)bias, out, f32 ? 1 : 0, M, N, K};
     const Mxfp4Way way = mxfp4_way(M, N, K, x_format, x_e8m0 != nullptr);
-    if (way.blocks && !way.quantise_first) return status(launch_mxfp4_rows(a, way.blocks, stream));
+    if (way.blocks && !way.quantise_first) return hip_status(launch_mxfp4_rows(a, way.blocks, stream));
     float *ws = nullptr;
     unsigned *tk = nullptr;
     rc = acquire(stream, floats_of(linear_workspace_bytes((size_t)M, K)), 0, &ws, &tk);
@@ -271,7 +248,7 @@ extern "C" int skinny_gemm_mxfp4(const void *x, const void *x_e8m0, int x_format
     if (e != (int)hipSuccess) return SKG_ERR_HIP;
     a.xe = scales;
     a.es = mx_scale_stride(K);
-    return status(way.blocks ? launch_mxfp4_rows(a, way.blocks, stream) : launch_mxfp4(a, stream));
+    return hip_status(way.blocks ? launch_mxfp4_rows(a, way.blocks, stream) : launch_mxfp4(a, stream));
 }
 
 extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weights,
@@ -296,7 +273,7 @@ extern "C" int skinny_moe_mxfp4(const void *x, const int *ids, const float *weig
     if (rc != SKG_OK) return rc;
     const MoeArgs a{(const uint16_t *)x, ids, weights, (const uint8_t *)w13, (const uint8_t *)w2,
                     (uint16_t *)out, x_format, T, k, H, I, E};
-    return status(launch_moe(a, ws, stream));
+    return hip_status(launch_moe(a, ws, stream));
 }
 
 // For the tests: the way a product takes (its blocks of rows, 0 for tiles, with

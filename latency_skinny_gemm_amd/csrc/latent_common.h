@@ -1,0 +1,132 @@
+// latent_common.h -- device helpers shared by the kernels of latent attention.
+#pragma once
+
+#include "device_common.h"
+
+namespace skg {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------- sequences
+// New tokens of sequence b, their number and the first, within [0, T].
+struct Tokens {
+    int first, n;
+};
+__device__ __forceinline__ Tokens new_tokens(const int *starts, int b, int T) {
+    if (!starts) return {b, 1};
+    const int s = min(max(starts[b], 0), T), e = min(max(starts[b + 1], 0), T);
+    return {s, max(e - s, 0)};
+}
+
+// pre[b] = sum of work(0 .. b - 1) for b = 0 .. B, by a workgroup of 256; `part`
+// holds 4 values.  Every thread calls it; ends with a barrier.
+template <class Work>
+__device__ __forceinline__ void block_prefix(int B, long *pre, long *part, Work work) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    long carry = 0;
+    if (t == 0) pre[0] = 0;
+    for (int b0 = 0; b0 < B; b0 += 256) {
+        const int b = b0 + t;
+        long v = b < B ? work(b) : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const long u = __shfl_up(v, d, 64);
+            if (lane >= d) v += u;
+        }
+        if (lane == 63) part[wave] = v;
+        __syncthreads();
+        long before = carry;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) before += part[w];
+            carry += part[w];
+        }
+        if (b < B) pre[b + 1] = before + v;
+        __syncthreads();
+    }
+}
+// The b with pre[b] <= x < pre[b + 1], for 0 <= x < pre[B].
+__device__ __forceinline__ int find_sequence(const long *pre, int B, long x) {
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (pre[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- tiles in LDS
+// Rows lie in LDS with 16-byte pieces permuted among eight (piece c of row r at
+// c ^ swz8(r)), so that eight rows' same piece, which one fragment read takes at
+// once, and four rows' same pair of pieces, which a transposed read takes, come
+// from different banks.
+__device__ __forceinline__ int swz8(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+
+// Four 2-byte values of this lane's column from four rows: lane i of 16 points at
+// row i / 4, columns 4 (i % 4) .. + 3, and gets column i of rows 0 .. 3.
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 lds_transposed4(const unsigned char *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+}
+// Eight 1-byte values of this lane's column from eight rows: lane i of 16 points
+// at row i / 2, columns 8 (i % 2) .. + 7.
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+__device__ __forceinline__ i32x2 lds_transposed8(const unsigned char *p) {
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)p);
+}
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+// Eight e4m3 codes -> eight bf16 values (exact).
+__device__ __forceinline__ bf16x8 e4m3_to_bf16(i32x2 c) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, 1.0f, true);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false);
+    const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true);
+    return bf16x8{a.x, a.y, b.x, b.y, d.x, d.y, e.x, e.y};
+}
+
+// ---------------------------------------------------------------- softmax
+// Eight fp32 values -> bf16, to nearest, ties to even.
+__device__ __forceinline__ bf16x8 to_bf16x8(const float *v) {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];
+    return r;
+}
+// sum + the eight values.  The sum of the weights is made of the rounded ones, which
+// the second product takes: what their roundings have in common then cancels in the
+// quotient (errors of 1.0 to 1.4 times the output's own rounding instead of 1.1 to 1.5).
+__device__ __forceinline__ float add_bf16x8(bf16x8 v, float sum) {
+    const bf16x2 one{(__bf16)1.0f, (__bf16)1.0f};
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 0, 1), one, sum, false);
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 2, 3), one, sum, false);
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 4, 5), one, sum, false);
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(v, v, 6, 7), one, sum, false);
+}
+__device__ __forceinline__ uint2 to_bf16x4(float a, float b, float c, float d) {
+    const bf16x4 r{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d};
+    return __builtin_bit_cast(uint2, r);
+}
+
+// The other half's value: lane l and lane l ^ 32.
+__device__ __forceinline__ float other_half_max(float v) {
+    const unsigned u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float other_half_sum(float v) {
+    const unsigned u = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ bool not_finite(float v) {
+    return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u;
+}
+
+}  // namespace skg
