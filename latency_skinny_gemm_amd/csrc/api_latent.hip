@@ -132,7 +132,7 @@ extern "C" int skinny_latent_attention(const skinny_latent_batch *batch, const v
     const int tile = latent_rows(batch->B, batch->T, H);
     float *ws = nullptr;
     unsigned *tk = nullptr;
-    rc = acquire(stream, latent_workspace_bytes(tile) / 4, 0, &ws, &tk);
+    rc = acquire(stream, latent_workspace_bytes(tile, e4m3) / 4, 0, &ws, &tk);
     if (rc != SKG_OK) return rc;
     const LatentArgs a{(const uint16_t *)q, (const uint8_t *)cache, scale, batch->table, batch->kv_lens, batch->q_starts,
                        (uint16_t *)out, ws, (float)(softmax_scale * kLog2e), batch->B, batch->T, batch->table_width,
@@ -196,5 +196,5 @@ extern "C" int skinny_latent_reserve(int H, hipStream_t stream) {
     if (H > SKG_LATENT_MAX_H) return SKG_ERR_UNSUPPORTED;
     float *ws = nullptr;
     unsigned *tk = nullptr;
-    return acquire(stream, latent_workspace_bytes(64) / 4, 0, &ws, &tk);
+    return acquire(stream, std::max(latent_workspace_bytes(64, false), latent_workspace_bytes(32, true)) / 4, 0, &ws, &tk);
 }

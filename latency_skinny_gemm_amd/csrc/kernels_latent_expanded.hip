@@ -27,7 +27,7 @@ constexpr int kQuery = SKG_EXPANDED_NOPE + SKG_LATENT_ROPE;
 
 }  // namespace
 
-__global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a, int tiles) {
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) latent_expanded_kernel(ExpandedArgs a, int tiles) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     // a head's tiles lie on one XCD, those with the most keys first
@@ -39,13 +39,13 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
     int b = 0, i = n;
     if (a.B > 1) {
         long *pre = reinterpret_cast<long *>(lds_raw);
-        block_prefix(a.B, pre, pre + a.B + 1, [&](int s) { return (long)((new_tokens(a.q_starts, s, a.T).n + kRows - 1) / kRows); });
+        block_prefix<4>(a.B, pre, pre + a.B + 1, [&](int s) { return (long)((new_tokens(a.q_starts, s, a.T).n + kRows - 1) / kRows); });
         if (n >= pre[a.B]) return;
-        b = __builtin_amdgcn_readfirstlane(find_sequence(pre, a.B, n));
-        i = __builtin_amdgcn_readfirstlane(n - (int)pre[b]);
+        b = uniform(find_sequence(pre, a.B, n));
+        i = uniform(n - (int)pre[b]);
         __syncthreads();
     }
-    const Tokens q = new_tokens(a.q_starts, b, a.T), kv = new_tokens(a.kv_starts, b, a.S);
+    const Tokens q = uniform(new_tokens(a.q_starts, b, a.T)), kv = uniform(new_tokens(a.kv_starts, b, a.S));
     if (i * kRows >= q.n) return;
     const int before = a.causal ? kv.n - q.n : kv.n - 1;  // token j sees keys 0 .. before + j (causal) or before
     auto sees = [&](int j) { return max(a.causal ? before + j + 1 : kv.n, 0); };
@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
             qf[k] = __builtin_bit_cast(bf16x8, v);
         }
     }
+    wait_vmcnt_lds<0>();  // here, so that the compiler waits for no load inside the loop over the ring
     // direct loads: rows of 32 and of 8 pieces, permuted among eight
     const unsigned row_bytes = (unsigned)a.H * kKvRow;
     unsigned src[4];
@@ -96,8 +97,8 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
         const Rsrc rr = make_rsrc(a.k_rope + at * a.rope_stride, rows ? (unsigned)(rows - 1) * rope_bytes + kRopeRow : 0u);
         unsigned char *dst = lds_raw + slot * kSlotBytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) lds_load16<kCacheDefault>(rk, dst + wave * 8 * kKvRow + k * 1024, src[k]);
-        lds_load16<kCacheDefault>(rr, dst + kStep * kKvRow + wave * 1024, rope_src);
+        for (int k = 0; k < 4; ++k) ring_load16(rk, dst + wave * 8 * kKvRow + k * 1024, src[k]);
+        ring_load16(rr, dst + kStep * kKvRow + wave * 1024, rope_src);
     };
 
     unsigned char *flags = lds_raw + kSlots * kSlotBytes;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
             const int row0 = k * kStep;
             const bool masked = row0 + kStep > lim0;
             float p[16];
-            bf16x8 pf[2];
+            bf16x8 pf[2] = {};
             if (row0 < wave_most) {
                 f32x16 z;
 #pragma unroll
@@ -161,9 +162,6 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
                 pf[0] = to_bf16x8(p);
                 pf[1] = to_bf16x8(p + 8);
                 l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
-            } else {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) p[r] = 0.0f;
             }
             if (__builtin_expect(careful && row0 + kStep > sees(i * kRows), 0)) {
                 // keys whose values hold an infinity or NaN, in a step that some tokens do
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(256, 2) latent_expanded_kernel(ExpandedArgs a,
                     const int r0 = __builtin_ctz(f), r = (r0 >> 3) * 4 + (r0 & 3), kh = (r0 >> 2) & 1;
                     float own_p = 0.0f;
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) own_p = u == r ? p[u] : own_p;
+                    for (int u = 0; u < 16; ++u) own_p = u == r ? (float)pf[u >> 3][u & 7] : own_p;
                     const float pk = __shfl(own_p, l31 + 32 * kh, 64);
                     const bool in = row0 + r0 < lim;
 #pragma unroll

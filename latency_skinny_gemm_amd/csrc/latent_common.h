@@ -7,6 +7,7 @@ namespace skg {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
@@ -21,14 +22,14 @@ __device__ __forceinline__ Tokens new_tokens(const int *starts, int b, int T) {
     return {s, max(e - s, 0)};
 }
 
-// pre[b] = sum of work(0 .. b - 1) for b = 0 .. B, by a workgroup of 256; `part`
-// holds 4 values.  Every thread calls it; ends with a barrier.
-template <class Work>
+// pre[b] = sum of work(0 .. b - 1) for b = 0 .. B, by a workgroup of WAVES waves;
+// `part` holds as many values.  Every thread calls it; ends with a barrier.
+template <int WAVES, class Work>
 __device__ __forceinline__ void block_prefix(int B, long *pre, long *part, Work work) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     long carry = 0;
     if (t == 0) pre[0] = 0;
-    for (int b0 = 0; b0 < B; b0 += 256) {
+    for (int b0 = 0; b0 < B; b0 += 64 * WAVES) {
         const int b = b0 + t;
         long v = b < B ? work(b) : 0;
 #pragma unroll
@@ -40,7 +41,7 @@ __device__ __forceinline__ void block_prefix(int B, long *pre, long *part, Work 
         __syncthreads();
         long before = carry;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             if (w < wave) before += part[w];
             carry += part[w];
         }
@@ -60,6 +61,20 @@ __device__ __forceinline__ int find_sequence(const long *pre, int B, long x) {
 }
 
 // ---------------------------------------------------------------- tiles in LDS
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ Tokens uniform(Tokens q) { return {uniform(q.first), uniform(q.n)}; }
+
+// 16 bytes a lane from a buffer straight into LDS, at dst + 16 * lane (dst uniform).
+// Written as an instruction: beside the builtin, the compiler waits for every such
+// load that is under way before a transposed read (vmcnt(0) in each step of the
+// ring).  It writes no register but m0, which nothing else here keeps a value in;
+// the ring's own waits count it.
+__device__ __forceinline__ void ring_load16(Rsrc r, const unsigned char *dst, unsigned off) {
+    const unsigned at = (unsigned)uniform((int)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
+                 : "memory");
+}
+
 // Rows lie in LDS with 16-byte pieces permuted among eight (piece c of row r at
 // c ^ swz8(r)), so that eight rows' same piece, which one fragment read takes at
 // once, and four rows' same pair of pieces, which a transposed read takes, come
@@ -88,6 +103,19 @@ __device__ __forceinline__ bf16x8 e4m3_to_bf16(i32x2 c) {
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, false);
     const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, 1.0f, true);
     return bf16x8{a.x, a.y, b.x, b.y, d.x, d.y, e.x, e.y};
+}
+
+// A fragment as the matrix instruction takes it.
+__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+__device__ __forceinline__ bf16x8 as_bf16(s16x8 v) { return __builtin_bit_cast(bf16x8, v); }
+__device__ __forceinline__ bf16x8 as_bf16(i32x2 v) { return e4m3_to_bf16(v); }
+
+// Fragments read ahead: what stands before this in the source is read before, and x is
+// there after it.  (Left to itself the compiler reads each fragment right before its use.)
+template <class T, int N>
+__device__ __forceinline__ void arrived(T (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i])::"memory");
 }
 
 // ---------------------------------------------------------------- softmax

@@ -21,8 +21,6 @@ struct LatentAppendArgs {
 };
 int launch_latent_append(const LatentAppendArgs &a, int style, bool e4m3, hipStream_t stream);
 
-// Workgroups of the absorbed form: one a CU.
-constexpr int kLatentGroups = 256;
 struct LatentArgs {
     const uint16_t *q;
     const uint8_t *cache;
@@ -33,9 +31,9 @@ struct LatentArgs {
     float factor;  // softmax scale * log2 e
     int B, T, W, page_shift, pages, H;
 };
-// Rows (token, head) a workgroup takes at once: 32, 64 or 128.
+// Rows (token, head) a workgroup takes at once: 32 or 64.
 int latent_rows(int B, int T, int H);
-size_t latent_workspace_bytes(int rows);
+size_t latent_workspace_bytes(int rows, bool e4m3);
 int launch_latent_attention(const LatentArgs &a, bool e4m3, int rows, hipStream_t stream);
 
 struct ExpandedArgs {
