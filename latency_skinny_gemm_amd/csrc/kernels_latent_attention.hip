@@ -37,11 +37,12 @@ constexpr size_t part_floats() {
     return (size_t)RG * 32 * (SKG_LATENT + 2);
 }
 __host__ __device__ constexpr int row_bytes(bool e4m3) { return SKG_LATENT_ROW * (e4m3 ? 1 : 2); }
-// The ring, and two steps' scores of 32 cache rows by 32 rows for each four waves.
-constexpr int kScores = 32 * 32;
+// The ring; two steps' weights of 32 cache rows by 32 rows in bf16 for each four
+// waves, or one step's scores in fp32; flags.
+constexpr int kWeights = 32 * 32;
 template <int RG, bool E4M3>
 constexpr size_t lds_bytes() {
-    return (size_t)kRing * kTile * row_bytes(E4M3) + 2 * RG * kScores * 4;
+    return (size_t)kRing * kTile * row_bytes(E4M3) + 2 * RG * kWeights * 2 + 64;
 }
 static_assert(lds_bytes<2, false>() <= 160 * 1024 && 2 * lds_bytes<1, true>() <= 160 * 1024, "a CU's LDS");
 static_assert((SKG_LATENT_MAX_B + 1) * 8 <= kRing * kTile * row_bytes(true), "prefix sums fit the ring");
@@ -84,11 +85,17 @@ __device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f3
 
 }  // namespace
 
-// A workgroup takes 32 RG rows, four waves 32 of them: each makes the scores of half
-// of a step's cache rows and half of its own, all hold the weights, and each sums its
-// quarter of the 512 columns.  While the weights of a step are made, the scores of
-// the next one are: one barrier a step, behind which both its scores (exchanged
-// through LDS) and the next step's cache rows are there.
+// A workgroup takes 32 RG rows, four waves 32 of them: each makes the weights of half
+// of a step's cache rows and half of its own, which all four then read from LDS, and
+// sums its quarter of the 512 columns.  The weights are made a step ahead: one barrier a
+// step, behind which its weights and the next step's cache rows are there.  Of the
+// two waves that share a SIMD one makes the next weights first and the other sums
+// first, so that matrix and vector instructions of the two run side by side.
+//
+// Weights are 2^(score - m), m a row's maximum as of the last step in which a score was
+// over m + 8: sums and weights then stay below 2^8 times their number, no wave needs
+// the others' scores, and the sums are multiplied in few steps only.  In those steps
+// (the first of a row tile, rarely a later one) all scores go through LDS.
 //
 // Workgroups that hold different heads of the same tokens form a team, which takes
 // its share of all steps together, so that a cache row is read from memory once.
@@ -105,7 +112,8 @@ latent_attention_kernel(Shape s) {
     const LatentArgs &a = s.a;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
     const int rg = wave >> 2, cs = wave & 3;
-    float *const exchange = reinterpret_cast<float *>(lds_raw + kRing * TILE);
+    unsigned char *const exchange = lds_raw + kRing * TILE;
+    unsigned *const flags = reinterpret_cast<unsigned *>(exchange + 2 * RG * kWeights * 2);
     // neighbouring groups on one XCD
     const int G = gridDim.x, group = (int)(blockIdx.x & 7) * (G / 8) + (int)(blockIdx.x >> 3);
     const int teams = G / s.hg, team = group / s.hg, g = group - team * s.hg;
@@ -142,6 +150,8 @@ latent_attention_kernel(Shape s) {
         at = uniform((int)(off - steps_before(before, q.n, s.tp, i)));
     }
     __syncthreads();
+    if (t < 16) flags[t] = 0;
+    unsigned epoch = 0;  // steps so far: a step's flag is its number
     Shared mine{0, 0, 0, 0};
 
     // ---- constants of the lane
@@ -150,7 +160,7 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
         const int p = k * 64 + lane, row = p / PIECES, c = p % PIECES, tr = wave * WR + row;
-        const int piece = E4M3 ? (c & ~3) | ((c & 3) ^ ((tr >> 1) & 3)) : (c & ~7) | ((c & 7) ^ swz8(tr & 7));
+        const int piece = E4M3 ? (c & ~3) | ((c & 3) ^ swz4(tr)) : (c & ~7) | ((c & 7) ^ swz8(tr));
         src[k] = (unsigned)(row * ROWB + piece * 16);
     }
     // fragments of keys, 16 rows by 32 values
@@ -158,28 +168,33 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int row = (cs & 1) * 16 + l15;
-        koff[j] = (unsigned)(row * ROWB) + (unsigned)(E4M3 ? ((j * 2 + (g4 >> 1)) ^ ((row >> 1) & 3)) * 16 + (g4 & 1) * 8
-                                                           : ((j * 4 + g4) ^ swz8(row & 7)) * 16);
+        koff[j] = (unsigned)(row * ROWB) + (unsigned)(E4M3 ? ((j * 2 + (g4 >> 1)) ^ swz4(row)) * 16 + (g4 & 1) * 8
+                                                           : ((j * 4 + g4) ^ swz8(row)) * 16);
     }
     // and of values, 32 columns by 16 rows: this lane's column from rows 4 half + 0 .. 3
     // and 8 + 4 half + 0 .. 3, as the scores' registers have them
-    unsigned voff[2];
+    unsigned voff[2][E4M3 ? 1 : 2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int dg = g4 & 1;
         if constexpr (E4M3) {
             const int k = l15 >> 1, row = (k >> 2) * 8 + 4 * half + (k & 3);
-            voff[j] = (unsigned)(row * ROWB + (((j * 2 + dg) ^ ((row >> 1) & 3)) * 16) + (l15 & 1) * 8 + cs * DB * 32);
+            voff[j][0] = (unsigned)(row * ROWB + (((j * 2 + dg) ^ swz4(row)) * 16) + (l15 & 1) * 8 + cs * DB * 32);
         } else {
-            const int row = 4 * half + (l15 >> 2);
-            voff[j] = (unsigned)(row * ROWB + (((j * 4 + dg * 2 + ((l15 & 3) >> 1)) ^ swz8(row)) * 16) + (l15 & 1) * 8 + cs * DB * 64);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int row = 8 * y + 4 * half + (l15 >> 2);
+                voff[j][y] = (unsigned)(row * ROWB + (((j * 4 + dg * 2 + ((l15 & 3) >> 1)) ^ swz8(row)) * 16) + (l15 & 1) * 8 + cs * DB * 64);
+            }
         }
     }
-    // scores of 16 cache rows by 16 rows, four of a row in 16 bytes; pieces permuted
-    // among the row's eight
-    const int ex_row = (cs >> 1) * 16 + l15;
-    const unsigned put_at = (unsigned)(rg * kScores + ex_row * 32 + (((cs & 1) * 4 + g4) ^ (ex_row & 7)) * 4);
-    const unsigned get_at = (unsigned)(rg * kScores + l31 * 32);
+    // Weights of 16 cache rows by 16 rows, four of a row a lane: into a row's 32 in the
+    // order in which the second product's lanes take eight of them, the row's four
+    // 16-byte pieces permuted.  Scores likewise, in the order of the cache rows.
+    const int own_row = (cs >> 1) * 16 + l15;
+    const unsigned put_at = (unsigned)((rg * 32 + own_row) * 64 + ((((cs & 1) * 2 + (g4 & 1)) ^ ((own_row >> 2) & 3)) * 16) + (g4 >> 1) * 8);
+    const unsigned get_at[2] = {(unsigned)((rg * 32 + l31) * 64 + ((half ^ ((l31 >> 2) & 3)) * 16)),
+                                (unsigned)((rg * 32 + l31) * 64 + (((2 + half) ^ ((l31 >> 2) & 3)) * 16))};
     const float kv_scale = E4M3 ? a.scale[0] : 1.0f;
     const float factor = a.factor * kv_scale;
 
@@ -203,18 +218,18 @@ latent_attention_kernel(Shape s) {
             tok += j0;
             return ok;
         };
-        // how many cache rows the lane's row sees
+        // how many cache rows the row whose weights this lane makes sees
         int lim;
         {
             int tok, head;
-            lim = place(rg * 32 + l31, tok, head) ? max(before + tok + 1, 0) : 0;
+            lim = place(rg * 32 + own_row, tok, head) ? max(before + tok + 1, 0) : 0;
         }
 
         // queries: fragments of 16 rows by 32 values
         bf16x8 qf[18];
         {
             int qt, qh;
-            const bool ok = place(rg * 32 + (cs >> 1) * 16 + l15, qt, qh);
+            const bool ok = place(rg * 32 + own_row, qt, qh);
             const uint16_t *p = a.q + ((size_t)(q.first + (ok ? qt : 0)) * a.H + (ok ? qh : 0)) * SKG_LATENT_ROW + g4 * 8;
 #pragma unroll
             for (int k = 0; k < 18; ++k) {
@@ -227,7 +242,7 @@ latent_attention_kernel(Shape s) {
         wait_vmcnt_lds<0>();
 
         f32x16 acc[DB];
-        float m, l;
+        float m, l;  // of row l31
         bool careful = false;
         for (;;) {
 #pragma unroll
@@ -236,6 +251,8 @@ latent_attention_kernel(Shape s) {
                 for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
             m = -__builtin_inff();
             l = 0.0f;
+            float own_ref = 0.0f, own_most = -__builtin_inff();  // of row own_row: m, or 0 where there is none; m + 8
+            f32x4 last;                                          // this lane's scores of the step to come
 
             // table entries of 64 pages, one a lane
             int first_page = -64, entry = -1;
@@ -271,9 +288,9 @@ latent_attention_kernel(Shape s) {
                 for (int k = 0; k < LOADS; ++k)
                     if ((k + 1) * 64 <= WR * PIECES || lane < WR * PIECES - k * 64) ring_load16(rs, dst + k * 1024, src[k]);
             };
-            // Scores of a step (16 by 16 a wave), times the factor, to where all four
-            // waves read them.  Behind the last step they are those of old rows, and unused.
-            auto scores = [&](const unsigned char *tile, float *to) {
+            // Weights of a step (16 by 16 a wave) to where all four waves read them.  Behind
+            // the last step they are those of old rows, and unused.
+            auto weigh = [&](const unsigned char *tile, int row0, unsigned bits, int parity, unsigned number) {
                 f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                 Key kf[2][KB];
                 auto read = [&](int c0, Key(&k)[KB]) {
@@ -290,7 +307,19 @@ latent_attention_kernel(Shape s) {
                     for (int c = 0; c < KB; ++c)
                         y[c & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[(c0 / KB) & 1][c]), qf[c0 + c], y[c & 1], 0, 0, 0);
                 }
-                *reinterpret_cast<f32x4 *>(to + put_at) = (y[0] + y[1]) * factor;
+                f32x4 z = (y[0] + y[1]) * factor;
+                if (row0 + kTile > lim0 || bits != 15u) {
+                    const bool held = bits >> ((cs & 1) * 2 + (g4 >> 1)) & 1u;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) z[r] = held && row0 + (cs & 1) * 16 + g4 * 4 + r < lim ? z[r] : -__builtin_inff();
+                }
+                last = z;
+                if (__any(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > own_most)) {
+                    if (lane == 0) flags[parity] = number;
+                }
+                const uint2 w = to_bf16x4(__builtin_amdgcn_exp2f(z[0] - own_ref), __builtin_amdgcn_exp2f(z[1] - own_ref),
+                                          __builtin_amdgcn_exp2f(z[2] - own_ref), __builtin_amdgcn_exp2f(z[3] - own_ref));
+                *reinterpret_cast<uint2 *>(exchange + parity * RG * kWeights * 2 + put_at) = w;
             };
 
             for (int k = 0; k < kRing - 1; ++k)
@@ -299,65 +328,67 @@ latent_attention_kernel(Shape s) {
             else if (n > 1) wait_vmcnt_lds<LOADS>();
             else wait_vmcnt_lds<0>();
             barrier_nofence();
-            scores(lds_raw, exchange);
+            ++epoch;
+            weigh(lds_raw, at * kTile, (seen >> (4 * min(kRing - 2, n - 1))) & 15u, 0, epoch);
             int slot = 0;
             for (int k = 0; k < n; ++k) {
                 // the next step's rows are there when one later step may be under way
                 if (k + 2 < n) wait_vmcnt_lds<LOADS>();
                 else wait_vmcnt_lds<0>();
                 barrier_nofence();
-                const unsigned bits = (seen >> (4 * min(kRing - 2, n - 1 - k))) & 15u;
+                const int ahead = min(kRing - 2, n - 1 - k);  // steps asked for behind this one
+                const unsigned bits = (seen >> (4 * ahead)) & 15u, next_bits = (seen >> (4 * max(ahead - 1, 0))) & 15u;
                 // every wave is done with the slot of the step before
                 if (k + kRing - 1 < n) issue(at + k + kRing - 1, (slot + kRing - 1) & (kRing - 1));
                 const unsigned char *tile = lds_raw + slot * TILE;
+                slot = (slot + 1) & (kRing - 1);
+                const unsigned char *next = lds_raw + slot * TILE;
                 const int row0 = (at + k) * kTile;
 
-                // register r of a lane is row 8 (r / 4) + 4 half + r % 4 of the step, its column
-                // the lane's (token, head)
-                float z[16];
-                const float *ex = exchange + (k & 1) * RG * kScores + get_at;
+                // of column l31, the lane's (token, head), in the second product's order
+                bf16x8 pf[2];
+                if (__builtin_expect(uniform((int)flags[k & 1]) == (int)epoch, 0)) {
+                    // a maximum has grown: new weights of all scores, old sums multiplied
+                    float *all = reinterpret_cast<float *>(exchange);
+                    *reinterpret_cast<f32x4 *>(all + (rg * 32 + own_row) * 32 + ((((cs & 1) * 4 + g4) ^ (own_row & 7)) * 4)) = last;
+                    __syncthreads();
+                    float z[16];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) *reinterpret_cast<f32x4 *>(z + 4 * v) = *reinterpret_cast<const f32x4 *>(ex + ((2 * v + half) ^ (l31 & 7)) * 4);
-                slot = (slot + 1) & (kRing - 1);
-                scores(lds_raw + slot * TILE, exchange + ((k + 1) & 1) * RG * kScores);
-
-                const bool masked = row0 + kTile > lim0 || bits != 15u;
-                if (masked) {
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<f32x4 *>(z + 4 * v) = *reinterpret_cast<const f32x4 *>(all + (rg * 32 + l31) * 32 + ((2 * v + half) ^ (l31 & 7)) * 4);
+                    float top = z[0];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int row = row0 + 8 * (r >> 2) + 4 * half + (r & 3);
-                        z[r] = row < lim && (bits >> (r >> 2) & 1u) ? z[r] : -__builtin_inff();
-                    }
-                }
-                float top = z[0];
-#pragma unroll
-                for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
-                top = other_half_max(top);
-                // The running maximum follows only where a score is over 2^8 times it: sums and
-                // weights then stay below 2^8 times their number, and the columns' sums are
-                // multiplied in few steps only.
-                if (__any(top > m + 8.0f)) {
-                    const float next = fmaxf(m, top);
-                    const float down = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - next);
-                    m = next;
+                    for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
+                    top = fmaxf(m, other_half_max(top));
+                    const float down = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+                    const float ref = top == -__builtin_inff() ? 0.0f : top;
+                    m = top;
                     l *= down;
 #pragma unroll
                     for (int d = 0; d < DB; ++d)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) acc[d][r] *= down;
-                }
-                const float ref = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) z[r] = __builtin_amdgcn_exp2f(z[r] - ref);
-                // the registers of eight weights are what the second product takes, as they lie
-                const bf16x8 pf[2] = {to_bf16x8(z), to_bf16x8(z + 8)};
+                    for (int r = 0; r < 16; ++r) z[r] = __builtin_amdgcn_exp2f(z[r] - ref);
+                    pf[0] = to_bf16x8(z);
+                    pf[1] = to_bf16x8(z + 8);
+                    own_ref = __shfl(ref, own_row, 64);
+                    own_most = __shfl(m, own_row, 64) + 8.0f;
+                    __syncthreads();
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) pf[v] = *reinterpret_cast<const bf16x8 *>(exchange + (k & 1) * RG * kWeights * 2 + get_at[v]);
+                }
+                ++epoch;
+                if (rg == 0) weigh(next, row0 + kTile, next_bits, (k + 1) & 1, epoch);
                 l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
+                const bool masked = row0 + kTile > lim0 || bits != 15u;
                 if (__builtin_expect(careful && masked, 0)) {
                     // Rows with infinities or NaN that some of the tile's tokens see and some do
                     // not: their products by vector instructions for those that do, and zeros
                     // in their place for the matrix instruction.
-                    __syncthreads();  // all waves have read this step's scores
-                    unsigned char *flags = reinterpret_cast<unsigned char *>(exchange + (k & 1) * RG * kScores);
+                    __syncthreads();
+                    unsigned char *bad_rows = reinterpret_cast<unsigned char *>(flags + 4);
                     bool bad = false;
                     for (int e = 0; e < ROWB * 512 / 576 / 8 / 4; ++e) {
                         const unsigned w = *reinterpret_cast<const unsigned *>(
@@ -373,16 +404,20 @@ latent_attention_kernel(Shape s) {
                     unsigned rows8 = 0;
 #pragma unroll
                     for (int r = 0; r < 8; ++r) rows8 |= ((any >> (8 * r)) & 0xFFull ? 1u : 0u) << r;
-                    if (lane == 0) flags[cs] = (unsigned char)rows8;  // each four waves the same
+                    if (lane == 0) bad_rows[cs] = (unsigned char)rows8;  // each four waves the same
                     __syncthreads();
-                    const unsigned flagged = (unsigned)uniform((int)*reinterpret_cast<const unsigned *>(flags));
+                    const unsigned flagged = (unsigned)uniform((int)flags[4]);
+                    const int col_lim = [&] {
+                        int tok, head;
+                        return place(rg * 32 + l31, tok, head) ? max(before + tok + 1, 0) : 0;
+                    }();
                     for (unsigned f = flagged; f; f &= f - 1) {
                         const int e = __builtin_ctz(f), r = (e >> 3) * 4 + (e & 3), eh = (e >> 2) & 1;
                         float own = 0.0f;
 #pragma unroll
                         for (int u = 0; u < 16; ++u) own = u == r ? (float)pf[u >> 3][u & 7] : own;
                         const float w = __shfl(own, l31 + 32 * eh, 64);
-                        const bool sees = row0 + e < lim && (bits >> (e >> 3) & 1u);
+                        const bool sees = row0 + e < col_lim && (bits >> (e >> 3) & 1u);
 #pragma unroll
                         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -392,14 +427,14 @@ latent_attention_kernel(Shape s) {
                                 if constexpr (E4M3) {
                                     const int c = col >> 4;
                                     const unsigned x = *reinterpret_cast<const unsigned *>(
-                                        tile + e * ROWB + ((c & ~3) | ((c & 3) ^ ((e >> 1) & 3))) * 16 + (col & 15));
+                                        tile + e * ROWB + ((c & ~3) | ((c & 3) ^ swz4(e))) * 16 + (col & 15));
                                     const bf16x8 c8 = e4m3_to_bf16(i32x2{(int)x, 0});
 #pragma unroll
                                     for (int u = 0; u < 4; ++u) y[u] = (float)c8[u];
                                 } else {
                                     const int c = col >> 3;
                                     const uint2 x = *reinterpret_cast<const uint2 *>(
-                                        tile + e * ROWB + ((c & ~7) | ((c & 7) ^ swz8(e & 7))) * 16 + (col & 7) * 2);
+                                        tile + e * ROWB + ((c & ~7) | ((c & 7) ^ swz8(e))) * 16 + (col & 7) * 2);
                                     y[0] = bf16_lo(x.x);
                                     y[1] = bf16_hi(x.x);
                                     y[2] = bf16_lo(x.y);
@@ -421,9 +456,9 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int d = d0 + (e >> 1);
-                        const unsigned char *v = tile + voff[d & 1] + (e & 1) * 16 * ROWB + (d >> 1) * (E4M3 ? 64 : 128);
-                        if constexpr (E4M3) x[e] = lds_transposed8(v);
-                        else x[e] = __builtin_shufflevector(lds_transposed4(v), lds_transposed4(v + 8 * ROWB), 0, 1, 2, 3, 4, 5, 6, 7);
+                        const unsigned char *v = tile + (e & 1) * 16 * ROWB + (d >> 1) * (E4M3 ? 64 : 128);
+                        if constexpr (E4M3) x[e] = lds_transposed8(v + voff[d & 1][0]);
+                        else x[e] = __builtin_shufflevector(lds_transposed4(v + voff[d & 1][0]), lds_transposed4(v + voff[d & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
                     }
                 };
                 read(0, vf[0]);
@@ -435,6 +470,7 @@ latent_attention_kernel(Shape s) {
                     for (int e = 0; e < 4; ++e)
                         acc[d0 + (e >> 1)] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[(d0 / 2) & 1][e]), pf[e & 1], acc[d0 + (e >> 1)], 0, 0, 0);
                 }
+                if (rg != 0) weigh(next, row0 + kTile, next_bits, (k + 1) & 1, epoch);
             }
             wait_vmcnt_lds<0>();
             __syncthreads();  // the ring is free
@@ -447,13 +483,12 @@ latent_attention_kernel(Shape s) {
             for (int d = 0; d < DB; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) bad |= not_finite(acc[d][r]);
-            const unsigned long long found = __ballot(bad && lim > 0);
-            unsigned *flags = reinterpret_cast<unsigned *>(exchange);
-            if (lane == 0) flags[wave] = found != 0;
+            const unsigned long long found = __ballot(bad);
+            if (lane == 0) flags[8 + wave] = found != 0;
             __syncthreads();
             unsigned some = 0;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) some |= flags[w];
+            for (int w = 0; w < NW; ++w) some |= flags[8 + w];
             __syncthreads();
             if (!uniform((int)some)) break;
             careful = true;

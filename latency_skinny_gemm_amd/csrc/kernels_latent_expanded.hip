@@ -68,28 +68,28 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
         }
     }
     wait_vmcnt_lds<0>();  // here, so that the compiler waits for no load inside the loop over the ring
-    // direct loads: rows of 32 and of 8 pieces, permuted among eight
+    // direct loads: rows of 32 pieces, permuted among 16, and of 8
     const unsigned row_bytes = (unsigned)a.H * kKvRow;
     unsigned src[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int p = k * 64 + lane, row = p >> 5, c = p & 31;
-        src[k] = (unsigned)row * row_bytes + (unsigned)(((c & ~7) | ((c & 7) ^ swz8(row))) * 16);
+        src[k] = (unsigned)row * row_bytes + (unsigned)((c ^ swz16(wave * 8 + row)) * 16);
     }
     const unsigned rope_bytes = (unsigned)a.rope_stride * 2;
-    const unsigned rope_src = (unsigned)(lane >> 3) * rope_bytes + (unsigned)(((lane & 7) ^ swz8(lane >> 3)) * 16);
-    unsigned koff[4], roff[4], voff[2];
+    const unsigned rope_src = (unsigned)(lane >> 3) * rope_bytes + (unsigned)(((lane & 7) ^ swz8(wave * 8 + (lane >> 3))) * 16);
+    unsigned koff[8], roff[4], voff[2][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const unsigned piece = (unsigned)(((c * 2 + half) ^ swz8(l31 & 7)) * 16);
-        koff[c] = (unsigned)l31 * kKvRow + piece;
-        roff[c] = (unsigned)(kStep * kKvRow) + (unsigned)l31 * kRopeRow + piece;
-    }
+    for (int c = 0; c < 8; ++c) koff[c] = (unsigned)l31 * kKvRow + (unsigned)(((c * 2 + half) ^ swz16(l31)) * 16);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int row = 4 * half + (l15 >> 2);
-        voff[c] = (unsigned)(row * kKvRow + 2 * SKG_EXPANDED_NOPE + ((c * 4 + (g4 & 1) * 2 + ((l15 & 3) >> 1)) ^ swz8(row)) * 16 + (l15 & 1) * 8);
-    }
+    for (int c = 0; c < 4; ++c) roff[c] = (unsigned)(kStep * kKvRow) + (unsigned)l31 * kRopeRow + (unsigned)(((c * 2 + half) ^ swz8(l31)) * 16);
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int row = 8 * y + 4 * half + (l15 >> 2);
+            voff[y][d] = (unsigned)(row * kKvRow + 2 * SKG_EXPANDED_NOPE + ((d * 4 + (g4 & 1) * 2 + ((l15 & 3) >> 1)) ^ swz16(row)) * 16 + (l15 & 1) * 8);
+        }
     auto issue = [&](int step, int slot) {
         const int row = step * kStep + wave * 8, rows = min(max(most - row, 0), 8);
         const size_t at = (size_t)kv.first + (rows ? row : 0);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
                 for (int r = 0; r < 16; ++r) z[r] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 12; ++c) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(tile + (c < 8 ? koff[c & 3] + (c >> 2) * 128 : roff[c & 3]));
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(tile + (c < 8 ? koff[c] : roff[c - 8]));
                     z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[c], z, 0, 0, 0);
                 }
                 if (masked) {
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
                     for (int d = 0; d < 4; ++d)
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            const int c = 16 + d * 4 + v;
-                            const uint2 w = *reinterpret_cast<const uint2 *>(tile + r0 * kKvRow + ((c & ~7) | ((c & 7) ^ swz8(r0 & 7))) * 16 + half * 8);
+                            const int c = d * 4 + v;
+                            const uint2 w = *reinterpret_cast<const uint2 *>(tile + r0 * kKvRow + 2 * SKG_EXPANDED_NOPE + (c ^ swz16(r0)) * 16 + half * 8);
                             const float y[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
                 for (int d = 0; d < 4; ++d) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
-                        const unsigned char *v = tile + voff[d & 1] + kk * 16 * kKvRow + (d >> 1) * 128;
-                        const s16x4 x = lds_transposed4(v), y = lds_transposed4(v + 8 * kKvRow);
+                        const s16x4 x = lds_transposed4(tile + voff[0][d] + kk * 16 * kKvRow);
+                        const s16x4 y = lds_transposed4(tile + voff[1][d] + kk * 16 * kKvRow);
                         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                             __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf[kk], acc[d], 0, 0, 0);
                     }

@@ -75,11 +75,14 @@ __device__ __forceinline__ void ring_load16(Rsrc r, const unsigned char *dst, un
                  : "memory");
 }
 
-// Rows lie in LDS with 16-byte pieces permuted among eight (piece c of row r at
-// c ^ swz8(r)), so that eight rows' same piece, which one fragment read takes at
-// once, and four rows' same pair of pieces, which a transposed read takes, come
-// from different banks.
-__device__ __forceinline__ int swz8(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+// Rows lie in LDS with 16-byte pieces permuted: piece c of row r at c ^ swz(r) within
+// 4, 8 or 16.  LDS has 64 banks of 4 bytes; a fragment read takes the same piece of 16
+// rows at once, a transposed read the same four of four rows, and either comes from 16
+// different places of 16 bytes.  By the rows' size: 576 bytes (swz4), 1152 or 128 bytes, an odd
+// multiple of 128 (swz8), 512 bytes (swz16).
+__device__ __forceinline__ int swz4(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int swz8(int r) { return ((r & 2) << 1) | ((r >> 2) & 3); }
+__device__ __forceinline__ int swz16(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 
 // Four 2-byte values of this lane's column from four rows: lane i of 16 points at
 // row i / 4, columns 4 (i % 4) .. + 3, and gets column i of rows 0 .. 3.
