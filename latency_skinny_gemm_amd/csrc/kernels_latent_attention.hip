@@ -88,9 +88,10 @@ __device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f3
 // A workgroup takes 32 RG rows, four waves 32 of them: each makes the weights of half
 // of a step's cache rows and half of its own, which all four then read from LDS, and
 // sums its quarter of the 512 columns.  The weights are made a step ahead: one barrier a
-// step, behind which its weights and the next step's cache rows are there.  Of the
-// two waves that share a SIMD one makes the next weights first and the other sums
-// first, so that matrix and vector instructions of the two run side by side.
+// step, behind which its weights and the next step's cache rows are there.  Scores, sums
+// and the loads of a later step are interleaved, since a barrier starts all waves at
+// the same point: behind one another they had waited for LDS reads and for the way to memory
+// (36 KB a step at 64 bytes a clock) most of the time.
 //
 // Weights are 2^(score - m), m a row's maximum as of the last step in which a score was
 // over m + 8: sums and weights then stay below 2^8 times their number, no wave needs
@@ -105,7 +106,7 @@ latent_attention_kernel(Shape s) {
     constexpr int NW = 4 * RG, R = 32 * RG, ROWB = row_bytes(E4M3), TILE = kTile * ROWB;
     constexpr int WR = kTile / NW, PIECES = ROWB / 16, LOADS = (WR * PIECES + 63) / 64;  // rows that a wave brings
     constexpr int DB = 4;                                                               // blocks of 32 columns a wave
-    constexpr int KB = RG == 2 && !E4M3 ? 3 : 6;  // key fragments read together, as registers allow
+    static_assert(LOADS <= 9, "turn() asks for one a ninth");
     using Key = std::conditional_t<E4M3, i32x2, u32x4>;  // fragments as they lie in LDS
     using Value = std::conditional_t<E4M3, i32x2, s16x8>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
@@ -193,8 +194,9 @@ latent_attention_kernel(Shape s) {
     // 16-byte pieces permuted.  Scores likewise, in the order of the cache rows.
     const int own_row = (cs >> 1) * 16 + l15;
     const unsigned put_at = (unsigned)((rg * 32 + own_row) * 64 + ((((cs & 1) * 2 + (g4 & 1)) ^ ((own_row >> 2) & 3)) * 16) + (g4 >> 1) * 8);
-    const unsigned get_at[2] = {(unsigned)((rg * 32 + l31) * 64 + ((half ^ ((l31 >> 2) & 3)) * 16)),
-                                (unsigned)((rg * 32 + l31) * 64 + (((2 + half) ^ ((l31 >> 2) & 3)) * 16))};
+    const unsigned get_at = (unsigned)((rg * 32 + l31) * 64 + ((half ^ ((l31 >> 2) & 3)) * 16));
+    const unsigned ring = (unsigned)uniform((int)lds_address(lds_raw + wave * WR * ROWB));
+    const bool wide = a.page_shift >= 5;
     const float kv_scale = E4M3 ? a.scale[0] : 1.0f;
     const float factor = a.factor * kv_scale;
 
@@ -254,67 +256,91 @@ latent_attention_kernel(Shape s) {
             float own_ref = 0.0f, own_most = -__builtin_inff();  // of row own_row: m, or 0 where there is none; m + 8
             f32x4 last;                                          // this lane's scores of the step to come
 
-            // table entries of 64 pages, one a lane
-            int first_page = -64, entry = -1;
-            unsigned seen = 0;  // four bits a step, the newest lowest: groups of 8 rows whose page is one
-            auto issue = [&](int step, int slot) {
-                const int row0 = step * kTile, row = row0 + WR * wave;
-                const int one = row0 >> a.page_shift;
-                if (((row0 + kTile - 1) >> a.page_shift) >= first_page + 64) {
-                    first_page = one;
-                    const int e = first_page + lane;
-                    entry = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
+            // where the rows of 64 steps lie in the cache (of 16, by eights, where a step may
+            // have several pages), one a lane; -1: nowhere
+            int first = 0, place_of = -1;
+            unsigned known = 0;  // steps in it
+            unsigned seen = 0;   // four bits a step, the newest lowest: groups of 8 rows whose page is one
+            // Step `step` to ring slot `slot`: where its rows are, and then the loads, number k
+            // of LOADS each.  Behind the last step no row is there, and the loads bring zeros.
+            Rsrc rs;
+            unsigned dst;
+            auto locate = [&](int step, int slot) {
+                if (__builtin_expect((unsigned)(step - first) >= known, 0)) {
+                    first = step;
+                    known = wide ? 64 : 16;
+                    const long row = (long)step * kTile + lane * (wide ? kTile : 8);
+                    const long e = row >> a.page_shift;
+                    int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
                     wait_vmcnt_lds<0>();
+                    place_of = (unsigned)page < (unsigned)a.pages ? (int)(((unsigned)page << a.page_shift) + (unsigned)(row & ((1 << a.page_shift) - 1))) : -1;
                 }
-                int page = __builtin_amdgcn_readlane(entry, one - first_page);
-                unsigned bits = (unsigned)page < (unsigned)a.pages ? 15u : 0u;
-                bool held = bits != 0;
-                if (a.page_shift < 5) {  // several pages a step
+                int row, bits;
+                if (wide) {
+                    row = __builtin_amdgcn_readlane(place_of, step - first);
+                    bits = row >= 0 ? 15 : 0;
+                    row += WR * wave;
+                } else {
+                    const int l0 = (step - first) * 4;
                     bits = 0;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int p = __builtin_amdgcn_readlane(entry, ((row0 + 8 * w) >> a.page_shift) - first_page);
-                        bits |= ((unsigned)p < (unsigned)a.pages ? 1u : 0u) << w;
-                    }
-                    page = __builtin_amdgcn_readlane(entry, (row >> a.page_shift) - first_page);
-                    held = bits >> (WR * wave >> 3) & 1u;
+                    for (int w = 0; w < 4; ++w) bits |= (__builtin_amdgcn_readlane(place_of, l0 + w) >= 0 ? 1 : 0) << w;
+                    row = __builtin_amdgcn_readlane(place_of, l0 + (WR * wave >> 3)) + (WR * wave & 7);
                 }
-                seen = seen << 4 | bits;
-                const int rows = held ? min(max(most - row, 0), WR) : 0;
-                const size_t off = ((size_t)(rows ? page : 0) << a.page_shift) + (row & ((1 << a.page_shift) - 1));
-                const Rsrc rs = make_rsrc(a.cache + off * ROWB, (unsigned)(rows * ROWB));
-                unsigned char *dst = lds_raw + slot * TILE + wave * WR * ROWB;
-#pragma unroll
-                for (int k = 0; k < LOADS; ++k)
-                    if ((k + 1) * 64 <= WR * PIECES || lane < WR * PIECES - k * 64) ring_load16(rs, dst + k * 1024, src[k]);
+                seen = seen << 4 | (unsigned)bits;
+                row = uniform(row);
+                const int rows = uniform(bits >> (WR * wave >> 3) & 1 ? min(max(most - step * kTile - WR * wave, 0), WR) : 0);
+                rs = make_rsrc(a.cache + (rows ? (size_t)(unsigned)row * ROWB : 0), (unsigned)(rows * ROWB));
+                dst = ring + slot * TILE;
             };
-            // Weights of a step (16 by 16 a wave) to where all four waves read them.  Behind
-            // the last step they are those of old rows, and unused.
-            auto weigh = [&](const unsigned char *tile, int row0, unsigned bits, int parity, unsigned number) {
-                f32x4 y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                Key kf[2][KB];
-                auto read = [&](int c0, Key(&k)[KB]) {
+            auto load = [&](int k) {
+                if (k < LOADS && ((k + 1) * 64 <= WR * PIECES || lane < WR * PIECES - k * 64)) ring_load16(rs, dst + k * 1024, src[k]);
+            };
+            auto read_keys = [&](const unsigned char *tile, int c, Key(&x)[2]) {
 #pragma unroll
-                    for (int c = 0; c < KB; ++c)
-                        k[c] = *reinterpret_cast<const Key *>(tile + koff[(c0 + c) & 1] + ((c0 + c) >> 1) * (E4M3 ? 64 : 128));
-                };
-                read(0, kf[0]);
+                for (int e = 0; e < 2; ++e) x[e] = *reinterpret_cast<const Key *>(tile + koff[e] + c * (E4M3 ? 64 : 128));
+            };
+            auto read_values = [&](const unsigned char *tile, int e, Value(&x)[1]) {
+                const unsigned char *v = tile + (e & 1) * 16 * ROWB + (e >> 2) * (E4M3 ? 64 : 128);
+                if constexpr (E4M3) x[0] = lds_transposed8(v + voff[e >> 1 & 1][0]);
+                else x[0] = __builtin_shufflevector(lds_transposed4(v + voff[e >> 1 & 1][0]), lds_transposed4(v + voff[e >> 1 & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
+            };
+            // Scores of a step (16 by 16 a wave), and beside them the columns' sums of the step
+            // before (tile, with weights pf) and the loads of a later one: fragments are read a
+            // ninth ahead of their use.
+            f32x4 y[2];
+            bf16x8 pf[2];
+            auto turn = [&](auto both, const unsigned char *tile, const unsigned char *next) {
+                constexpr bool SUM = decltype(both)::value;
+                Key kf[2][2];
+                Value vf[2][1];
+                y[0] = y[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                read_keys(next, 0, kf[0]);
 #pragma unroll
-                for (int c0 = 0; c0 < 18; c0 += KB) {
-                    if (c0 + KB < 18) read(c0 + KB, kf[(c0 / KB + 1) & 1]);
-                    arrived(kf[(c0 / KB) & 1]);
+                for (int c = 0; c < 9; ++c) {
+                    if (c < 8) read_keys(next, c + 1, kf[(c + 1) & 1]);
+                    if (SUM && c < 8) read_values(tile, c, vf[c & 1]);
+                    if (SUM) load(c);
+                    arrived(kf[c & 1]);
 #pragma unroll
-                    for (int c = 0; c < KB; ++c)
-                        y[c & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[(c0 / KB) & 1][c]), qf[c0 + c], y[c & 1], 0, 0, 0);
+                    for (int e = 0; e < 2; ++e) y[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[c & 1][e]), qf[2 * c + e], y[e], 0, 0, 0);
+                    if (SUM && c >= 1) {
+                        arrived(vf[(c - 1) & 1]);
+                        acc[(c - 1) >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[(c - 1) & 1][0]), pf[(c - 1) & 1], acc[(c - 1) >> 1], 0, 0, 0);
+                    }
                 }
+            };
+            // Their weights to where all four waves read them.  Behind the last step the
+            // scores are those of zeros, and unused.
+            auto weigh = [&](int row0, unsigned bits, int parity, unsigned number) {
                 f32x4 z = (y[0] + y[1]) * factor;
-                if (row0 + kTile > lim0 || bits != 15u) {
+                if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
                     const bool held = bits >> ((cs & 1) * 2 + (g4 >> 1)) & 1u;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) z[r] = held && row0 + (cs & 1) * 16 + g4 * 4 + r < lim ? z[r] : -__builtin_inff();
                 }
                 last = z;
-                if (__any(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > own_most)) {
+                if (__builtin_expect(__any(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > own_most), 0)) {
                     if (lane == 0) flags[parity] = number;
                 }
                 const uint2 w = to_bf16x4(__builtin_amdgcn_exp2f(z[0] - own_ref), __builtin_amdgcn_exp2f(z[1] - own_ref),
@@ -322,33 +348,37 @@ latent_attention_kernel(Shape s) {
                 *reinterpret_cast<uint2 *>(exchange + parity * RG * kWeights * 2 + put_at) = w;
             };
 
-            for (int k = 0; k < kRing - 1; ++k)
-                if (k < n) issue(at + k, k);
-            if (n > 2) wait_vmcnt_lds<2 * LOADS>();
-            else if (n > 1) wait_vmcnt_lds<LOADS>();
-            else wait_vmcnt_lds<0>();
+#pragma unroll
+            for (int k = 0; k < kRing - 1; ++k) {
+                locate(at + k, k);
+#pragma unroll
+                for (int e = 0; e < LOADS; ++e) load(e);
+            }
+            wait_vmcnt_lds<2 * LOADS>();
             barrier_nofence();
             ++epoch;
-            weigh(lds_raw, at * kTile, (seen >> (4 * min(kRing - 2, n - 1))) & 15u, 0, epoch);
+            turn(std::false_type{}, lds_raw, lds_raw);
+            weigh(at * kTile, seen >> 8 & 15u, 0, epoch);
             int slot = 0;
             for (int k = 0; k < n; ++k) {
-                // the next step's rows are there when one later step may be under way
-                if (k + 2 < n) wait_vmcnt_lds<LOADS>();
-                else wait_vmcnt_lds<0>();
+                // the next step's rows are there when the one behind it may be under way
+                wait_vmcnt_lds<LOADS>();
                 barrier_nofence();
-                const int ahead = min(kRing - 2, n - 1 - k);  // steps asked for behind this one
-                const unsigned bits = (seen >> (4 * ahead)) & 15u, next_bits = (seen >> (4 * max(ahead - 1, 0))) & 15u;
+                // weights of column l31, the lane's (token, head), in the second product's order
+                const unsigned flag = flags[k & 1];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) pf[v] = *reinterpret_cast<const bf16x8 *>(exchange + (k & 1) * RG * kWeights * 2 + (get_at ^ (v * 32)));
+                const unsigned bits = seen >> 8 & 15u, next_bits = seen >> 4 & 15u;
                 // every wave is done with the slot of the step before
-                if (k + kRing - 1 < n) issue(at + k + kRing - 1, (slot + kRing - 1) & (kRing - 1));
+                locate(at + k + kRing - 1, (slot + kRing - 1) & (kRing - 1));
                 const unsigned char *tile = lds_raw + slot * TILE;
                 slot = (slot + 1) & (kRing - 1);
                 const unsigned char *next = lds_raw + slot * TILE;
                 const int row0 = (at + k) * kTile;
 
-                // of column l31, the lane's (token, head), in the second product's order
-                bf16x8 pf[2];
-                if (__builtin_expect(uniform((int)flags[k & 1]) == (int)epoch, 0)) {
+                if (__builtin_expect((unsigned)uniform((int)flag) == epoch, 0)) {
                     // a maximum has grown: new weights of all scores, old sums multiplied
+                    __syncthreads();
                     float *all = reinterpret_cast<float *>(exchange);
                     *reinterpret_cast<f32x4 *>(all + (rg * 32 + own_row) * 32 + ((((cs & 1) * 4 + g4) ^ (own_row & 7)) * 4)) = last;
                     __syncthreads();
@@ -375,12 +405,8 @@ latent_attention_kernel(Shape s) {
                     own_ref = __shfl(ref, own_row, 64);
                     own_most = __shfl(m, own_row, 64) + 8.0f;
                     __syncthreads();
-                } else {
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) pf[v] = *reinterpret_cast<const bf16x8 *>(exchange + (k & 1) * RG * kWeights * 2 + get_at[v]);
                 }
                 ++epoch;
-                if (rg == 0) weigh(next, row0 + kTile, next_bits, (k + 1) & 1, epoch);
                 l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
                 const bool masked = row0 + kTile > lim0 || bits != 15u;
                 if (__builtin_expect(careful && masked, 0)) {
@@ -451,26 +477,8 @@ latent_attention_kernel(Shape s) {
                             *reinterpret_cast<unsigned *>(const_cast<unsigned char *>(tile) + __builtin_ctz(f) * ROWB + e * 4) = 0;
                     __syncthreads();
                 }
-                Value vf[2][4];
-                auto read = [&](int d0, Value(&x)[4]) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = d0 + (e >> 1);
-                        const unsigned char *v = tile + (e & 1) * 16 * ROWB + (d >> 1) * (E4M3 ? 64 : 128);
-                        if constexpr (E4M3) x[e] = lds_transposed8(v + voff[d & 1][0]);
-                        else x[e] = __builtin_shufflevector(lds_transposed4(v + voff[d & 1][0]), lds_transposed4(v + voff[d & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
-                };
-                read(0, vf[0]);
-#pragma unroll
-                for (int d0 = 0; d0 < DB; d0 += 2) {
-                    if (d0 + 2 < DB) read(d0 + 2, vf[(d0 / 2 + 1) & 1]);
-                    arrived(vf[(d0 / 2) & 1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[d0 + (e >> 1)] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[(d0 / 2) & 1][e]), pf[e & 1], acc[d0 + (e >> 1)], 0, 0, 0);
-                }
-                if (rg != 0) weigh(next, row0 + kTile, next_bits, (k + 1) & 1, epoch);
+                turn(std::true_type{}, tile, next);
+                weigh(row0 + kTile, next_bits, (k + 1) & 1, epoch);
             }
             wait_vmcnt_lds<0>();
             __syncthreads();  // the ring is free

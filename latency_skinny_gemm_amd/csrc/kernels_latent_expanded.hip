@@ -90,12 +90,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
             const int row = 8 * y + 4 * half + (l15 >> 2);
             voff[y][d] = (unsigned)(row * kKvRow + 2 * SKG_EXPANDED_NOPE + ((d * 4 + (g4 & 1) * 2 + ((l15 & 3) >> 1)) ^ swz16(row)) * 16 + (l15 & 1) * 8);
         }
+    const unsigned ring = uniform((int)lds_address(lds_raw));
     auto issue = [&](int step, int slot) {
         const int row = step * kStep + wave * 8, rows = min(max(most - row, 0), 8);
         const size_t at = (size_t)kv.first + (rows ? row : 0);
         const Rsrc rk = make_rsrc(a.kv + (at * a.H + h) * (kKvRow / 2), rows ? (unsigned)(rows - 1) * row_bytes + kKvRow : 0u);
         const Rsrc rr = make_rsrc(a.k_rope + at * a.rope_stride, rows ? (unsigned)(rows - 1) * rope_bytes + kRopeRow : 0u);
-        unsigned char *dst = lds_raw + slot * kSlotBytes;
+        const unsigned dst = ring + slot * kSlotBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k) ring_load16(rk, dst + wave * 8 * kKvRow + k * 1024, src[k]);
         ring_load16(rr, dst + kStep * kKvRow + wave * 1024, rope_src);

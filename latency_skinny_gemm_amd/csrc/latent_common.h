@@ -64,24 +64,31 @@ __device__ __forceinline__ int find_sequence(const long *pre, int B, long x) {
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ Tokens uniform(Tokens q) { return {uniform(q.first), uniform(q.n)}; }
 
+// An address in LDS, for the loads below.
+__device__ __forceinline__ unsigned lds_address(const unsigned char *p) {
+    return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
+}
 // 16 bytes a lane from a buffer straight into LDS, at dst + 16 * lane (dst uniform).
 // Written as an instruction: beside the builtin, the compiler waits for every such
 // load that is under way before a transposed read (vmcnt(0) in each step of the
 // ring).  It writes no register but m0, which nothing else here keeps a value in;
 // the ring's own waits count it.
-__device__ __forceinline__ void ring_load16(Rsrc r, const unsigned char *dst, unsigned off) {
-    const unsigned at = (unsigned)uniform((int)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
+__device__ __forceinline__ void ring_load16(Rsrc r, unsigned dst, unsigned off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(r)
                  : "memory");
 }
 
 // Rows lie in LDS with 16-byte pieces permuted: piece c of row r at c ^ swz(r) within
-// 4, 8 or 16.  LDS has 64 banks of 4 bytes; a fragment read takes the same piece of 16
-// rows at once, a transposed read the same four of four rows, and either comes from 16
+// 4, 8 or 16.  LDS has 64 banks of 4 bytes; a fragment read takes one piece of 16
+// rows at once, or neighbouring ones of two times 8 rows (rows 0-3 and 12-15 beside 4-11),
+// a transposed read four pieces of four rows, and either comes from 16
 // different places of 16 bytes.  By the rows' size: 576 bytes (swz4), 1152 or 128 bytes, an odd
 // multiple of 128 (swz8), 512 bytes (swz16).
 __device__ __forceinline__ int swz4(int r) { return (r >> 2) & 3; }
-__device__ __forceinline__ int swz8(int r) { return ((r & 2) << 1) | ((r >> 2) & 3); }
+__device__ __forceinline__ int swz8(int r) {
+    const int x = (r >> 2) & 3;
+    return ((r & 2) << 1) | (((x ^ (x >> 1)) & 1) << 1) | (x >> 1);
+}
 __device__ __forceinline__ int swz16(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 
 // Four 2-byte values of this lane's column from four rows: lane i of 16 points at
