@@ -88,10 +88,10 @@ __device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f3
 // A workgroup takes 32 RG rows, four waves 32 of them: each makes the weights of half
 // of a step's cache rows and half of its own, which all four then read from LDS, and
 // sums its quarter of the 512 columns.  The weights are made a step ahead: one barrier a
-// step, behind which its weights and the next step's cache rows are there.  Scores, sums
-// and the loads of a later step are interleaved, since a barrier starts all waves at
-// the same point: behind one another they had waited for LDS reads and for the way to memory
-// (36 KB a step at 64 bytes a clock) most of the time.
+// step, behind which its weights and the next step's cache rows are there.  A barrier
+// starts all waves at the same point, so that each has to fill its own waits: scores
+// run while the weights come from LDS, sums beside the next weights' vector
+// instructions, and the loads of a later step (36 KB at 64 bytes a clock) between both.
 //
 // Weights are 2^(score - m), m a row's maximum as of the last step in which a score was
 // over m + 8: sums and weights then stay below 2^8 times their number, no wave needs
@@ -106,7 +106,7 @@ latent_attention_kernel(Shape s) {
     constexpr int NW = 4 * RG, R = 32 * RG, ROWB = row_bytes(E4M3), TILE = kTile * ROWB;
     constexpr int WR = kTile / NW, PIECES = ROWB / 16, LOADS = (WR * PIECES + 63) / 64;  // rows that a wave brings
     constexpr int DB = 4;                                                               // blocks of 32 columns a wave
-    static_assert(LOADS <= 9, "turn() asks for one a ninth");
+    static_assert(LOADS <= 9, "one beside each ninth of the scores");
     using Key = std::conditional_t<E4M3, i32x2, u32x4>;  // fragments as they lie in LDS
     using Value = std::conditional_t<E4M3, i32x2, s16x8>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
@@ -261,11 +261,12 @@ latent_attention_kernel(Shape s) {
             int first = 0, place_of = -1;
             unsigned known = 0;  // steps in it
             unsigned seen = 0;   // four bits a step, the newest lowest: groups of 8 rows whose page is one
-            // Step `step` to ring slot `slot`: where its rows are, and then the loads, number k
-            // of LOADS each.  Behind the last step no row is there, and the loads bring zeros.
+            // Step `step` to ring slot `slot`: the table's entry, where the rows are, and then the
+            // loads, number k of LOADS each.  Behind the last step no row is there, and the
+            // loads bring zeros.
             Rsrc rs;
             unsigned dst;
-            auto locate = [&](int step, int slot) {
+            auto look_up = [&](int step) {
                 if (__builtin_expect((unsigned)(step - first) >= known, 0)) {
                     first = step;
                     known = wide ? 64 : 16;
@@ -275,6 +276,8 @@ latent_attention_kernel(Shape s) {
                     wait_vmcnt_lds<0>();
                     place_of = (unsigned)page < (unsigned)a.pages ? (int)(((unsigned)page << a.page_shift) + (unsigned)(row & ((1 << a.page_shift) - 1))) : -1;
                 }
+            };
+            auto locate = [&](int step, int slot) {
                 int row, bits;
                 if (wide) {
                     row = __builtin_amdgcn_readlane(place_of, step - first);
@@ -300,39 +303,38 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) x[e] = *reinterpret_cast<const Key *>(tile + koff[e] + c * (E4M3 ? 64 : 128));
             };
-            auto read_values = [&](const unsigned char *tile, int e, Value(&x)[1]) {
-                const unsigned char *v = tile + (e & 1) * 16 * ROWB + (e >> 2) * (E4M3 ? 64 : 128);
-                if constexpr (E4M3) x[0] = lds_transposed8(v + voff[e >> 1 & 1][0]);
-                else x[0] = __builtin_shufflevector(lds_transposed4(v + voff[e >> 1 & 1][0]), lds_transposed4(v + voff[e >> 1 & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
-            };
-            // Scores of a step (16 by 16 a wave), and beside them the columns' sums of the step
-            // before (tile, with weights pf) and the loads of a later one: fragments are read a
-            // ninth ahead of their use.
-            f32x4 y[2];
-            bf16x8 pf[2];
-            auto turn = [&](auto both, const unsigned char *tile, const unsigned char *next) {
-                constexpr bool SUM = decltype(both)::value;
-                Key kf[2][2];
-                Value vf[2][1];
-                y[0] = y[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-                read_keys(next, 0, kf[0]);
+            auto read_values = [&](const unsigned char *tile, int d, Value(&x)[2]) {
 #pragma unroll
-                for (int c = 0; c < 9; ++c) {
-                    if (c < 8) read_keys(next, c + 1, kf[(c + 1) & 1]);
-                    if (SUM && c < 8) read_values(tile, c, vf[c & 1]);
-                    if (SUM) load(c);
-                    arrived(kf[c & 1]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) y[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[c & 1][e]), qf[2 * c + e], y[e], 0, 0, 0);
-                    if (SUM && c >= 1) {
-                        arrived(vf[(c - 1) & 1]);
-                        acc[(c - 1) >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[(c - 1) & 1][0]), pf[(c - 1) & 1], acc[(c - 1) >> 1], 0, 0, 0);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const unsigned char *v = tile + e * 16 * ROWB + (d >> 1) * (E4M3 ? 64 : 128);
+                    if constexpr (E4M3) x[e] = lds_transposed8(v + voff[d & 1][0]);
+                    else x[e] = __builtin_shufflevector(lds_transposed4(v + voff[d & 1][0]), lds_transposed4(v + voff[d & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
                 }
             };
-            // Their weights to where all four waves read them.  Behind the last step the
-            // scores are those of zeros, and unused.
-            auto weigh = [&](int row0, unsigned bits, int parity, unsigned number) {
+            // Ninth c of the scores of a step, 16 by 16 a wave; the keys are read a ninth ahead.
+            f32x4 y[2];
+            Key kf[2][2];
+            auto score = [&](const unsigned char *next, int c) {
+                if (c < 8) read_keys(next, c + 1, kf[(c + 1) & 1]);
+                arrived(kf[c & 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) y[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[c & 1][e]), qf[2 * c + e], y[e], 0, 0, 0);
+            };
+            auto first_keys = [&](const unsigned char *next) {
+                y[0] = y[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                read_keys(next, 0, kf[0]);
+            };
+            // Columns 32 d .. + 31 of the wave's quarter: their sums of a step.
+            bf16x8 pf[2];
+            Value vf[2][2];
+            auto sum = [&](int d) {
+                arrived(vf[d & 1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[d & 1][e]), pf[e], acc[d], 0, 0, 0);
+            };
+            // The scores' weights to where all four waves read them, in three parts.  Behind
+            // the last step the scores are those of zeros, and unused.
+            auto scaled = [&](int row0, unsigned bits) {
                 f32x4 z = (y[0] + y[1]) * factor;
                 if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
                     const bool held = bits >> ((cs & 1) * 2 + (g4 >> 1)) & 1u;
@@ -340,16 +342,21 @@ latent_attention_kernel(Shape s) {
                     for (int r = 0; r < 4; ++r) z[r] = held && row0 + (cs & 1) * 16 + g4 * 4 + r < lim ? z[r] : -__builtin_inff();
                 }
                 last = z;
-                if (__builtin_expect(__any(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > own_most), 0)) {
+            };
+            auto warn = [&](int parity, unsigned number) {
+                if (__builtin_expect(__any(fmaxf(fmaxf(last[0], last[1]), fmaxf(last[2], last[3])) > own_most), 0)) {
                     if (lane == 0) flags[parity] = number;
                 }
-                const uint2 w = to_bf16x4(__builtin_amdgcn_exp2f(z[0] - own_ref), __builtin_amdgcn_exp2f(z[1] - own_ref),
-                                          __builtin_amdgcn_exp2f(z[2] - own_ref), __builtin_amdgcn_exp2f(z[3] - own_ref));
+            };
+            auto weigh = [&](int parity) {
+                const uint2 w = to_bf16x4(__builtin_amdgcn_exp2f(last[0] - own_ref), __builtin_amdgcn_exp2f(last[1] - own_ref),
+                                          __builtin_amdgcn_exp2f(last[2] - own_ref), __builtin_amdgcn_exp2f(last[3] - own_ref));
                 *reinterpret_cast<uint2 *>(exchange + parity * RG * kWeights * 2 + put_at) = w;
             };
 
 #pragma unroll
             for (int k = 0; k < kRing - 1; ++k) {
+                look_up(at + k);
                 locate(at + k, k);
 #pragma unroll
                 for (int e = 0; e < LOADS; ++e) load(e);
@@ -357,8 +364,12 @@ latent_attention_kernel(Shape s) {
             wait_vmcnt_lds<2 * LOADS>();
             barrier_nofence();
             ++epoch;
-            turn(std::false_type{}, lds_raw, lds_raw);
-            weigh(at * kTile, seen >> 8 & 15u, 0, epoch);
+            first_keys(lds_raw);
+#pragma unroll
+            for (int c = 0; c < 9; ++c) score(lds_raw, c);
+            scaled(at * kTile, seen >> 8 & 15u);
+            warn(0, epoch);
+            weigh(0);
             int slot = 0;
             for (int k = 0; k < n; ++k) {
                 // the next step's rows are there when the one behind it may be under way
@@ -369,13 +380,20 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v) pf[v] = *reinterpret_cast<const bf16x8 *>(exchange + (k & 1) * RG * kWeights * 2 + (get_at ^ (v * 32)));
                 const unsigned bits = seen >> 8 & 15u, next_bits = seen >> 4 & 15u;
-                // every wave is done with the slot of the step before
-                locate(at + k + kRing - 1, (slot + kRing - 1) & (kRing - 1));
                 const unsigned char *tile = lds_raw + slot * TILE;
+                const int free_slot = (slot + kRing - 1) & (kRing - 1);  // every wave is done with the step before
                 slot = (slot + 1) & (kRing - 1);
                 const unsigned char *next = lds_raw + slot * TILE;
                 const int row0 = (at + k) * kTile;
-
+                look_up(at + k + kRing - 1);
+                first_keys(next);
+                score(next, 0);
+                locate(at + k + kRing - 1, free_slot);
+#pragma unroll
+                for (int c = 1; c < 4; ++c) {
+                    load(c - 1);
+                    score(next, c);
+                }
                 if (__builtin_expect((unsigned)uniform((int)flag) == epoch, 0)) {
                     // a maximum has grown: new weights of all scores, old sums multiplied
                     __syncthreads();
@@ -407,7 +425,6 @@ latent_attention_kernel(Shape s) {
                     __syncthreads();
                 }
                 ++epoch;
-                l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
                 const bool masked = row0 + kTile > lim0 || bits != 15u;
                 if (__builtin_expect(careful && masked, 0)) {
                     // Rows with infinities or NaN that some of the tile's tokens see and some do
@@ -477,8 +494,23 @@ latent_attention_kernel(Shape s) {
                             *reinterpret_cast<unsigned *>(const_cast<unsigned char *>(tile) + __builtin_ctz(f) * ROWB + e * 4) = 0;
                     __syncthreads();
                 }
-                turn(std::true_type{}, tile, next);
-                weigh(row0 + kTile, next_bits, (k + 1) & 1, epoch);
+#pragma unroll
+                for (int c = 4; c < 9; ++c) {
+                    load(c - 1);
+                    if (c >= 7) read_values(tile, c - 7, vf[(c + 1) & 1]);
+                    score(next, c);
+                }
+                load(8);
+                sum(0);
+                scaled(row0 + kTile, next_bits);
+                read_values(tile, 2, vf[0]);
+                sum(1);
+                warn((k + 1) & 1, epoch);
+                read_values(tile, 3, vf[1]);
+                weigh((k + 1) & 1);
+                sum(2);
+                l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
+                sum(3);
             }
             wait_vmcnt_lds<0>();
             __syncthreads();  // the ring is free
