@@ -85,9 +85,10 @@ __device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f3
 
 }  // namespace
 
-// A workgroup takes 32 RG rows, four waves 32 of them: each makes the weights of half
-// of a step's cache rows and half of its own, which all four then read from LDS, and
-// sums its quarter of the 512 columns.  The weights are made a step ahead: one barrier a
+// A workgroup of four waves takes 32 RG rows, 4 / RG waves 32 of them: each makes the
+// weights of half of a step's cache rows and of half of its own (all, if they are two
+// waves), which all of them then read from LDS, and sums its
+// part of the 512 columns.  The weights are made a step ahead: one barrier a
 // step, behind which its weights and the next step's cache rows are there.  A barrier
 // starts all waves at the same point, so that each has to fill its own waits: scores
 // run while the weights come from LDS, sums beside the next weights' vector
@@ -100,19 +101,23 @@ __device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f3
 //
 // Workgroups that hold different heads of the same tokens form a team, which takes
 // its share of all steps together, so that a cache row is read from memory once.
-template <int RG, bool E4M3>
-__global__ void __launch_bounds__(256 * RG) __attribute__((amdgpu_waves_per_eu(groups_of(RG, E4M3) / 256 * RG, groups_of(RG, E4M3) / 256 * RG)))
+template <int RG, int CS, bool E4M3>
+__global__ void __launch_bounds__(64 * RG * CS)
+    __attribute__((amdgpu_waves_per_eu(groups_of(RG, E4M3) / 256 * RG * CS / 4, groups_of(RG, E4M3) / 256 * RG * CS / 4)))
 latent_attention_kernel(Shape s) {
-    constexpr int NW = 4 * RG, R = 32 * RG, ROWB = row_bytes(E4M3), TILE = kTile * ROWB;
+    constexpr int NW = RG * CS, R = 32 * RG, ROWB = row_bytes(E4M3), TILE = kTile * ROWB;
+    constexpr int QR = 3 - CS / 2;                                                       // halves of the 32 rows that a wave scores
     constexpr int WR = kTile / NW, PIECES = ROWB / 16, LOADS = (WR * PIECES + 63) / 64;  // rows that a wave brings
-    constexpr int DB = 4;                                                               // blocks of 32 columns a wave
-    static_assert(LOADS <= 9, "one beside each ninth of the scores");
+    constexpr int DB = 16 / CS;                                                         // blocks of 32 columns a wave
+    constexpr bool ROOMY = groups_of(RG, E4M3) / 256 * NW == 4;  // a wave a SIMD
+    constexpr int KD = ROOMY ? 4 : 2, VD = ROOMY ? 3 : 2, YN = ROOMY ? 2 : 1;  
     using Key = std::conditional_t<E4M3, i32x2, u32x4>;  // fragments as they lie in LDS
     using Value = std::conditional_t<E4M3, i32x2, s16x8>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
     const LatentArgs &a = s.a;
     const int t = threadIdx.x, lane = t & 63, wave = uniform(t >> 6);
-    const int rg = wave >> 2, cs = wave & 3;
+    const int rg = wave / CS, cs = wave % CS;
+    const int step_half = cs & 1;
     unsigned char *const exchange = lds_raw + kRing * TILE;
     unsigned *const flags = reinterpret_cast<unsigned *>(exchange + 2 * RG * kWeights * 2);
     // neighbouring groups on one XCD
@@ -168,7 +173,7 @@ latent_attention_kernel(Shape s) {
     unsigned koff[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int row = (cs & 1) * 16 + l15;
+        const int row = step_half * 16 + l15;
         koff[j] = (unsigned)(row * ROWB) + (unsigned)(E4M3 ? ((j * 2 + (g4 >> 1)) ^ swz4(row)) * 16 + (g4 & 1) * 8
                                                            : ((j * 4 + g4) ^ swz8(row)) * 16);
     }
@@ -192,8 +197,8 @@ latent_attention_kernel(Shape s) {
     // Weights of 16 cache rows by 16 rows, four of a row a lane: into a row's 32 in the
     // order in which the second product's lanes take eight of them, the row's four
     // 16-byte pieces permuted.  Scores likewise, in the order of the cache rows.
-    const int own_row = (cs >> 1) * 16 + l15;
-    const unsigned put_at = (unsigned)((rg * 32 + own_row) * 64 + ((((cs & 1) * 2 + (g4 & 1)) ^ ((own_row >> 2) & 3)) * 16) + (g4 >> 1) * 8);
+    const int own_row = (CS == 4 ? (cs >> 1) * 16 : 0) + l15;  // and, with both halves, own_row + 16
+    const unsigned put_at = (unsigned)((rg * 32 + own_row) * 64 + (((step_half * 2 + (g4 & 1)) ^ ((own_row >> 2) & 3)) * 16) + (g4 >> 1) * 8);
     const unsigned get_at = (unsigned)((rg * 32 + l31) * 64 + ((half ^ ((l31 >> 2) & 3)) * 16));
     const unsigned ring = (unsigned)uniform((int)lds_address(lds_raw + wave * WR * ROWB));
     const bool wide = a.page_shift >= 5;
@@ -220,24 +225,26 @@ latent_attention_kernel(Shape s) {
             tok += j0;
             return ok;
         };
-        // how many cache rows the row whose weights this lane makes sees
-        int lim;
-        {
+        // how many cache rows the rows whose weights this lane makes see
+        int lim[QR];
+#pragma unroll
+        for (int x = 0; x < QR; ++x) {
             int tok, head;
-            lim = place(rg * 32 + own_row, tok, head) ? max(before + tok + 1, 0) : 0;
+            lim[x] = place(rg * 32 + own_row + 16 * x, tok, head) ? max(before + tok + 1, 0) : 0;
         }
 
         // queries: fragments of 16 rows by 32 values
-        bf16x8 qf[18];
-        {
+        bf16x8 qf[QR][18];
+#pragma unroll
+        for (int x = 0; x < QR; ++x) {
             int qt, qh;
-            const bool ok = place(rg * 32 + own_row, qt, qh);
+            const bool ok = place(rg * 32 + own_row + 16 * x, qt, qh);
             const uint16_t *p = a.q + ((size_t)(q.first + (ok ? qt : 0)) * a.H + (ok ? qh : 0)) * SKG_LATENT_ROW + g4 * 8;
 #pragma unroll
             for (int k = 0; k < 18; ++k) {
                 u32x4 v{0, 0, 0, 0};
                 if (ok) v = *reinterpret_cast<const u32x4 *>(p + k * 32);
-                qf[k] = __builtin_bit_cast(bf16x8, v);
+                qf[x][k] = __builtin_bit_cast(bf16x8, v);
             }
         }
         // here, so that the compiler waits for no load inside the loop over the ring
@@ -253,15 +260,23 @@ latent_attention_kernel(Shape s) {
                 for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
             m = -__builtin_inff();
             l = 0.0f;
-            float own_ref = 0.0f, own_most = -__builtin_inff();  // of row own_row: m, or 0 where there is none; m + 8
-            f32x4 last;                                          // this lane's scores of the step to come
+            float own_ref[QR], own_most[QR];  // of this lane's rows: m, or 0 where there is none; m + 8
+            f32x4 last[QR];                   // and scores of the step to come
+#pragma unroll
+            for (int x = 0; x < QR; ++x) {
+                own_ref[x] = 0.0f;
+                own_most[x] = -__builtin_inff();
+            }
 
-            // where the rows of 64 steps lie in the cache (of 16, by eights, where a step may
-            // have several pages), one a lane; -1: nowhere
-            int first = 0, place_of = -1;
+            // Where this wave's rows of 64 steps lie in the cache, and how many bytes of them
+            // there are, one step a lane; of 16 steps in fours where a step may have several
+            // pages.  held: whose page is one of the cache's, a bit a lane.
+            int first = 0;
             unsigned known = 0;  // steps in it
-            unsigned seen = 0;   // four bits a step, the newest lowest: groups of 8 rows whose page is one
-            // Step `step` to ring slot `slot`: the table's entry, where the rows are, and then the
+            unsigned place_lo = 0, place_hi = 0, place_bytes = 0;
+            unsigned long long held = 0;
+            unsigned seen = 0;  // four bits a step, the newest lowest: groups of 8 rows whose page is one
+            // Step `step` to ring slot `slot`: the table's entries, where the rows are, and then the
             // loads, number k of LOADS each.  Behind the last step no row is there, and the
             // loads bring zeros.
             Rsrc rs;
@@ -272,28 +287,24 @@ latent_attention_kernel(Shape s) {
                     known = wide ? 64 : 16;
                     const long row = (long)step * kTile + lane * (wide ? kTile : 8);
                     const long e = row >> a.page_shift;
-                    int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
+                    const int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
                     wait_vmcnt_lds<0>();
-                    place_of = (unsigned)page < (unsigned)a.pages ? (int)(((unsigned)page << a.page_shift) + (unsigned)(row & ((1 << a.page_shift) - 1))) : -1;
+                    const bool ok = (unsigned)page < (unsigned)a.pages;
+                    held = __ballot(ok);
+                    const int in_step = wide ? WR * wave : WR * wave & 7;
+                    const size_t at_row = ((size_t)(ok ? page : 0) << a.page_shift) + (size_t)(row & ((1 << a.page_shift) - 1)) + in_step;
+                    const size_t p = (size_t)(uintptr_t)a.cache + at_row * ROWB;
+                    place_lo = (unsigned)p;
+                    place_hi = (unsigned)(p >> 32);
+                    place_bytes = ok ? (unsigned)(min(max((long)most - (row + in_step), 0L), (long)WR) * ROWB) : 0u;
                 }
             };
             auto locate = [&](int step, int slot) {
-                int row, bits;
-                if (wide) {
-                    row = __builtin_amdgcn_readlane(place_of, step - first);
-                    bits = row >= 0 ? 15 : 0;
-                    row += WR * wave;
-                } else {
-                    const int l0 = (step - first) * 4;
-                    bits = 0;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) bits |= (__builtin_amdgcn_readlane(place_of, l0 + w) >= 0 ? 1 : 0) << w;
-                    row = __builtin_amdgcn_readlane(place_of, l0 + (WR * wave >> 3)) + (WR * wave & 7);
-                }
-                seen = seen << 4 | (unsigned)bits;
-                row = uniform(row);
-                const int rows = uniform(bits >> (WR * wave >> 3) & 1 ? min(max(most - step * kTile - WR * wave, 0), WR) : 0);
-                rs = make_rsrc(a.cache + (rows ? (size_t)(unsigned)row * ROWB : 0), (unsigned)(rows * ROWB));
+                const int i0 = (step - first) * (wide ? 1 : 4), own = i0 + (wide ? 0 : WR * wave >> 3);
+                const unsigned bits = (unsigned)(held >> i0) & (wide ? 1u : 15u);
+                seen = seen << 4 | (wide ? bits * 15u : bits);
+                const size_t p = (size_t)(unsigned)__builtin_amdgcn_readlane((int)place_hi, own) << 32 | (unsigned)__builtin_amdgcn_readlane((int)place_lo, own);
+                rs = make_rsrc(reinterpret_cast<const void *>(p), (unsigned)__builtin_amdgcn_readlane((int)place_bytes, own));
                 dst = ring + slot * TILE;
             };
             auto load = [&](int k) {
@@ -311,47 +322,61 @@ latent_attention_kernel(Shape s) {
                     else x[e] = __builtin_shufflevector(lds_transposed4(v + voff[d & 1][0]), lds_transposed4(v + voff[d & 1][1]), 0, 1, 2, 3, 4, 5, 6, 7);
                 }
             };
-            // Ninth c of the scores of a step, 16 by 16 a wave; the keys are read a ninth ahead.
-            f32x4 y[2];
-            Key kf[2][2];
+            // Ninth c of the scores of a step, 16 by 16 QR a wave; the keys are read ahead.
+            f32x4 y[QR][YN];
+            Key kf[KD][2];
             auto score = [&](const unsigned char *next, int c) {
-                if (c < 8) read_keys(next, c + 1, kf[(c + 1) & 1]);
-                arrived(kf[c & 1]);
+                if (c + KD - 1 < 9) read_keys(next, c + KD - 1, kf[(c + KD - 1) % KD]);
+                arrived(kf[c % KD]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) y[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[c & 1][e]), qf[2 * c + e], y[e], 0, 0, 0);
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int x = 0; x < QR; ++x)
+                        y[x][e % YN] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kf[c % KD][e]), qf[x][2 * c + e], y[x][e % YN], 0, 0, 0);
             };
             auto first_keys = [&](const unsigned char *next) {
-                y[0] = y[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-                read_keys(next, 0, kf[0]);
+#pragma unroll
+                for (int x = 0; x < QR; ++x) y[x][0] = y[x][YN - 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < KD - 1; ++c) read_keys(next, c, kf[c]);
             };
-            // Columns 32 d .. + 31 of the wave's quarter: their sums of a step.
+            // Columns 32 d .. + 31 of the wave's part: their sums of a step.
             bf16x8 pf[2];
-            Value vf[2][2];
+            Value vf[VD][2];
             auto sum = [&](int d) {
-                arrived(vf[d & 1]);
+                arrived(vf[d % VD]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[d & 1][e]), pf[e], acc[d], 0, 0, 0);
+                for (int e = 0; e < 2; ++e) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[d % VD][e]), pf[e], acc[d], 0, 0, 0);
             };
-            // The scores' weights to where all four waves read them, in three parts.  Behind
-            // the last step the scores are those of zeros, and unused.
+            // The scores' weights to where all waves read them, in three parts.  Behind the
+            // last step the scores are those of zeros, and unused.
             auto scaled = [&](int row0, unsigned bits) {
-                f32x4 z = (y[0] + y[1]) * factor;
-                if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
-                    const bool held = bits >> ((cs & 1) * 2 + (g4 >> 1)) & 1u;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) z[r] = held && row0 + (cs & 1) * 16 + g4 * 4 + r < lim ? z[r] : -__builtin_inff();
+                for (int x = 0; x < QR; ++x) last[x] = (YN == 2 ? y[x][0] + y[x][YN - 1] : y[x][0]) * factor;
+                if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
+                    const bool held = bits >> (step_half * 2 + (g4 >> 1)) & 1u;
+#pragma unroll
+                    for (int x = 0; x < QR; ++x)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) last[x][r] = held && row0 + step_half * 16 + g4 * 4 + r < lim[x] ? last[x][r] : -__builtin_inff();
                 }
-                last = z;
             };
             auto warn = [&](int parity, unsigned number) {
-                if (__builtin_expect(__any(fmaxf(fmaxf(last[0], last[1]), fmaxf(last[2], last[3])) > own_most), 0)) {
+                bool over = false;
+#pragma unroll
+                for (int x = 0; x < QR; ++x) over |= fmaxf(fmaxf(last[x][0], last[x][1]), fmaxf(last[x][2], last[x][3])) > own_most[x];
+                if (__builtin_expect(__any(over), 0)) {
                     if (lane == 0) flags[parity] = number;
                 }
             };
             auto weigh = [&](int parity) {
-                const uint2 w = to_bf16x4(__builtin_amdgcn_exp2f(last[0] - own_ref), __builtin_amdgcn_exp2f(last[1] - own_ref),
-                                          __builtin_amdgcn_exp2f(last[2] - own_ref), __builtin_amdgcn_exp2f(last[3] - own_ref));
-                *reinterpret_cast<uint2 *>(exchange + parity * RG * kWeights * 2 + put_at) = w;
+#pragma unroll
+                for (int x = 0; x < QR; ++x) {
+                    float w[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) w[r] = __builtin_amdgcn_exp2f(last[x][r] - own_ref[x]);
+                    *reinterpret_cast<uint2 *>(exchange + parity * RG * kWeights * 2 + put_at + x * 16 * 64) = to_bf16x4(w[0], w[1], w[2], w[3]);
+                }
             };
 
 #pragma unroll
@@ -397,8 +422,12 @@ latent_attention_kernel(Shape s) {
                 if (__builtin_expect((unsigned)uniform((int)flag) == epoch, 0)) {
                     // a maximum has grown: new weights of all scores, old sums multiplied
                     __syncthreads();
+                    const int lane = here(threadIdx.x & 63), half = lane >> 5, l31 = lane & 31, l15 = lane & 15, g4 = lane >> 4;
+                    const int own_row = (CS == 4 ? (cs >> 1) * 16 : 0) + l15;
                     float *all = reinterpret_cast<float *>(exchange);
-                    *reinterpret_cast<f32x4 *>(all + (rg * 32 + own_row) * 32 + ((((cs & 1) * 4 + g4) ^ (own_row & 7)) * 4)) = last;
+#pragma unroll
+                    for (int x = 0; x < QR; ++x)
+                        *reinterpret_cast<f32x4 *>(all + (rg * 32 + own_row + 16 * x) * 32 + (((step_half * 4 + g4) ^ (own_row & 7)) * 4)) = last[x];
                     __syncthreads();
                     float z[16];
 #pragma unroll
@@ -420,8 +449,11 @@ latent_attention_kernel(Shape s) {
                     for (int r = 0; r < 16; ++r) z[r] = __builtin_amdgcn_exp2f(z[r] - ref);
                     pf[0] = to_bf16x8(z);
                     pf[1] = to_bf16x8(z + 8);
-                    own_ref = __shfl(ref, own_row, 64);
-                    own_most = __shfl(m, own_row, 64) + 8.0f;
+#pragma unroll
+                    for (int x = 0; x < QR; ++x) {
+                        own_ref[x] = __shfl(ref, own_row + 16 * x, 64);
+                        own_most[x] = __shfl(m, own_row + 16 * x, 64) + 8.0f;
+                    }
                     __syncthreads();
                 }
                 ++epoch;
@@ -431,11 +463,12 @@ latent_attention_kernel(Shape s) {
                     // not: their products by vector instructions for those that do, and zeros
                     // in their place for the matrix instruction.
                     __syncthreads();
+                    const int t = here(threadIdx.x), lane = t & 63, half = lane >> 5, l31 = lane & 31;
                     unsigned char *bad_rows = reinterpret_cast<unsigned char *>(flags + 4);
                     bool bad = false;
                     for (int e = 0; e < ROWB * 512 / 576 / 8 / 4; ++e) {
                         const unsigned w = *reinterpret_cast<const unsigned *>(
-                            tile + (cs * 8 + (lane >> 3)) * ROWB + (lane & 7) * (ROWB * 512 / 576 / 8) + e * 4);
+                            tile + ((wave & 3) * 8 + (lane >> 3)) * ROWB + (lane & 7) * (ROWB * 512 / 576 / 8) + e * 4);
                         if constexpr (E4M3) {
                             const unsigned u = w & 0x7F7F7F7Fu;
                             bad |= ((u + 0x01010101u) & 0x80808080u) != 0;
@@ -447,7 +480,7 @@ latent_attention_kernel(Shape s) {
                     unsigned rows8 = 0;
 #pragma unroll
                     for (int r = 0; r < 8; ++r) rows8 |= ((any >> (8 * r)) & 0xFFull ? 1u : 0u) << r;
-                    if (lane == 0) bad_rows[cs] = (unsigned char)rows8;  // each four waves the same
+                    if (lane == 0) bad_rows[wave & 3] = (unsigned char)rows8;  // each four waves the same
                     __syncthreads();
                     const unsigned flagged = (unsigned)uniform((int)flags[4]);
                     const int col_lim = [&] {
@@ -486,31 +519,31 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
                                 for (int u = 0; u < 4; ++u)
                                     if (sees) acc[d][4 * v + u] = __builtin_fmaf(w, y[u], acc[d][4 * v + u]);
+                                __builtin_amdgcn_sched_barrier(0);  // one after another: rare, and short of registers
                             }
                     }
                     __syncthreads();
                     for (unsigned f = flagged; f; f &= f - 1)
-                        for (int e = t; e < ROWB * 512 / 576 / 4; e += 256 * RG)
+                        for (int e = t; e < ROWB * 512 / 576 / 4; e += 64 * NW)
                             *reinterpret_cast<unsigned *>(const_cast<unsigned char *>(tile) + __builtin_ctz(f) * ROWB + e * 4) = 0;
                     __syncthreads();
                 }
 #pragma unroll
                 for (int c = 4; c < 9; ++c) {
                     load(c - 1);
-                    if (c >= 7) read_values(tile, c - 7, vf[(c + 1) & 1]);
+                    if (c >= 10 - VD) read_values(tile, c - (10 - VD), vf[c - (10 - VD)]);
                     score(next, c);
                 }
                 load(8);
-                sum(0);
-                scaled(row0 + kTile, next_bits);
-                read_values(tile, 2, vf[0]);
-                sum(1);
-                warn((k + 1) & 1, epoch);
-                read_values(tile, 3, vf[1]);
-                weigh((k + 1) & 1);
-                sum(2);
-                l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
-                sum(3);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    if (d + VD - 1 < DB) read_values(tile, d + VD - 1, vf[(d + VD - 1) % VD]);
+                    sum(d);
+                    if (d == 0) scaled(row0 + kTile, next_bits);
+                    if (d == 1) warn((k + 1) & 1, epoch);
+                    if (d == 2) weigh((k + 1) & 1);
+                    if (d == 2) l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
+                }
             }
             wait_vmcnt_lds<0>();
             __syncthreads();  // the ring is free
@@ -646,15 +679,15 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
 
 namespace {
 
-template <int RG, bool E4M3>
+template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 4};
     static std::atomic<unsigned long long> done{0};
     constexpr size_t lds = lds_bytes<RG, E4M3>();
-    const hipError_t e = allow_dynamic_lds((const void *)latent_attention_kernel<RG, E4M3>, lds, done);
+    const hipError_t e = allow_dynamic_lds((const void *)latent_attention_kernel<RG, CS, E4M3>, lds, done);
     if (e != hipSuccess) return (int)e;
-    hipLaunchKernelGGL((latent_attention_kernel<RG, E4M3>), dim3(groups_of(RG, E4M3)), dim3(256 * RG), lds, stream, s);
+    hipLaunchKernelGGL((latent_attention_kernel<RG, CS, E4M3>), dim3(groups_of(RG, E4M3)), dim3(64 * RG * CS), lds, stream, s);
     const hipError_t f = hipGetLastError();
     if (f != hipSuccess) return (int)f;
     hipLaunchKernelGGL((latent_combine_kernel<RG>), dim3(groups_of(RG, E4M3), 16), dim3(256), 0, stream, s, a.scale);
@@ -663,7 +696,7 @@ int go(const LatentArgs &a, hipStream_t stream) {
 
 template <bool E4M3>
 int by_rows(const LatentArgs &a, int rows, hipStream_t stream) {
-    return rows == 32 ? go<1, E4M3>(a, stream) : go<2, E4M3>(a, stream);
+    return rows == 32 ? go<1, 4, E4M3>(a, stream) : go<2, 2, E4M3>(a, stream);
 }
 
 }  // namespace

@@ -62,6 +62,12 @@ __device__ __forceinline__ int find_sequence(const long *pre, int B, long x) {
 
 // ---------------------------------------------------------------- tiles in LDS
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+// v, of which nothing is computed before this point: in a rare path, so that no
+// register holds its addresses everywhere else.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 __device__ __forceinline__ Tokens uniform(Tokens q) { return {uniform(q.first), uniform(q.n)}; }
 
 // An address in LDS, for the loads below.
