@@ -91,11 +91,13 @@ __device__ __forceinline__ void ring_load16(Rsrc r, unsigned dst, unsigned off) 
 // different places of 16 bytes.  By the rows' size: 576 bytes (swz4), 1152 or 128 bytes, an odd
 // multiple of 128 (swz8), 512 bytes (swz16).
 __device__ __forceinline__ int swz4(int r) { return (r >> 2) & 3; }
-__device__ __forceinline__ int swz8(int r) {
+// 0, 2, 3, 1: with it rows 0-3 and 12-15 differ from each other in the lowest bit alone.
+__device__ __forceinline__ int swz_quarter(int r) {
     const int x = (r >> 2) & 3;
-    return ((r & 2) << 1) | (((x ^ (x >> 1)) & 1) << 1) | (x >> 1);
+    return (((x ^ (x >> 1)) & 1) << 1) | (x >> 1);
 }
-__device__ __forceinline__ int swz16(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+__device__ __forceinline__ int swz8(int r) { return ((r & 2) << 1) | swz_quarter(r); }
+__device__ __forceinline__ int swz16(int r) { return ((r & 3) << 2) | swz_quarter(r); }
 
 // Four 2-byte values of this lane's column from four rows: lane i of 16 points at
 // row i / 4, columns 4 (i % 4) .. + 3, and gets column i of rows 0 .. 3.

@@ -36,6 +36,7 @@ ROPE_HALVES = 1
 
 _STYLES = {"pairs": ROPE_PAIRS, "halves": ROPE_HALVES}
 _I32 = (torch.int32,)
+_BF = torch.bfloat16
 _CACHE = (torch.bfloat16, torch.float8_e4m3fn)
 
 LatentOut = namedtuple("LatentOut", "latent q_rope")
@@ -61,41 +62,61 @@ def declare(L):
         f.argtypes, f.restype = args, I
 
 
-def _strided(name, t, shape):
-    """Checks bf16 t of `shape` (None: any size) whose last dimension is dense;
-    returns its strides in the others."""
+def _refuse(name, t, shape):
+    """Raises for what _rows and _heads did not take."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
         raise ValueError(f"{name} must be {['any' if s is None else s for s in shape]}, got {list(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
-    # a dimension of one row has whatever stride torch gives it
-    full = t.shape[-1]
-    out = []
-    for d in range(t.dim() - 2, -1, -1):
-        out.append(t.stride(d) if t.shape[d] > 1 else full)
-        full = max(full, out[-1] * t.shape[d])
-    return out[::-1]
+    raise ValueError(f"{name} must be dense in its last dimension")
+
+
+def _rows(name, t, rows, n):
+    """The stride of bf16 t [rows, n] (rows None: any number) from row to row; the
+    last dimension is dense."""
+    if isinstance(t, torch.Tensor) and t.dtype is _BF and t.is_cuda and t.dim() == 2:
+        r, c = t.shape
+        if c == n and (rows is None or r == rows):
+            s, one = t.stride()
+            if one == 1:
+                return s if r > 1 else n  # torch may give one row any stride
+    _refuse(name, t, (rows, n))
+
+
+def _heads(name, t, T, H, n):
+    """The strides of bf16 t [T, H, n] (T, H None: any number) from token to token and
+    from head to head; the last dimension is dense."""
+    if isinstance(t, torch.Tensor) and t.dtype is _BF and t.is_cuda and t.dim() == 3:
+        r, h, c = t.shape
+        if c == n and (T is None or r == T) and (H is None or h == H):
+            s, sh, one = t.stride()
+            if one == 1 or n == 1:
+                if h == 1:
+                    sh = n
+                return (s if r > 1 else max(n, sh * h)), sh
+    _refuse(name, t, (T, H, n))
 
 
 def _batch(cache, table, kv_lens, q_starts, T):
-    _tensor("cache", cache, _CACHE)
-    if cache.dim() != 3 or cache.shape[2] != ROW:
+    if not (cache.dtype in _CACHE and cache.is_cuda and cache.dim() == 3 and cache.is_contiguous()):
+        _tensor("cache", cache, _CACHE)
+    pages, page, row = cache.shape if cache.dim() == 3 else (0, 0, 0)
+    if row != ROW:
         raise ValueError(f"cache must be [pages, page_size, {ROW}], got {list(cache.shape)}")
     _tensor("table", table, _I32)
     if table.dim() != 2:
         raise ValueError("table must be [B, table_width]")
-    B = table.shape[0]
+    B, W = table.shape
     _tensor("kv_lens", kv_lens, _I32, (B,))
     if q_starts is not None:
         _tensor("q_starts", q_starts, _I32, (B + 1,))
     elif T != B:
         raise ValueError(f"without q_starts every sequence has one new token, got {T} for {B} sequences")
-    return LatentBatch(table.data_ptr(), kv_lens.data_ptr(), _c._addr(q_starts), _count(B), _count(T),
-                       _count(table.shape[1]), _count(cache.shape[1]), _count(cache.shape[0]))
+    _count(max(B, T, W, page, pages))
+    return LatentBatch(table.data_ptr(), kv_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
+                       B, T, W, page, pages)
 
 
 def _cache_scale(cache, scale):
@@ -117,7 +138,7 @@ def latent_append(kv, cache, table, kv_lens, rotations, q_starts=None, weight=No
     a row.  rope: "pairs" or "halves".  Returns LatentOut(latent, q_rope): latent
     = the rows in bf16 [T, 576] if asked for, q_rope the rotated queries if given."""
     style = _choice("rope", rope, _STYLES)
-    (kv_stride,) = _strided("kv", kv, (None, ROW))
+    kv_stride = _rows("kv", kv, None, ROW)
     T = kv.shape[0]
     batch = _batch(cache, table, kv_lens, q_starts, T)
     dtype = _cache_scale(cache, scale)
@@ -126,13 +147,18 @@ def latent_append(kv, cache, table, kv_lens, rotations, q_starts=None, weight=No
         raise ValueError(f"rotations must be [rows, {ROPE}]")
     if weight is not None:
         _tensor("weight", weight, _BF16, (LATENT,))
-    H, qs, os = 0, (0, 0), (0, 0)
+    H = qt = qh = ot = oh = 0
+    qp = op = None
     if q_rope is not None:
-        qs = _strided("q_rope", q_rope, (T, None, ROPE))
+        qt, qh = _heads("q_rope", q_rope, T, None, ROPE)
         H = q_rope.shape[1]
         if q_rope_out is None:
             q_rope_out = _c._empty((T, H, ROPE), torch.bfloat16, kv.device, stream)
-        os = _strided("q_rope_out", q_rope_out, (T, H, ROPE))
+            ot, oh = H * ROPE, ROPE
+        else:
+            ot, oh = _heads("q_rope_out", q_rope_out, T, H, ROPE)
+        if H:
+            qp, op = q_rope.data_ptr(), q_rope_out.data_ptr()
     elif q_rope_out is not None:
         raise ValueError("q_rope_out needs a q_rope")
     out = _c._empty((T, ROW), torch.bfloat16, kv.device, stream) if latent else None
@@ -140,7 +166,7 @@ def latent_append(kv, cache, table, kv_lens, rotations, q_starts=None, weight=No
     rc = _c._launch(_same_device(kv, cache, table, kv_lens, q_starts, rotations, weight, scale, q_rope, q_rope_out),
                     stream, _c._load().skinny_latent_append, batch, kv.data_ptr(), kv_stride, p(weight), eps,
                     rotations.data_ptr(), _count(rotations.shape[0]), style, cache.data_ptr(), dtype, p(scale),
-                    p(out), p(q_rope) if H else None, *qs, p(q_rope_out) if H else None, *os, H)
+                    p(out), qp, qt, qh, op, ot, oh, H)
     if rc:
         _c._check(rc, f"skinny_latent_append(T={T}, H={H}, {cache.dtype}, {rope})")
     return LatentOut(out, q_rope_out)
@@ -184,7 +210,7 @@ def latent_attention_expanded(q, kv, k_rope, q_starts, softmax_scale, kv_starts=
     if kv.dim() != 3 or tuple(kv.shape[1:]) != (H, NOPE + V):
         raise ValueError(f"kv must be [S, {H}, {NOPE + V}], got {list(kv.shape)}")
     S = kv.shape[0]
-    (rs,) = _strided("k_rope", k_rope, (S, ROPE))
+    rs = _rows("k_rope", k_rope, S, ROPE)
     _tensor("q_starts", q_starts, _I32)
     if q_starts.dim() != 1 or q_starts.shape[0] < 1:
         raise ValueError("q_starts must be [B + 1]")
@@ -213,13 +239,13 @@ def heads_gemm(x, W, out=None, stream=None):
     if W.dim() != 3:
         raise ValueError("W must be [H, N, K]")
     H, N, K = W.shape
-    xs = _strided("x", x, (None, H, K))
+    xs = _heads("x", x, None, H, K)
     T = x.shape[0]
     if out is None:
         out = _c._empty((T, H, N), torch.bfloat16, x.device, stream)
         os = (H * N, N)
     else:
-        os = _strided("out", out, (T, H, N))
+        os = _heads("out", out, T, H, N)
     rc = _c._launch(_same_device(x, W, out), stream, _c._load().skinny_heads_gemm, x.data_ptr(), *xs, W.data_ptr(),
                     out.data_ptr(), *os, _count(T), _count(H), _count(N), _count(K))
     if rc:
