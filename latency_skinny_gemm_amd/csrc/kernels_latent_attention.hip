@@ -24,12 +24,14 @@ struct Shape {
     LatentArgs a;
     int tp;         // tokens a row tile
     int hg;         // head groups (row tiles a token, if it has more heads than a tile rows)
+    int teams;      // groups that hold all head groups of some tokens
     int min_share;  // least number of steps a workgroup takes
+    int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
 
-// A row tile that ends in other workgroups' shares: its parts.
+// A row tile that begins in `group`'s share: how many groups' shares it reaches over.
 struct Shared {
-    int b, i, g, parts;
+    int b, i, group, parts;
 };
 
 template <int RG>
@@ -122,28 +124,39 @@ latent_attention_kernel(Shape s) {
     unsigned *const flags = reinterpret_cast<unsigned *>(exchange + 2 * RG * kWeights * 2);
     // neighbouring groups on one XCD
     const int G = gridDim.x, group = (int)(blockIdx.x & 7) * (G / 8) + (int)(blockIdx.x >> 3);
-    const int teams = G / s.hg, team = group / s.hg, g = group - team * s.hg;
+    const int team = group / s.hg, g = group - team * s.hg;
     const int cap = (int)min((long)a.W << a.page_shift, 0x7FFFFFFFL - 64);
     auto length = [&](int b) { return min(max(a.kv_lens[b], 0), cap); };
 
+    Shared *const records = reinterpret_cast<Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>());
+
     // ---- this team's share of all steps
     long *pre = reinterpret_cast<long *>(lds_raw);
-    block_prefix<NW>(a.B, pre, reinterpret_cast<long *>(exchange), [&](int b) {
-        const Tokens q = new_tokens(a.q_starts, b, a.T);
-        return steps_before(length(b) - q.n, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
-    });
-    const long total = pre[a.B], share = max((long)s.min_share, (total + teams - 1) / teams);
-    const long from = team * share;
-    long left = team < teams ? min(total, from + share) - from : 0;
-    int b = 0, i = 0;
+    int b = 0, i = 0, before = 0, at = 0;  // sequence, row tile and its first step; rows before the sequence's new ones
     Tokens q{0, 0};
-    int before = 0;
-    int at = 0;  // first step in the row tile
+    long total, start = 0;  // the start of b's steps
+    if (a.B == 1) {
+        q = uniform(new_tokens(a.q_starts, 0, a.T));
+        before = uniform(length(0)) - q.n;
+        total = steps_before(before, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
+    } else {
+        block_prefix<NW>(a.B, pre, reinterpret_cast<long *>(exchange), [&](int b) {
+            const Tokens q = new_tokens(a.q_starts, b, a.T);
+            return steps_before(length(b) - q.n, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
+        });
+        total = pre[a.B];
+    }
+    const long share = max((long)s.min_share, total <= 0x7FFFFFFFL - 512 ? (long)((unsigned)(total + s.teams - 1) / (unsigned)s.teams) : (total + s.teams - 1) / s.teams);
+    const long from = team * share;
+    long left = team < s.teams ? min(total, from + share) - from : 0;
     if (left > 0) {
-        b = uniform(find_sequence(pre, a.B, from));
-        q = uniform(new_tokens(a.q_starts, b, a.T));
-        before = uniform(length(b)) - q.n;
-        const long off = from - pre[b];
+        if (a.B > 1) {
+            b = uniform(find_sequence(pre, a.B, from));
+            q = uniform(new_tokens(a.q_starts, b, a.T));
+            before = uniform(length(b)) - q.n;
+            start = pre[b];
+        }
+        const long off = from - start;
         int lo = 0, hi = (q.n + s.tp - 1) / s.tp;
         while (hi - lo > 1) {
             const int step = (hi - lo + 63) / 64, cand = lo + lane * step;
@@ -153,7 +166,7 @@ latent_attention_kernel(Shape s) {
             hi = min(hi, lo + step);
         }
         i = uniform(lo);
-        at = uniform((int)(off - steps_before(before, q.n, s.tp, i)));
+        at = uniform((int)(off - (i ? steps_before(before, q.n, s.tp, i) : 0)));
     }
     __syncthreads();
     if (t < 16) flags[t] = 0;
@@ -235,20 +248,51 @@ latent_attention_kernel(Shape s) {
 
         // queries: fragments of 16 rows by 32 values
         bf16x8 qf[QR][18];
+        {
+            const Rsrc rq = make_rsrc(a.q + ((size_t)(q.first + j0) * a.H + (a.H > R ? g * R : 0)) * SKG_LATENT_ROW, R * SKG_LATENT_ROW * 2u);
 #pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            int qt, qh;
-            const bool ok = place(rg * 32 + own_row + 16 * x, qt, qh);
-            const uint16_t *p = a.q + ((size_t)(q.first + (ok ? qt : 0)) * a.H + (ok ? qh : 0)) * SKG_LATENT_ROW + g4 * 8;
+            for (int x = 0; x < QR; ++x) {
+                int qt, qh;
+                const int r = rg * 32 + own_row + 16 * x;  // rows of a tile lie one after another
+                const unsigned off = place(r, qt, qh) ? (unsigned)(r * SKG_LATENT_ROW + g4 * 8) * 2u : kOOB;
 #pragma unroll
-            for (int k = 0; k < 18; ++k) {
-                u32x4 v{0, 0, 0, 0};
-                if (ok) v = *reinterpret_cast<const u32x4 *>(p + k * 32);
-                qf[x][k] = __builtin_bit_cast(bf16x8, v);
+                for (int k = 0; k < 18; ++k) qf[x][k] = __builtin_bit_cast(bf16x8, load16<kCacheDefault>(rq, off + k * 64));
             }
         }
-        // here, so that the compiler waits for no load inside the loop over the ring
-        wait_vmcnt_lds<0>();
+        // Where this wave's rows of 64 steps lie in the cache, and how many bytes of them
+        // there are, one step a lane; of 16 steps in fours where a step may have several
+        // pages.  held: whose page is one of the cache's, a bit a lane.
+        int first = 0;
+        const unsigned known = wide ? 64 : 16;  // steps
+        unsigned place_lo = 0, place_hi = 0, place_bytes = 0;
+        unsigned long long held = 0;
+        auto fill = [&](int step) {
+            const int lane = here(threadIdx.x & 63);
+            first = step;
+            const long row = (long)step * kTile + lane * (wide ? kTile : 8);
+            const long e = row >> a.page_shift;
+            const int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
+            wait_vmcnt_lds<0>();
+            const bool ok = (unsigned)page < (unsigned)a.pages;
+            held = __ballot(ok);
+            const int in_step = wide ? WR * wave : WR * wave & 7;
+            const size_t at_row = ((size_t)(ok ? page : 0) << a.page_shift) + (size_t)(row & ((1 << a.page_shift) - 1)) + in_step;
+            const size_t p = (size_t)(uintptr_t)a.cache + at_row * ROWB;
+            place_lo = (unsigned)p;
+            place_hi = (unsigned)(p >> 32);
+            place_bytes = ok ? (unsigned)(min(max((long)most - (row + in_step), 0L), (long)WR) * ROWB) : 0u;
+        };
+        // Its wait is for the queries as well: the compiler then waits for no load inside the
+        // loop over the ring.
+        fill(at);
+        // The sums take 128 of the 256 registers that vector instructions reach; the queries,
+        // which only the matrix instruction reads, go to the others.
+        if constexpr (QR == 2) {
+#pragma unroll
+            for (int x = 0; x < QR; ++x)
+#pragma unroll
+                for (int k = 0; k < 18; ++k) asm volatile("" : "+a"(qf[x][k]));
+        }
 
         f32x16 acc[DB];
         float m, l;  // of row l31
@@ -268,13 +312,6 @@ latent_attention_kernel(Shape s) {
                 own_most[x] = -__builtin_inff();
             }
 
-            // Where this wave's rows of 64 steps lie in the cache, and how many bytes of them
-            // there are, one step a lane; of 16 steps in fours where a step may have several
-            // pages.  held: whose page is one of the cache's, a bit a lane.
-            int first = 0;
-            unsigned known = 0;  // steps in it
-            unsigned place_lo = 0, place_hi = 0, place_bytes = 0;
-            unsigned long long held = 0;
             unsigned seen = 0;  // four bits a step, the newest lowest: groups of 8 rows whose page is one
             // Step `step` to ring slot `slot`: the table's entries, where the rows are, and then the
             // loads, number k of LOADS each.  Behind the last step no row is there, and the
@@ -282,22 +319,7 @@ latent_attention_kernel(Shape s) {
             Rsrc rs;
             unsigned dst;
             auto look_up = [&](int step) {
-                if (__builtin_expect((unsigned)(step - first) >= known, 0)) {
-                    first = step;
-                    known = wide ? 64 : 16;
-                    const long row = (long)step * kTile + lane * (wide ? kTile : 8);
-                    const long e = row >> a.page_shift;
-                    const int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
-                    wait_vmcnt_lds<0>();
-                    const bool ok = (unsigned)page < (unsigned)a.pages;
-                    held = __ballot(ok);
-                    const int in_step = wide ? WR * wave : WR * wave & 7;
-                    const size_t at_row = ((size_t)(ok ? page : 0) << a.page_shift) + (size_t)(row & ((1 << a.page_shift) - 1)) + in_step;
-                    const size_t p = (size_t)(uintptr_t)a.cache + at_row * ROWB;
-                    place_lo = (unsigned)p;
-                    place_hi = (unsigned)(p >> 32);
-                    place_bytes = ok ? (unsigned)(min(max((long)most - (row + in_step), 0L), (long)WR) * ROWB) : 0u;
-                }
+                if (__builtin_expect((unsigned)(step - first) >= known, 0)) fill(step);
             };
             auto locate = [&](int step, int slot) {
                 const int i0 = (step - first) * (wide ? 1 : 4), own = i0 + (wide ? 0 : WR * wave >> 3);
@@ -565,11 +587,13 @@ latent_attention_kernel(Shape s) {
             __syncthreads();
             if (!uniform((int)some)) break;
             careful = true;
+            fill(at);
         }
         l = other_half_sum(l);
 
         if (at == 0 && n == steps) {
             const float inv = l == 0.0f ? 0.0f : kv_scale / l;
+            const int lane = here(threadIdx.x & 63), half = lane >> 5, l31 = lane & 31;
             int tok, head;
             if (place(rg * 32 + l31, tok, head)) {
                 uint16_t *o = a.out + ((size_t)(q.first + tok) * a.H + head) * SKG_LATENT + cs * DB * 32 + 4 * half;
@@ -582,6 +606,7 @@ latent_attention_kernel(Shape s) {
             }
         } else {
             // a part: the sums in the registers' order, then maxima and sums of weights
+            const int lane = here(threadIdx.x & 63), half = lane >> 5, l31 = lane & 31;
             float *part = a.ws + (2 * (size_t)group + (at == 0 ? 1 : 0)) * part_floats<RG>();
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -594,8 +619,10 @@ latent_attention_kernel(Shape s) {
                 ml[0] = m;
                 ml[1] = l;
             }
-            if (at == 0) mine = Shared{b, i, g, 1 + (int)((steps - n + share - 1) / share)};
+            if (at == 0) mine = Shared{b, i, group, 1 + (int)((steps - n + share - 1) / share)};
         }
+        if (s.by_tile && at == 0 && t == 0)
+            records[b * s.hg + g] = n == steps ? Shared{b, i, group, 1} : mine;
 
         left -= n;
         at = 0;
@@ -608,21 +635,22 @@ latent_attention_kernel(Shape s) {
             before = uniform(length(b)) - q.n;
         }
     }
-    if (t == 0) reinterpret_cast<Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>())[group] = mine;
+    if (!s.by_tile && t == 0) records[group] = mine;
 }
 
-// Row tiles that several workgroups shared.  One workgroup for a group and 32
+// Row tiles that several workgroups shared.  One workgroup for a record and 32
 // columns; a wave adds up every fourth part in the order of the steps, then the
 // waves' sums are added in theirs.
 template <int RG>
-__global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const float *scale) {
+__global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const float *scale, int G) {
     constexpr int R = 32 * RG;
     __shared__ f32x4 sums[4][4][64];
     __shared__ f32x2 stats[4][64];
     const LatentArgs &a = s.a;
-    const int group = blockIdx.x, G = gridDim.x, d = blockIdx.y;
-    const Shared e = reinterpret_cast<const Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>())[group];
+    const int d = blockIdx.y;
+    const Shared e = reinterpret_cast<const Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>())[blockIdx.x];
     if (e.parts < 2) return;
+    const int group = e.group, g = group % s.hg;
     const Tokens q = new_tokens(a.q_starts, e.b, a.T);
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63, half = lane >> 5;
     const float kv_scale = scale ? scale[0] : 1.0f;
@@ -662,7 +690,7 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
             add_part(m, l, one, stats[w][lane], y);
         }
         __syncthreads();
-        int tok = e.i * s.tp, head = e.g * R + r;
+        int tok = e.i * s.tp, head = g * R + r;
         bool live = head < a.H;
         if (a.H <= R) {
             const int x = r / a.H;
@@ -682,15 +710,18 @@ namespace {
 template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 4};
+    constexpr int G = groups_of(RG, E4M3);
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 4, 0};
+    s.teams = G / s.hg;
+    s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
     constexpr size_t lds = lds_bytes<RG, E4M3>();
     const hipError_t e = allow_dynamic_lds((const void *)latent_attention_kernel<RG, CS, E4M3>, lds, done);
     if (e != hipSuccess) return (int)e;
-    hipLaunchKernelGGL((latent_attention_kernel<RG, CS, E4M3>), dim3(groups_of(RG, E4M3)), dim3(64 * RG * CS), lds, stream, s);
+    hipLaunchKernelGGL((latent_attention_kernel<RG, CS, E4M3>), dim3(G), dim3(64 * RG * CS), lds, stream, s);
     const hipError_t f = hipGetLastError();
     if (f != hipSuccess) return (int)f;
-    hipLaunchKernelGGL((latent_combine_kernel<RG>), dim3(groups_of(RG, E4M3), 16), dim3(256), 0, stream, s, a.scale);
+    hipLaunchKernelGGL((latent_combine_kernel<RG>), dim3(s.by_tile ? a.B * s.hg : G, 16), dim3(256), 0, stream, s, a.scale, G);
     return (int)hipGetLastError();
 }
 
