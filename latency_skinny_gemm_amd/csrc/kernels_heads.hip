@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
     auto issue = [&](int step, int slot) {
         const int t = t0 + step * 16, rows = min(max(t1 - t, 0), 16);
         const Rsrc rs = make_rsrc(a.x + (size_t)(rows ? t : t0) * a.xt + (size_t)h * a.xh, rows ? (unsigned)(rows - 1) * row_bytes + KS * 64u : 0u);
-#pragma unroll
-        for (int k = 0; k < LOADS; ++k) ring_load16(rs, ring + slot * SLOT + k * 4096, src[k]);
+        each<LOADS>([&](auto k) { ring_load16<k * 4096>(rs, ring + slot * SLOT, src[k]); });
     };
     const int n_first = n_tile * 128 + wave * 32;
     const uint16_t *w = a.W + ((size_t)h * a.N) * a.K;

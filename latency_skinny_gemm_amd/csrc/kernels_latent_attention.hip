@@ -329,8 +329,11 @@ latent_attention_kernel(Shape s) {
                 rs = make_rsrc(reinterpret_cast<const void *>(p), (unsigned)__builtin_amdgcn_readlane((int)place_bytes, own));
                 dst = ring + slot * TILE;
             };
-            auto load = [&](int k) {
-                if (k < LOADS && ((k + 1) * 64 <= WR * PIECES || lane < WR * PIECES - k * 64)) ring_load16(rs, dst + k * 1024, src[k]);
+            auto load = [&](auto number) {
+                constexpr int k = decltype(number)::value;
+                if constexpr (k < LOADS) {
+                    if ((k + 1) * 64 <= WR * PIECES || lane < WR * PIECES - k * 64) ring_load16<k * 1024>(rs, dst, src[k]);
+                }
             };
             auto read_keys = [&](const unsigned char *tile, int c, Key(&x)[2]) {
 #pragma unroll
@@ -405,8 +408,7 @@ latent_attention_kernel(Shape s) {
             for (int k = 0; k < kRing - 1; ++k) {
                 look_up(at + k);
                 locate(at + k, k);
-#pragma unroll
-                for (int e = 0; e < LOADS; ++e) load(e);
+                each<LOADS>(load);
             }
             wait_vmcnt_lds<2 * LOADS>();
             barrier_nofence();
@@ -436,11 +438,10 @@ latent_attention_kernel(Shape s) {
                 first_keys(next);
                 score(next, 0);
                 locate(at + k + kRing - 1, free_slot);
-#pragma unroll
-                for (int c = 1; c < 4; ++c) {
-                    load(c - 1);
-                    score(next, c);
-                }
+                each<3>([&](auto c) {
+                    load(c);
+                    score(next, c + 1);
+                });
                 if (__builtin_expect((unsigned)uniform((int)flag) == epoch, 0)) {
                     // a maximum has grown: new weights of all scores, old sums multiplied
                     __syncthreads();
@@ -550,13 +551,13 @@ latent_attention_kernel(Shape s) {
                             *reinterpret_cast<unsigned *>(const_cast<unsigned char *>(tile) + __builtin_ctz(f) * ROWB + e * 4) = 0;
                     __syncthreads();
                 }
-#pragma unroll
-                for (int c = 4; c < 9; ++c) {
-                    load(c - 1);
-                    if (c >= 10 - VD) read_values(tile, c - (10 - VD), vf[c - (10 - VD)]);
+                each<5>([&](auto e) {
+                    constexpr int c = decltype(e)::value + 4;
+                    load(std::integral_constant<int, c - 1>{});
+                    if (c >= 10 - VD) read_values(tile, c - (10 - VD), vf[c >= 10 - VD ? c - (10 - VD) : 0]);
                     score(next, c);
-                }
-                load(8);
+                });
+                load(std::integral_constant<int, 8>{});
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     if (d + VD - 1 < DB) read_values(tile, d + VD - 1, vf[(d + VD - 1) % VD]);

@@ -97,9 +97,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
         const Rsrc rk = make_rsrc(a.kv + (at * a.H + h) * (kKvRow / 2), rows ? (unsigned)(rows - 1) * row_bytes + kKvRow : 0u);
         const Rsrc rr = make_rsrc(a.k_rope + at * a.rope_stride, rows ? (unsigned)(rows - 1) * rope_bytes + kRopeRow : 0u);
         const unsigned dst = ring + slot * kSlotBytes;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ring_load16(rk, dst + wave * 8 * kKvRow + k * 1024, src[k]);
-        ring_load16(rr, dst + kStep * kKvRow + wave * 1024, rope_src);
+        each<4>([&](auto k) { ring_load16<k * 1024>(rk, dst + wave * 8 * kKvRow, src[k]); });
+        ring_load16<kStep * kKvRow>(rr, dst + wave * 1024, rope_src);
     };
 
     unsigned char *flags = lds_raw + kSlots * kSlotBytes;

@@ -1,6 +1,8 @@
 // latent_common.h -- device helpers shared by the kernels of latent attention.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace skg {
@@ -10,6 +12,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// f(0), f(1), .. f(N - 1), the numbers as types.
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (N > 0) {
+        each<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
+}
 
 // ---------------------------------------------------------------- sequences
 // New tokens of sequence b, their number and the first, within [0, T].
@@ -74,14 +85,15 @@ __device__ __forceinline__ Tokens uniform(Tokens q) { return {uniform(q.first), 
 __device__ __forceinline__ unsigned lds_address(const unsigned char *p) {
     return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const unsigned char *)p;
 }
-// 16 bytes a lane from a buffer straight into LDS, at dst + 16 * lane (dst uniform).
+// 16 bytes a lane from a buffer straight into LDS, at dst + AT + 16 * lane (dst uniform).
 // Written as an instruction: beside the builtin, the compiler waits for every such
 // load that is under way before a transposed read (vmcnt(0) in each step of the
 // ring).  It writes no register but m0, which nothing else here keeps a value in;
 // the ring's own waits count it.
+template <int AT>
 __device__ __forceinline__ void ring_load16(Rsrc r, unsigned dst, unsigned off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(r)
-                 : "memory");
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(r), "i"(AT)
+                 : "memory", "scc");
 }
 
 // Rows lie in LDS with 16-byte pieces permuted: piece c of row r at c ^ swz(r) within
@@ -133,7 +145,7 @@ __device__ __forceinline__ bf16x8 as_bf16(i32x2 v) { return e4m3_to_bf16(v); }
 template <class T, int N>
 __device__ __forceinline__ void arrived(T (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(x[i])::"memory");
+    for (int i = N - 1; i >= 0; --i) asm volatile("" : "+v"(x[i])::"memory");  // LDS reads return in order: one wait
 }
 
 // ---------------------------------------------------------------- softmax
