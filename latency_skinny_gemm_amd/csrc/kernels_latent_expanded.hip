@@ -18,11 +18,13 @@ namespace {
 
 constexpr int kStep = 32, kSlots = 3;
 constexpr int kKvRow = 2 * (SKG_EXPANDED_NOPE + SKG_EXPANDED_V);  // bytes
-constexpr int kRopeRow = 2 * SKG_LATENT_ROPE;
-constexpr int kSlotBytes = kStep * (kKvRow + kRopeRow);
-constexpr int kLoads = 5;  // a wave's direct loads a step: 8 rows of keys and values, 8 shared parts
-constexpr size_t kExpandedLds = std::max<size_t>(kSlots * kSlotBytes + 64, (SKG_LATENT_MAX_B + 1) * 8 + 64);
+constexpr int kOwnRow = 2 * SKG_EXPANDED_NOPE, kRopeRow = 2 * SKG_LATENT_ROPE, kValueRow = 2 * SKG_EXPANDED_V;
+constexpr int kKeyBytes = kStep * (kOwnRow + kRopeRow), kValueBytes = kStep * kValueRow;
+constexpr int kLoads = 5;  // a wave's direct loads a step: 8 keys, their shared parts, 8 values
+constexpr int kFlags = kSlots * (kKeyBytes + kValueBytes);
+constexpr size_t kExpandedLds = std::max<size_t>(kFlags + 64, (SKG_LATENT_MAX_B + 1) * 8 + 64);
 constexpr int kRows = 128;
+constexpr int kAhead = 4;  // keys' fragments under way
 constexpr int kQuery = SKG_EXPANDED_NOPE + SKG_LATENT_ROPE;
 
 }  // namespace
@@ -68,171 +70,251 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
         }
     }
     wait_vmcnt_lds<0>();  // here, so that the compiler waits for no load inside the loop over the ring
-    // direct loads: rows of 32 pieces, permuted among 16, and of 8
+    // direct loads: a head's keys and values in rows of 16 pieces, the shared parts of 8
     const unsigned row_bytes = (unsigned)a.H * kKvRow;
-    unsigned src[4];
+    unsigned src[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int p = k * 64 + lane, row = p >> 5, c = p & 31;
-        src[k] = (unsigned)row * row_bytes + (unsigned)((c ^ swz16(wave * 8 + row)) * 16);
+    for (int k = 0; k < 2; ++k) {
+        const int row = k * 4 + g4;
+        src[k] = (unsigned)row * row_bytes + (unsigned)((l15 ^ swz16(wave * 8 + row)) * 16);
     }
     const unsigned rope_bytes = (unsigned)a.rope_stride * 2;
     const unsigned rope_src = (unsigned)(lane >> 3) * rope_bytes + (unsigned)(((lane & 7) ^ swz8(wave * 8 + (lane >> 3))) * 16);
     unsigned koff[8], roff[4], voff[2][4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) koff[c] = (unsigned)l31 * kKvRow + (unsigned)(((c * 2 + half) ^ swz16(l31)) * 16);
+    for (int c = 0; c < 8; ++c) koff[c] = (unsigned)l31 * kOwnRow + (unsigned)(((c * 2 + half) ^ swz16(l31)) * 16);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) roff[c] = (unsigned)(kStep * kKvRow) + (unsigned)l31 * kRopeRow + (unsigned)(((c * 2 + half) ^ swz8(l31)) * 16);
+    for (int c = 0; c < 4; ++c) roff[c] = (unsigned)(kStep * kOwnRow) + (unsigned)l31 * kRopeRow + (unsigned)(((c * 2 + half) ^ swz8(l31)) * 16);
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             const int row = 8 * y + 4 * half + (l15 >> 2);
-            voff[y][d] = (unsigned)(row * kKvRow + 2 * SKG_EXPANDED_NOPE + ((d * 4 + (g4 & 1) * 2 + ((l15 & 3) >> 1)) ^ swz16(row)) * 16 + (l15 & 1) * 8);
+            voff[y][d] = (unsigned)(kSlots * kKeyBytes + row * kValueRow + ((d * 4 + (g4 & 1) * 2 + ((l15 & 3) >> 1)) ^ swz16(row)) * 16 + (l15 & 1) * 8);
         }
     const unsigned ring = uniform((int)lds_address(lds_raw));
-    auto issue = [&](int step, int slot) {
-        const int row = step * kStep + wave * 8, rows = min(max(most - row, 0), 8);
-        const size_t at = (size_t)kv.first + (rows ? row : 0);
-        const Rsrc rk = make_rsrc(a.kv + (at * a.H + h) * (kKvRow / 2), rows ? (unsigned)(rows - 1) * row_bytes + kKvRow : 0u);
-        const Rsrc rr = make_rsrc(a.k_rope + at * a.rope_stride, rows ? (unsigned)(rows - 1) * rope_bytes + kRopeRow : 0u);
-        const unsigned dst = ring + slot * kSlotBytes;
-        each<4>([&](auto k) { ring_load16<k * 1024>(rk, dst + wave * 8 * kKvRow, src[k]); });
-        ring_load16<kStep * kKvRow>(rr, dst + wave * 1024, rope_src);
+    // a step's keys, and the values of the step before; steps are brought in order
+    struct Next {
+        const uint16_t *own, *shared;  // this wave's rows
+        int row;
+        unsigned value_bytes;
+    };
+    auto rewind = [&] {
+        const size_t at = (size_t)kv.first + wave * 8;
+        return Next{a.kv + (at * a.H + h) * (kKvRow / 2), a.k_rope + at * a.rope_stride, wave * 8, 0u};
+    };
+    auto issue = [&](Next &n, int key_slot, int value_slot) {
+        const int rows = min(uniform(most - n.row), 8);
+        const unsigned bytes = rows > 0 ? (unsigned)(rows - 1) * row_bytes + kOwnRow : 0u;
+        const unsigned shared = rows > 0 ? (unsigned)(rows - 1) * rope_bytes + kRopeRow : 0u;
+        const unsigned keys = ring + key_slot * kKeyBytes, values = ring + value_slot * kValueBytes;
+        const Rsrc rk = make_rsrc(n.own, bytes), rr = make_rsrc(n.shared, shared);
+        const Rsrc rv = make_rsrc(n.own - (size_t)(kStep / 2) * row_bytes + SKG_EXPANDED_NOPE, n.value_bytes);
+        each<2>([&](auto k) { ring_load16<k * 1024>(rk, keys + wave * 8 * kOwnRow, src[k]); });
+        ring_load16<kStep * kOwnRow>(rr, keys + wave * 1024, rope_src);
+        each<2>([&](auto k) { ring_load16<kSlots * kKeyBytes + k * 1024>(rv, values + wave * 8 * kValueRow, src[k]); });
+        n.own += (size_t)(kStep / 2) * row_bytes;
+        n.shared += (size_t)kStep * a.rope_stride;
+        n.row += kStep;
+        n.value_bytes = bytes;
     };
 
-    unsigned char *flags = lds_raw + kSlots * kSlotBytes;
+    unsigned char *flags = lds_raw + kFlags;
     const int steps = (most + kStep - 1) / kStep;
     f32x16 acc[4];
-    float m, l;
-    bool careful = false;
-    for (;;) {
+    float m = 0.0f, l = 0.0f, x[16];  // x: scores over m, logarithms of weights
+    bf16x8 pf[2];
+    auto read_key = [&](const unsigned char *keys, int c) { return *reinterpret_cast<const u32x4 *>(keys + (c < 8 ? koff[c] : roff[c - 8])); };
+    auto read_values = [&](const unsigned char *values, int d, s16x8 (&v)[2]) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const s16x4 v0 = lds_transposed4(values + voff[0][d] + kk * 16 * kValueRow);
+            const s16x4 v1 = lds_transposed4(values + voff[1][d] + kk * 16 * kValueRow);
+            v[kk] = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    };
+    auto weigh = [&](int part) {  // four of the weights
+        bf16x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = (__bf16)__builtin_amdgcn_exp2f(x[part * 4 + r]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) pf[part >> 1][(part & 1) * 4 + r] = w[r];
+        const bf16x2 one{(__bf16)1.0f, (__bf16)1.0f};
+        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(w, w, 0, 1), one, l, false);
+        l = __builtin_amdgcn_fdot2_f32_bf16(__builtin_shufflevector(w, w, 2, 3), one, l, false);
+    };
+    auto masked = [&](f32x16 &z, int row0) {
+        if (row0 + kStep > lim0) {
+            const int left = here(lim) - row0 - 4 * half;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z[r] = 8 * (r >> 2) + (r & 3) < left ? z[r] : -__builtin_inff();
+        }
+    };
+    auto scaled = [&](const f32x16 &z, float top) {
+        top = other_half_max(top) * a.factor;
+        if (__any(top > m + 8.0f)) {
+            const float next = fmaxf(m, top);
+            const float down = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+            m = next;
+            l *= down;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[d][r] *= down;
+        }
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(z[r], a.factor, -ref);
+    };
+    // the scores of a step, and between them the weights of the one before
+    auto scores = [&](const unsigned char *keys, auto weights) {
+        f32x16 z;
+        u32x4 kf[kAhead][1];
+#pragma unroll
+        for (int c = 0; c < kAhead - 1; ++c) kf[c][0] = read_key(keys, c);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 12; ++c) {
+            if (c + kAhead - 1 < 12) kf[(c + kAhead - 1) % kAhead][0] = read_key(keys, c + kAhead - 1);
+            arrived(kf[c % kAhead]);
+            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(kf[c % kAhead][0]), qf[c], z, 0, 0, 0);
+            if constexpr (decltype(weights)::value)
+                if (c % 3 == 0) weigh(c / 3);
+        }
+        return z;
+    };
+    // this step's sums, and between them the maximum of the next one's scores
+    auto sums = [&](const unsigned char *values, s16x8 (&vf)[2][2], const f32x16 &z) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            if (d + 1 < 4) read_values(values, d + 1, vf[(d + 1) & 1]);
+            arrived(vf[d & 1]);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(vf[d & 1][kk]), pf[kk], acc[d], 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, z[d * 4 + r]);
+        }
+        return top;
+    };
+    // keys whose values hold an infinity or NaN, in a step that some tokens do not see:
+    // their products by vector instructions for those that do, zeros for the matrix
+    // instruction
+    auto apart = [&](unsigned char *values, int row0) {
+        bool bad = false;
+        for (int e = 0; e < 8; ++e) {
+            const unsigned w = *reinterpret_cast<const unsigned *>(values + (wave * 8 + (lane >> 3)) * kValueRow + (lane & 7) * 32 + e * 4);
+            bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+        }
+        const unsigned long long any = __ballot(bad);
+        unsigned rows8 = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) rows8 |= ((any >> (8 * r)) & 0xFFull ? 1u : 0u) << r;
+        if (lane == 0) flags[wave] = (unsigned char)rows8;
+        __syncthreads();
+        const unsigned flagged = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const unsigned *>(flags));
+        for (unsigned f = flagged; f; f &= f - 1) {
+            const int r0 = __builtin_ctz(f), r = (r0 >> 3) * 4 + (r0 & 3), kh = (r0 >> 2) & 1;
+            float own_p = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) own_p = u == r ? (float)pf[u >> 3][u & 7] : own_p;
+            const float pk = __shfl(own_p, l31 + 32 * kh, 64);
+            const bool in = row0 + r0 < lim;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int c = d * 4 + v;
+                    const uint2 w = *reinterpret_cast<const uint2 *>(values + r0 * kValueRow + (c ^ swz16(r0)) * 16 + half * 8);
+                    const float y[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (in) acc[d][4 * v + u] = __builtin_fmaf(pk, y[u], acc[d][4 * v + u]);
+                }
+        }
+        __syncthreads();
+        for (unsigned f = flagged; f; f &= f - 1)
+            if (t < 64) *reinterpret_cast<unsigned *>(values + __builtin_ctz(f) * kValueRow + t * 4) = 0;
+        __syncthreads();
+    };
+    Next next;
+    auto begin = [&] {
 #pragma unroll
         for (int d = 0; d < 4; ++d)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
         m = -__builtin_inff();
         l = 0.0f;
-        for (int k = 0; k < kSlots - 1; ++k)
-            if (k < steps) issue(k, k);
-        int slot = 0, fill = kSlots - 1;
-        for (int k = 0; k < steps; ++k) {
-            if (k + 1 < steps) wait_vmcnt_lds<kLoads>();
-            else wait_vmcnt_lds<0>();
-            barrier_nofence();
-            if (k + kSlots - 1 < steps) issue(k + kSlots - 1, fill);
-            const unsigned char *tile = lds_raw + slot * kSlotBytes;
-            slot = slot + 1 == kSlots ? 0 : slot + 1;
-            fill = fill + 1 == kSlots ? 0 : fill + 1;
-            const int row0 = k * kStep;
-            const bool masked = row0 + kStep > lim0;
-            float p[16];
-            bf16x8 pf[2] = {};
-            if (row0 < wave_most) {
-                f32x16 z;
+        next = rewind();
+        issue(next, 0, 2);
+        issue(next, 1, 0);
+        issue(next, 2, 1);
+        wait_vmcnt_lds<2 * kLoads>();
+        barrier_nofence();
+        f32x16 z = scores(lds_raw, std::false_type{});
+        masked(z, 0);
+        float top = z[0];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) z[r] = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 12; ++c) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(tile + (c < 8 ? koff[c] : roff[c - 8]));
-                    z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[c], z, 0, 0, 0);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        z[r] = row0 + 8 * (r >> 2) + 4 * half + (r & 3) < lim ? z[r] : -__builtin_inff();
-                }
-                float top = z[0];
-#pragma unroll
-                for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
-                top = other_half_max(top) * a.factor;
-                if (__any(top > m + 8.0f)) {
-                    const float next = fmaxf(m, top);
-                    const float down = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - next);
-                    m = next;
-                    l *= down;
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[d][r] *= down;
-                }
-                const float ref = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[r], a.factor, -ref));
-                pf[0] = to_bf16x8(p);
-                pf[1] = to_bf16x8(p + 8);
-                l = add_bf16x8(pf[1], add_bf16x8(pf[0], l));
-            }
-            if (__builtin_expect(careful && row0 + kStep > sees(i * kRows), 0)) {
-                // keys whose values hold an infinity or NaN, in a step that some tokens do
-                // not see: their products by vector instructions for those that do, zeros
-                // for the matrix instruction
-                bool bad = false;
-                for (int e = 0; e < 8; ++e) {
-                    const unsigned w = *reinterpret_cast<const unsigned *>(
-                        tile + (wave * 8 + (lane >> 3)) * kKvRow + 2 * SKG_EXPANDED_NOPE + (lane & 7) * 32 + e * 4);
-                    bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-                }
-                const unsigned long long any = __ballot(bad);
-                unsigned rows8 = 0;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) rows8 |= ((any >> (8 * r)) & 0xFFull ? 1u : 0u) << r;
-                if (lane == 0) flags[wave] = (unsigned char)rows8;
-                __syncthreads();
-                const unsigned flagged = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const unsigned *>(flags));
-                for (unsigned f = flagged; f; f &= f - 1) {
-                    const int r0 = __builtin_ctz(f), r = (r0 >> 3) * 4 + (r0 & 3), kh = (r0 >> 2) & 1;
-                    float own_p = 0.0f;
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) own_p = u == r ? (float)pf[u >> 3][u & 7] : own_p;
-                    const float pk = __shfl(own_p, l31 + 32 * kh, 64);
-                    const bool in = row0 + r0 < lim;
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int c = d * 4 + v;
-                            const uint2 w = *reinterpret_cast<const uint2 *>(tile + r0 * kKvRow + 2 * SKG_EXPANDED_NOPE + (c ^ swz16(r0)) * 16 + half * 8);
-                            const float y[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                if (in) acc[d][4 * v + u] = __builtin_fmaf(pk, y[u], acc[d][4 * v + u]);
-                        }
-                }
-                __syncthreads();
-                for (unsigned f = flagged; f; f &= f - 1)
-                    if (t < 64) *reinterpret_cast<unsigned *>(const_cast<unsigned char *>(tile) + __builtin_ctz(f) * kKvRow + 2 * SKG_EXPANDED_NOPE + t * 4) = 0;
-                __syncthreads();
-            }
-            if (row0 < wave_most) {
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const s16x4 x = lds_transposed4(tile + voff[0][d] + kk * 16 * kKvRow);
-                        const s16x4 y = lds_transposed4(tile + voff[1][d] + kk * 16 * kKvRow);
-                        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), pf[kk], acc[d], 0, 0, 0);
-                    }
-                }
-            }
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
+        scaled(z, top);
+    };
+    // step k, with its values in slot `at` and the next one's keys in the slot after
+    auto step = [&](int k, int at, auto careful) {
+        const int after = (at + 1) % kSlots, last = (at + 2) % kSlots;
+        wait_vmcnt_lds<kLoads>();
+        barrier_nofence();
+        issue(next, at, last);
+        const int row0 = k * kStep;
+        unsigned char *const values = lds_raw + at * kValueBytes;
+        const bool seen = row0 < wave_most;
+        f32x16 z;
+        s16x8 vf[2][2];
+        if (seen) z = scores(lds_raw + after * kKeyBytes, std::true_type{});
+        if constexpr (decltype(careful)::value) {
+            if (!seen) pf[0] = pf[1] = bf16x8{};
+            if (row0 + kStep > sees(i * kRows)) apart(values + kSlots * kKeyBytes, row0);
+        }
+        if (!seen) return;
+        read_values(values, 0, vf[0]);
+        masked(z, row0 + kStep);
+        scaled(z, sums(values, vf, z));
+    };
+    if (steps > 0) {
+        begin();
+        for (int k = 0;; k += 3) {
+            step(k, 0, std::false_type{});
+            if (k + 1 >= steps) break;
+            step(k + 1, 1, std::false_type{});
+            if (k + 2 >= steps) break;
+            step(k + 2, 2, std::false_type{});
+            if (k + 3 >= steps) break;
         }
         wait_vmcnt_lds<0>();
         __syncthreads();
         // see kernels_latent_attention.hip: infinities and NaN of keys that a token does not see
-        if (careful || sees(i * kRows) >= most) break;
-        bool bad = false;
+        if (sees(i * kRows) < most) {
+            bool bad = false;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) bad |= not_finite(acc[d][r]);
+            const unsigned long long found = __ballot(bad && live);
+            if (lane == 0) flags[wave] = found != 0;
+            __syncthreads();
+            const unsigned some = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const unsigned *>(flags));
+            __syncthreads();
+            if (__builtin_expect(some, 0)) {
+                begin();
+                for (int k = 0; k < steps; ++k) step(k, k % kSlots, std::true_type{});
+                wait_vmcnt_lds<0>();
+            }
+        }
+    } else {
 #pragma unroll
         for (int d = 0; d < 4; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) bad |= not_finite(acc[d][r]);
-        const unsigned long long found = __ballot(bad && live);
-        if (lane == 0) flags[wave] = found != 0;
-        __syncthreads();
-        const unsigned some = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const unsigned *>(flags));
-        __syncthreads();
-        if (!some) break;
-        careful = true;
+            for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
     }
     l = other_half_sum(l);
     if (!live) return;
