@@ -42,6 +42,7 @@ EXTRA_FLAGS = {"kernels_tiled.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_fp8_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_mxfp4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_mxfp4_rows.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "kernels_latent_expanded.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                "kernels_latent_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 FLOORS_HIP = ["floors.hip"]
 

@@ -165,8 +165,15 @@ extern "C" int skinny_latent_attention_expanded(const void *q, const void *kv, c
                         {q_starts, ((size_t)B + 1) * 4},
                         {kv_starts, ((size_t)B + 1) * 4}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
+    const int parts = latent_expanded_parts(B, T, S, H);
+    float *ws = nullptr;
+    unsigned *tk = nullptr;
+    if (parts > 1) {
+        const int rc = acquire(stream, latent_expanded_workspace_bytes() / 4, 0, &ws, &tk);
+        if (rc != SKG_OK) return rc;
+    }
     const ExpandedArgs a{(const uint16_t *)q, (const uint16_t *)kv, (const uint16_t *)k_rope, q_starts, kv_starts,
-                         (uint16_t *)out, k_rope_stride, (float)(softmax_scale * kLog2e), causal, B, T, S, H};
+                         (uint16_t *)out, k_rope_stride, (float)(softmax_scale * kLog2e), causal, B, T, S, H, parts, ws};
     return hip_status(launch_latent_expanded(a, stream));
 }
 
@@ -196,5 +203,6 @@ extern "C" int skinny_latent_reserve(int H, hipStream_t stream) {
     if (H > SKG_LATENT_MAX_H) return SKG_ERR_UNSUPPORTED;
     float *ws = nullptr;
     unsigned *tk = nullptr;
-    return acquire(stream, std::max(latent_workspace_bytes(64, false), latent_workspace_bytes(32, true)) / 4, 0, &ws, &tk);
+    const size_t bytes = std::max({latent_workspace_bytes(64, false), latent_workspace_bytes(32, true), latent_expanded_workspace_bytes()});
+    return acquire(stream, bytes / 4, 0, &ws, &tk);
 }

@@ -71,20 +71,6 @@ __device__ __forceinline__ long steps_before(int before, int n, int tp, int upto
     return sum;
 }
 
-// Sums of weights, and of weighted columns, joined by those of another part; one that
-// saw no row has the maximum -inf and sums of 0.
-template <int N>
-__device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f32x2 ml, const f32x4 (&y)[N]) {
-    const float next = fmaxf(m, ml.x), ref = next == -__builtin_inff() ? 0.0f : next;
-    const float w0 = __builtin_amdgcn_exp2f(m - ref), w1 = __builtin_amdgcn_exp2f(ml.x - ref);
-    m = next;
-    l = __builtin_fmaf(w1, ml.y, l * w0);
-#pragma unroll
-    for (int v = 0; v < N; ++v)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) sum[v][u] = __builtin_fmaf(w1, y[v][u], sum[v][u] * w0);
-}
-
 }  // namespace
 
 // A workgroup of four waves takes 32 RG rows, 4 / RG waves 32 of them: each makes the

@@ -183,6 +183,20 @@ __device__ __forceinline__ float other_half_sum(float v) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Sums of weights, and of weighted columns, joined by those of another part; one that
+// saw no row has the maximum -inf and sums of 0.
+template <int N>
+__device__ __forceinline__ void add_part(float &m, float &l, f32x4 (&sum)[N], f32x2 ml, const f32x4 (&y)[N]) {
+    const float next = fmaxf(m, ml.x), ref = next == -__builtin_inff() ? 0.0f : next;
+    const float w0 = __builtin_amdgcn_exp2f(m - ref), w1 = __builtin_amdgcn_exp2f(ml.x - ref);
+    m = next;
+    l = __builtin_fmaf(w1, ml.y, l * w0);
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum[v][u] = __builtin_fmaf(w1, y[v][u], sum[v][u] * w0);
+}
+
 __device__ __forceinline__ bool not_finite(float v) {
     return (__float_as_uint(v) & 0x7F800000u) == 0x7F800000u;
 }

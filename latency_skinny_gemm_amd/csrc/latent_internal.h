@@ -43,7 +43,11 @@ struct ExpandedArgs {
     long rope_stride;
     float factor;
     int causal, B, T, S, H;
+    int parts;  // workgroups that share a tile's keys, at most
+    float *ws;  // parts > 1
 };
+int latent_expanded_parts(int B, int T, int S, int H);
+size_t latent_expanded_workspace_bytes();
 int launch_latent_expanded(const ExpandedArgs &a, hipStream_t stream);
 
 struct HeadsArgs {

@@ -307,6 +307,8 @@ PROMPTS = [
     ([40, 3], [10, 0], 2, True),      # more tokens than keys: some see none
     ([20, 150], [31, 70], 2, False),
     ([300], [300], 8, True),
+    # keys of few query tokens shared among workgroups
+    ([1, 0, 130, 7], [2100, 700, 530, 0], 2, True), ([64], [1999], 3, False), ([300, 40], [812, 4100], 5, True),
 ]
 
 
