@@ -18,14 +18,20 @@ namespace {
 constexpr int kStartsLds = 1024;  // sequences whose starts are searched in LDS
 
 // v in fp32 such that its next rounding is that of v: where v lies between two
-// fp32 numbers, the odd one of them (a tie of the next rounding is even).
+// fp32 numbers, the odd one of them (a tie of the next rounding is even).  One beyond
+// the largest number becomes that number, a NaN stays one.
 __device__ __forceinline__ float to_odd(double v) {
     const float f = (float)v;
-    if ((double)f == v || !(fabs(v) < __builtin_inf())) return f;
+    const double d = (double)f;
     const unsigned u = __float_as_uint(f);
-    if (u & 1u) return f;
-    const bool up = (double)f < v, neg = u >> 31;
-    return __uint_as_float(u == 0u || u == 0x80000000u ? (v < 0 ? 0x80000001u : 1u) : (up != neg ? u + 1 : u - 1));
+    const unsigned other = (d < v) != (bool)(u >> 31) ? u + 1 : u - 1;  // the fp32 number on v's other side
+    return __uint_as_float((u & 1u) || d == v ? u : other);
+}
+// The quotient u / s as the division's instructions end, without its scaling: with
+// inv = 1 / s rounded, one correction of u inv; exact where the quotient is.
+__device__ __forceinline__ double over(double u, double s, double inv) {
+    const double q = u * inv;
+    return fabs(q) < __builtin_inf() ? __builtin_fma(__builtin_fma(-q, s, u), inv, q) : q;
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {
@@ -133,9 +139,9 @@ __global__ void __launch_bounds__(256) latent_append_kernel(LatentAppendArgs a, 
         if constexpr (!E4M3) {
             put(reinterpret_cast<uint16_t *>(a.cache) + at);
         } else {
-            const double s = a.scale[0];
+            const double s = a.scale[0], inv = 1.0 / s;
             auto code2 = [&](double u, double v) {
-                return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(quant_clamp(to_odd(u / s)), quant_clamp(to_odd(v / s)), 0, false) & 0xFFFFu;
+                return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(quant_clamp(to_odd(over(u, s, inv))), quant_clamp(to_odd(over(v, s, inv))), 0, false) & 0xFFFFu;
             };
             uint2 c;
             c.x = code2(y[0], y[1]) | code2(y[2], y[3]) << 16;
