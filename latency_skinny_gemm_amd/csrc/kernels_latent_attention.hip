@@ -25,7 +25,7 @@ struct Shape {
     int tp;         // tokens a row tile
     int hg;         // head groups (row tiles a token, if it has more heads than a tile rows)
     int teams;      // groups that hold all head groups of some tokens
-    int min_share;  // least number of steps a workgroup takes
+    int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 27.1, 22.6, 21.6, 22.0 us with 2, 4, 6, 8
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
 
@@ -698,7 +698,7 @@ template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     constexpr int G = groups_of(RG, E4M3);
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 4, 0};
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 6, 0};
     s.teams = G / s.hg;
     s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
