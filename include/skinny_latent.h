@@ -130,8 +130,9 @@ int skinny_heads_gemm(const void *x, long x_token_stride, long x_head_stride, co
                       int K, hipStream_t stream);
 
 /* Workspace of `stream` for skinny_latent_attention calls of H heads, any B, T and
- * lengths (it holds what workgroups that share a sequence hand on).  As
- * skinny_gemm_reserve: before graph capture. */
+ * lengths, and for all skinny_latent_attention_expanded calls (those whose query
+ * tokens are few for their keys use it).  It holds what workgroups that share a
+ * sequence hand on.  As skinny_gemm_reserve: before graph capture. */
 int skinny_latent_reserve(int H, hipStream_t stream);
 
 #ifdef __cplusplus

@@ -157,6 +157,8 @@ def latent_append(kv, cache, table, kv_lens, rotations, q_starts=None, weight=No
             ot, oh = H * ROPE, ROPE
         else:
             ot, oh = _heads("q_rope_out", q_rope_out, T, H, ROPE)
+        if T == 0:
+            H = 0  # torch gives an empty tensor no address
         if H:
             qp, op = q_rope.data_ptr(), q_rope_out.data_ptr()
     elif q_rope_out is not None:
@@ -255,7 +257,8 @@ def heads_gemm(x, W, out=None, stream=None):
 
 def reserve_latent(H, stream=None):
     """Reserves workspace for `stream` (else the current stream): latent_attention
-    calls of H heads, any batch and lengths.  Before graph capture."""
+    calls of H heads, any batch and lengths, and latent_attention_expanded calls.
+    Before graph capture."""
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(s.device):
         _c._check(_c._load().skinny_latent_reserve(H, ctypes.c_void_p(s.cuda_stream)), "skinny_latent_reserve")
