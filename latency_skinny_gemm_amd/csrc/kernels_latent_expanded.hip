@@ -41,17 +41,27 @@ struct Place {
     bool there;
 };
 __device__ __forceinline__ Place place_of(const ExpandedArgs &a, int n, unsigned char *lds) {
-    int b = 0, i = n;
-    if (a.B > 1) {
-        long *pre = reinterpret_cast<long *>(lds);
-        block_prefix<4>(a.B, pre, pre + a.B + 1, [&](int s) INLINE { return (long)((new_tokens(a.q_starts, s, a.T).n + kRows - 1) / kRows); });
-        if (n >= pre[a.B]) return {{0, 0}, {0, 0}, 0, false};
-        b = uniform(find_sequence(pre, a.B, n));
-        i = uniform(n - (int)pre[b]);
-        __syncthreads();
+    if (a.B <= 64) {  // a sequence a lane, every wave for itself: one round of loads, no barrier
+        const int lane = threadIdx.x & 63, b = min(lane, a.B - 1);
+        const Tokens q = new_tokens(a.q_starts, b, a.T), kv = new_tokens(a.kv_starts, b, a.S);
+        const int tiles = lane < a.B ? (q.n + kRows - 1) / kRows : 0;
+        int upto = tiles;
+        for (int d = 1; d < a.B; d <<= 1) {
+            const int u = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += u;
+        }
+        const unsigned long long behind = __ballot(upto > n);
+        if (!behind) return {{0, 0}, {0, 0}, 0, false};
+        const int at = __builtin_ctzll(behind);
+        auto of = [&](int v) INLINE { return __builtin_amdgcn_readlane(v, at); };
+        return {{of(q.first), of(q.n)}, {of(kv.first), of(kv.n)}, n - of(upto - tiles), true};
     }
-    const Tokens q = uniform(new_tokens(a.q_starts, b, a.T));
-    return {q, uniform(new_tokens(a.kv_starts, b, a.S)), i, i * kRows < q.n};
+    long *pre = reinterpret_cast<long *>(lds);
+    block_prefix<4>(a.B, pre, pre + a.B + 1, [&](int s) INLINE { return (long)((new_tokens(a.q_starts, s, a.T).n + kRows - 1) / kRows); });
+    if (n >= pre[a.B]) return {{0, 0}, {0, 0}, 0, false};
+    const int b = uniform(find_sequence(pre, a.B, n)), i = uniform(n - (int)pre[b]);
+    __syncthreads();
+    return {uniform(new_tokens(a.q_starts, b, a.T)), uniform(new_tokens(a.kv_starts, b, a.S)), i, true};
 }
 // Keys that token j of a place's sequence sees.
 __device__ __forceinline__ int keys_of(const ExpandedArgs &a, const Place &p, int j) {
@@ -89,17 +99,6 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
     const int steps = (most + kStep - 1) / kStep;
     const int first = (int)((long)steps * part / parts), end = (int)((long)steps * (part + 1) / parts);
 
-    bf16x8 qf[12];
-    {
-        const uint16_t *p = a.q + ((size_t)(q.first + (j < q.n ? j : 0)) * a.H + h) * kQuery + half * 8;
-#pragma unroll
-        for (int k = 0; k < 12; ++k) {
-            u32x4 v{0, 0, 0, 0};
-            if (j < q.n) v = *reinterpret_cast<const u32x4 *>(p + k * 16);
-            qf[k] = __builtin_bit_cast(bf16x8, v);
-        }
-    }
-    wait_vmcnt_lds<0>();  // here, so that the compiler waits for no load inside the loop over the ring
     // A block holds four rows of 16 pieces of 16 bytes (a head's keys, its values), or eight
     // of 8 (shared parts): four pieces of each row, then the next four.  Four lanes load 64
     // bytes of a row, and a fragment's address is one register and a constant.  A fragment
@@ -150,6 +149,28 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
         else if constexpr (k == 2) ring_load16<kShared>(x.shared, x.key_at + wave * kSharedBlock, rope_src);
         else ring_load16<kSlots * kKeyBytes + (k - 3) * 1024>(x.values, x.value_at + wave * 2048, src[k - 3]);
     };
+
+    // the first steps, and under way with them the queries
+    Next next;
+    auto bring = [&]() INLINE {
+        next = rewind();
+        each<3>([&](auto k) INLINE {
+            const Loads x = loads(next, k, (k + 2) % kSlots);
+            each<kLoads>([&](auto p) INLINE { load(x, p); });
+        });
+    };
+    if (steps > 0) bring();
+    bf16x8 qf[12];
+    {
+        const uint16_t *p = a.q + ((size_t)(q.first + (j < q.n ? j : 0)) * a.H + h) * kQuery + half * 8;
+#pragma unroll
+        for (int k = 0; k < 12; ++k) {
+            u32x4 v{0, 0, 0, 0};
+            if (j < q.n) v = *reinterpret_cast<const u32x4 *>(p + k * 16);
+            qf[k] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+    wait_vmcnt_lds<0>();  // here, so that the compiler waits for no load inside the loop over the ring
 
     unsigned char *flags = lds_raw + kFlags;
     f32x16 acc[4], z;
@@ -277,14 +298,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
             if (t < 64) *reinterpret_cast<unsigned *>(at(__builtin_ctz(f), t >> 2) + (t & 3) * 4) = 0;
         __syncthreads();
     };
-    Next next;
     auto begin = [&]() INLINE {
         nothing();
-        next = rewind();
-        each<3>([&](auto k) INLINE {
-            const Loads x = loads(next, k, (k + 2) % kSlots);
-            each<kLoads>([&](auto part) INLINE { load(x, part); });
-        });
         wait_vmcnt_lds<2 * kLoads>();
         barrier_nofence();
         Keys kf;
@@ -349,6 +364,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
             const unsigned some = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const unsigned *>(flags));
             __syncthreads();
             if (__builtin_expect(some, 0)) {
+                bring();
                 begin();
                 for (int k = first; k < end; ++k) step(k, (k - first) % kSlots, std::true_type{});
                 wait_vmcnt_lds<0>();
