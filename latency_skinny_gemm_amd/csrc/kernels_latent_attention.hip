@@ -53,22 +53,22 @@ static_assert((SKG_LATENT_MAX_B + 1) * 8 <= kRing * kTile * row_bytes(true), "pr
 __device__ __forceinline__ int tile_steps(int before, int n, int tp, int i) {
     return max(1, (before + min((i + 1) * tp, n) + kTile - 1) / kTile);
 }
-// Their sum over the row tiles before `upto` of a sequence with `n` new tokens
-// behind `before` rows.  Tile i but the last sees before + (i + 1) tp rows; of 32
-// successive tiles each residue's counts grow by tp.
+// Their sum over the row tiles before `upto` of a sequence with `n` new tokens behind
+// `before` rows.  Tile i but the last sees x = before + (i + 1) tp rows and has
+// (x + (-x mod 32)) / 32 steps; -x mod 32 has the period 32 / g, g the largest power of
+// two that divides tp and 32, over which it takes every value of its remainder mod g.
 __device__ __forceinline__ long steps_before(int before, int n, int tp, int upto) {
+    static_assert(kTile == 32, "");
     const int tiles = (n + tp - 1) / tp;
     const int m = min(upto, tiles - 1);
     long sum = upto >= tiles && tiles > 0 ? tile_steps(before, n, tp, tiles - 1) : 0;
     if (m <= 0) return sum;
     const int ones = min(max((kTile - before) / tp, 0), m);  // tiles of one step
-    sum += ones;
     const int left = m - ones, c0 = before + (ones + 1) * tp;
-    for (int r = 0; r < min(left, kTile); ++r) {
-        const long k = (left - r + kTile - 1) / kTile;
-        sum += k * ((c0 + r * tp + kTile - 1) / kTile) + tp * (k * (k - 1) / 2);
-    }
-    return sum;
+    const int log_g = min(__builtin_ctz(tp), 5), g = 1 << log_g, period = 32 >> log_g;
+    long over = (long)(left >> (5 - log_g)) * (period * (-c0 & (g - 1)) + 16 * (period - 1));
+    for (int r = 0; r < (left & (period - 1)); ++r) over += -(c0 + r * tp) & 31;
+    return sum + ones + (((long)left * c0 + (long)tp * ((long)left * (left - 1) / 2) + over) >> 5);
 }
 
 }  // namespace
