@@ -26,6 +26,7 @@ struct Shape {
     int hg;         // head groups (row tiles a token, if it has more heads than a tile rows)
     int teams;      // groups that hold all head groups of some tokens
     int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 27.1, 22.6, 21.6, 22.0 us with 2, 4, 6, 8
+    int anew;       // steps that a team's beginning of another row tile costs it
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
 
@@ -117,32 +118,18 @@ latent_attention_kernel(Shape s) {
     Shared *const records = reinterpret_cast<Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>());
 
     // ---- this team's share of all steps
-    long *pre = reinterpret_cast<long *>(lds_raw);
     int b = 0, i = 0, before = 0, at = 0;  // sequence, row tile and its first step; rows before the sequence's new ones
     Tokens q{0, 0};
-    long total, start = 0;  // the start of b's steps
-    if (a.B == 1) {
-        q = uniform(new_tokens(a.q_starts, 0, a.T));
-        before = uniform(length(0)) - q.n;
-        total = steps_before(before, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
-    } else {
-        block_prefix<NW>(a.B, pre, reinterpret_cast<long *>(exchange), [&](int b) {
-            const Tokens q = new_tokens(a.q_starts, b, a.T);
-            return steps_before(length(b) - q.n, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
-        });
-        total = pre[a.B];
-    }
-    const long share = max((long)s.min_share, total <= 0x7FFFFFFFL - 512 ? (long)((unsigned)(total + s.teams - 1) / (unsigned)s.teams) : (total + s.teams - 1) / s.teams);
-    const long from = team * share;
-    long left = team < s.teams ? min(total, from + share) - from : 0;
-    if (left > 0) {
-        if (a.B > 1) {
-            b = uniform(find_sequence(pre, a.B, from));
-            q = uniform(new_tokens(a.q_starts, b, a.T));
-            before = uniform(length(b)) - q.n;
-            start = pre[b];
-        }
-        const long off = from - start;
+    long share, left = 0;
+    auto uniform_long = [](long v) { return (long)((unsigned long)(unsigned)uniform((int)(v >> 32)) << 32 | (unsigned)uniform((int)v)); };
+    auto share_of = [&](long total) {
+        return max((long)s.min_share, total <= 0x7FFFFFFFL - 512 ? (long)((unsigned)(total + s.teams - 1) / (unsigned)s.teams) : (total + s.teams - 1) / s.teams);
+    };
+    auto of_lane = [](long v, int l) {
+        return (long)((unsigned long)(unsigned)__builtin_amdgcn_readlane((int)(v >> 32), l) << 32 | (unsigned)__builtin_amdgcn_readlane((int)v, l));
+    };
+    // steps `off` .. of sequence b
+    auto seek = [&](long off) {
         int lo = 0, hi = (q.n + s.tp - 1) / s.tp;
         while (hi - lo > 1) {
             const int step = (hi - lo + 63) / 64, cand = lo + lane * step;
@@ -153,6 +140,73 @@ latent_attention_kernel(Shape s) {
         }
         i = uniform(lo);
         at = uniform((int)(off - (i ? steps_before(before, q.n, s.tp, i) : 0)));
+    };
+    if (a.B <= 64) {  // a sequence a lane, every wave for itself: one round of loads, no barrier
+        const int own_b = min(lane, a.B - 1);
+        const Tokens own = new_tokens(a.q_starts, own_b, a.T);
+        const int own_before = length(own_b) - own.n, tiles = lane < a.B ? (own.n + s.tp - 1) / s.tp : 0;
+        const int longest = tiles ? tile_steps(own_before, own.n, s.tp, tiles - 1) : 0;
+        const long steps = steps_before(own_before, own.n, s.tp, tiles);
+        long upto = steps;
+        int all = tiles;
+        for (int d = 1; d < a.B; d <<= 1) {
+            const long u = __shfl_up(upto, d, 64);
+            const int v = __shfl_up(all, d, 64);
+            if (lane >= d) upto += u, all += v;
+        }
+        const long total = of_lane(upto, a.B - 1);
+        all = __builtin_amdgcn_readlane(all, a.B - 1);
+        share = uniform_long(share_of(total));
+        // Shares of one row tile each, where they are little longer: a team whose share goes
+        // on in another tile begins anew there.
+        int whole = (int)min(share, 0x7FFFFFFFL), parts = 0, need = s.teams + 1;
+        while (all <= s.teams && whole <= share + s.anew) {
+            parts = (longest + whole - 1) / whole;
+            need = tiles * parts;
+            for (int d = 1; d < a.B; d <<= 1) {
+                const int v = __shfl_up(need, d, 64);
+                if (lane >= d) need += v;
+            }
+            const int last = __builtin_amdgcn_readlane(need, a.B - 1);
+            if (last <= s.teams) break;
+            whole = max(whole + 1, (int)((long)whole * last / s.teams));
+            need = s.teams + 1;
+        }
+        whole = uniform(whole);
+        const bool aligned = __builtin_amdgcn_readlane(need, a.B - 1) <= s.teams;
+        const long from = team * share;
+        const unsigned long long behind = __ballot(aligned ? need > team : upto > from);
+        if (team < s.teams && behind) {
+            b = __builtin_ctzll(behind);
+            q = {__builtin_amdgcn_readlane(own.first, b), __builtin_amdgcn_readlane(own.n, b)};
+            before = __builtin_amdgcn_readlane(own_before, b);
+            if (aligned) {
+                const int k = __builtin_amdgcn_readlane(parts, b), r = team - __builtin_amdgcn_readlane(need - tiles * parts, b);
+                share = whole;
+                i = uniform(r / k);
+                at = (r - i * k) * whole;
+                left = max(min(whole, tile_steps(before, q.n, s.tp, i) - at), 0);
+            } else {
+                left = min(total, from + share) - from;
+                seek(from - of_lane(upto - steps, b));
+            }
+        }
+    } else {
+        long *pre = reinterpret_cast<long *>(lds_raw);
+        block_prefix<NW>(a.B, pre, reinterpret_cast<long *>(exchange), [&](int b) {
+            const Tokens q = new_tokens(a.q_starts, b, a.T);
+            return steps_before(length(b) - q.n, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
+        });
+        const long total = pre[a.B];
+        share = uniform_long(share_of(total));
+        const long from = team * share;
+        left = team < s.teams ? min(total, from + share) - from : 0;
+        if (left > 0) {
+            b = uniform(find_sequence(pre, a.B, from));
+            q = uniform(new_tokens(a.q_starts, b, a.T));
+            before = uniform(length(b)) - q.n;
+            seek(from - pre[b]);
+        }
     }
     __syncthreads();
     if (t < 16) flags[t] = 0;
@@ -634,8 +688,8 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
     __shared__ f32x4 sums[4][4][64];
     __shared__ f32x2 stats[4][64];
     const LatentArgs &a = s.a;
-    const int d = blockIdx.y;
-    const Shared e = reinterpret_cast<const Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>())[blockIdx.x];
+    const int d = blockIdx.x;  // neighbouring workgroups lie on different XCDs: those of one record on all of them
+    const Shared e = reinterpret_cast<const Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>())[blockIdx.y];
     if (e.parts < 2) return;
     const int group = e.group, g = group % s.hg;
     const Tokens q = new_tokens(a.q_starts, e.b, a.T);
@@ -698,7 +752,7 @@ template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     constexpr int G = groups_of(RG, E4M3);
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 6, 0};
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 6, 4, 0};
     s.teams = G / s.hg;
     s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
@@ -708,7 +762,7 @@ int go(const LatentArgs &a, hipStream_t stream) {
     hipLaunchKernelGGL((latent_attention_kernel<RG, CS, E4M3>), dim3(G), dim3(64 * RG * CS), lds, stream, s);
     const hipError_t f = hipGetLastError();
     if (f != hipSuccess) return (int)f;
-    hipLaunchKernelGGL((latent_combine_kernel<RG>), dim3(s.by_tile ? a.B * s.hg : G, 16), dim3(256), 0, stream, s, a.scale, G);
+    hipLaunchKernelGGL((latent_combine_kernel<RG>), dim3(16, s.by_tile ? a.B * s.hg : G), dim3(256), 0, stream, s, a.scale, G);
     return (int)hipGetLastError();
 }
 
