@@ -129,7 +129,7 @@ extern "C" int skinny_latent_attention(const skinny_latent_batch *batch, const v
                         {batch->kv_lens, (size_t)batch->B * 4},
                         {batch->q_starts, ((size_t)batch->B + 1) * 4}};
     if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    const int tile = latent_rows(batch->B, batch->T, H);
+    const int tile = latent_rows(batch->B, batch->T, H, (long)batch->table_width * batch->page_size, e4m3);
     float *ws = nullptr;
     unsigned *tk = nullptr;
     rc = acquire(stream, latent_workspace_bytes(tile, e4m3) / 4, 0, &ws, &tk);

@@ -773,14 +773,23 @@ int by_rows(const LatentArgs &a, int rows, hipStream_t stream) {
 
 }  // namespace
 
-int latent_rows(int B, int T, int H) {
-    // row tiles of the call if its tokens are spread evenly
-    for (int rows = 64; rows > 32; rows /= 2) {
+// 64 rows read the cache half as often and waste fewer rows where H does not divide 32,
+// but fill the device with fewer tiles and hand on twice as much.  Measured, 32 against
+// 64 (bf16, us): 512 tokens of 128 heads over 8192 rows 1180, 916; 150 tokens of 20 heads
+// over 2000 to 9000 rows, 12 sequences, 134, 85; 128 tokens of 16 heads over 16000 rows
+// 105, 97, over 4000 (64 tokens) 32, 46; 100 tokens of 7 heads over 12000, 3 sequences,
+// 39, 43; 4 tokens of 128 heads over 6000, 4 sequences, 25, 36.  (e4m3, us): 99, 85 for
+// the second of these, 99, 103 for the third.
+int latent_rows(int B, int T, int H, long capacity, bool e4m3) {
+    auto tiles = [&](int rows) {  // of the call if its tokens are spread evenly
         const long tp = H > rows ? 1 : rows / H, hg = H > rows ? (H + rows - 1) / rows : 1;
-        const long each = ((long)T + B - 1) / B;
-        if (rows / 2 < H * each && B * ((each + tp - 1) / tp) * hg >= 256) return rows;
-    }
-    return 32;
+        return B * ((((long)T + B - 1) / B + tp - 1) / tp) * hg;
+    };
+    const long few = tiles(64), many = tiles(32);
+    if (few == many) return 32;
+    // steps of one of 256 workgroups if all sequences are as long as the table lets them be
+    const double share = (double)few * capacity / kTile / 256;
+    return few >= 256 || (many > 2 * few && share >= 20) || (!e4m3 && share >= 48) ? 64 : 32;
 }
 
 size_t latent_workspace_bytes(int rows, bool e4m3) {

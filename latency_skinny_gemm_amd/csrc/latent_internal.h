@@ -31,8 +31,9 @@ struct LatentArgs {
     float factor;  // softmax scale * log2 e
     int B, T, W, page_shift, pages, H;
 };
-// Rows (token, head) a workgroup takes at once: 32 or 64.
-int latent_rows(int B, int T, int H);
+// Rows (token, head) a workgroup takes at once: 32 or 64.  capacity: cache rows that a
+// sequence's pages may hold.
+int latent_rows(int B, int T, int H, long capacity, bool e4m3);
 size_t latent_workspace_bytes(int rows, bool e4m3);
 int launch_latent_attention(const LatentArgs &a, bool e4m3, int rows, hipStream_t stream);
 

@@ -219,6 +219,25 @@ def test_many_sequences(skg, T, B, H):
     _attention_case(skg, counts, lens, H, 16, False, seed=B)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("counts,lens,H", [([40], [300], 20), ([7, 0, 30, 1], [70, 5, 1000, 600], 20), ([9], [9], 100), ([5, 2], [400, 2], 65)])
+def test_wide_tables(skg, counts, lens, H, e4m3):
+    """Sequences that may be long and are not: the larger tile at few rows, and tables whose ends are never read."""
+    page, width = 64, 4096
+    cache, scale, made = _cache(sum(lens), lens, page, e4m3)
+    table = torch.full((len(lens), width), -7, dtype=torch.int32)
+    table[:, :made.shape[1]] = made
+    _attention_case(skg, counts, lens, H, page, e4m3, seed=sum(lens), single=False, table=table)
+
+
+@pytest.mark.parametrize("B", [63, 64, 65])
+def test_batches_around_a_wave(skg, B):
+    g = torch.Generator().manual_seed(B)
+    counts = torch.randint(0, 4, (B,), generator=g).tolist()
+    lens = [max(c, n) for c, n in zip(counts, torch.randint(0, 300, (B,), generator=g).tolist())]
+    _attention_case(skg, counts, lens, 3, 32, True, seed=B, single=False)
+
+
 def test_large_scores(skg):
     """Scores of hundreds: one key takes all the weight, and the running maximum climbs step after step."""
     _attention_case(skg, [1] * 3, [400, 33, 64], 16, 64, False, seed=9, qscale=60.0)
