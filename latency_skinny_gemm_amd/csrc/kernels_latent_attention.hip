@@ -649,16 +649,15 @@ latent_attention_kernel(Shape s) {
             // a part: the sums in the registers' order, then maxima and sums of weights
             const int lane = here(threadIdx.x & 63), half = lane >> 5, l31 = lane & 31;
             float *part = a.ws + (2 * (size_t)group + (at == 0 ? 1 : 0)) * part_floats<RG>();
+            int tok, head;
+            if (place(rg * 32 + l31, tok, head)) {  // rows of no token or head are not handed on
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
+                for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    *reinterpret_cast<f32x4 *>(part + (((rg * 16 + cs * DB + d) * 4 + v) * 64 + lane) * 4) =
-                        f32x4{acc[d][4 * v], acc[d][4 * v + 1], acc[d][4 * v + 2], acc[d][4 * v + 3]};
-            if (cs == 0 && half == 0) {
-                float *ml = part + R * SKG_LATENT + (rg * 32 + l31) * 2;
-                ml[0] = m;
-                ml[1] = l;
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<f32x4 *>(part + (((rg * 16 + cs * DB + d) * 4 + v) * 64 + lane) * 4) =
+                            f32x4{acc[d][4 * v], acc[d][4 * v + 1], acc[d][4 * v + 2], acc[d][4 * v + 3]};
+                if (cs == 0 && half == 0) *reinterpret_cast<f32x2 *>(part + R * SKG_LATENT + (rg * 32 + l31) * 2) = f32x2{m, l};
             }
             if (at == 0) mine = Shared{b, i, group, 1 + (int)((steps - n + share - 1) / share)};
         }
@@ -697,10 +696,19 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
     const float kv_scale = scale ? scale[0] : 1.0f;
     for (int rg = 0; rg < RG; ++rg) {
         const int r = rg * 32 + (lane & 31);
+        int tok = e.i * s.tp, head = g * R + r;
+        bool live = head < a.H;
+        if (a.H <= R) {
+            const int x = r / a.H;
+            head = r - x * a.H;
+            live = x < s.tp && tok + x < q.n;
+            tok += x;
+        }
+        if (!__any(live)) continue;  // the same in every wave
         float m = -__builtin_inff(), l = 0.0f;
         f32x4 sum[4] = {};
         constexpr int U = 4;  // parts whose loads are under way together
-        for (int p0 = wave; p0 < e.parts; p0 += 4 * U) {
+        for (int p0 = live ? wave : e.parts; p0 < e.parts; p0 += 4 * U) {
             f32x2 ml[U];
             f32x4 y[U][4];
 #pragma unroll
@@ -731,14 +739,6 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
             add_part(m, l, one, stats[w][lane], y);
         }
         __syncthreads();
-        int tok = e.i * s.tp, head = g * R + r;
-        bool live = head < a.H;
-        if (a.H <= R) {
-            const int x = r / a.H;
-            head = r - x * a.H;
-            live = x < s.tp && tok + x < q.n;
-            tok += x;
-        }
         if (!live) continue;
         const float inv = l == 0.0f ? 0.0f : kv_scale / l;
         *reinterpret_cast<uint2 *>(a.out + ((size_t)(q.first + tok) * a.H + head) * SKG_LATENT + d * 32 + 8 * wave + 4 * half) =
