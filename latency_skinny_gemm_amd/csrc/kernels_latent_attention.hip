@@ -679,8 +679,8 @@ latent_attention_kernel(Shape s) {
 }
 
 // Row tiles that several workgroups shared.  One workgroup for a record and 32
-// columns; a wave adds up every fourth part in the order of the steps, then the
-// waves' sums are added in theirs.
+// columns.  Up to four parts: a wave joins 8 of the columns in the order of the steps.
+// More: a wave adds up every fourth part, then the waves' sums are added in their order.
 template <int RG>
 __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const float *scale, int G) {
     constexpr int R = 32 * RG;
@@ -694,30 +694,73 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
     const Tokens q = new_tokens(a.q_starts, e.b, a.T);
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63, half = lane >> 5;
     const float kv_scale = scale ? scale[0] : 1.0f;
+    auto part = [&](int p) { return a.ws + (2 * (size_t)(group + p * s.hg) + (p == 0 ? 1 : 0)) * part_floats<RG>(); };
+    auto columns = [&](int rg, int v) { return (((rg * 16 + d) * 4 + v) * 64 + lane) * 4; };
+    // (token, head) of a row of the tile
+    auto place = [&](int r, int &tok, int &head) {
+        tok = e.i * s.tp;
+        head = g * R + r;
+        if (a.H > R) return head < a.H;
+        const int x = r / a.H;
+        head = r - x * a.H;
+        const bool ok = x < s.tp && tok + x < q.n;
+        tok += x;
+        return ok;
+    };
+    auto store = [&](int tok, int head, f32x4 sum, float l) {
+        const float inv = l == 0.0f ? 0.0f : kv_scale / l;
+        *reinterpret_cast<uint2 *>(a.out + ((size_t)(q.first + tok) * a.H + head) * SKG_LATENT + d * 32 + 8 * wave + 4 * half) =
+            to_bf16x4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+    };
+    constexpr int U = 4;  // parts whose loads are under way together
+    if (e.parts <= U) {
+        f32x2 ml[RG][U];
+        f32x4 y[RG][U];
+        int tok[RG], head[RG];
+        bool live[RG];
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) {
+            const int r = rg * 32 + (lane & 31);
+            live[rg] = place(r, tok[rg], head[rg]);
+#pragma unroll
+            for (int p = 0; p < U; ++p)
+                if (p < e.parts && live[rg]) {
+                    ml[rg][p] = *reinterpret_cast<const f32x2 *>(part(p) + R * SKG_LATENT + 2 * r);
+                    y[rg][p] = *reinterpret_cast<const f32x4 *>(part(p) + columns(rg, wave));
+                }
+        }
+#pragma unroll
+        for (int rg = 0; rg < RG; ++rg) {
+            if (!live[rg]) continue;
+            float m = -__builtin_inff(), l = 0.0f;
+            f32x4 sum[1] = {};
+#pragma unroll
+            for (int p = 0; p < U; ++p)
+                if (p < e.parts) {
+                    const f32x4 one[1] = {y[rg][p]};
+                    add_part(m, l, sum, ml[rg][p], one);
+                }
+            store(tok[rg], head[rg], sum[0], l);
+        }
+        return;
+    }
     for (int rg = 0; rg < RG; ++rg) {
         const int r = rg * 32 + (lane & 31);
-        int tok = e.i * s.tp, head = g * R + r;
-        bool live = head < a.H;
-        if (a.H <= R) {
-            const int x = r / a.H;
-            head = r - x * a.H;
-            live = x < s.tp && tok + x < q.n;
-            tok += x;
-        }
+        int tok, head;
+        const bool live = place(r, tok, head);
         if (!__any(live)) continue;  // the same in every wave
         float m = -__builtin_inff(), l = 0.0f;
         f32x4 sum[4] = {};
-        constexpr int U = 4;  // parts whose loads are under way together
         for (int p0 = live ? wave : e.parts; p0 < e.parts; p0 += 4 * U) {
             f32x2 ml[U];
             f32x4 y[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int p = min(p0 + 4 * u, e.parts - 1);
-                const float *x = a.ws + (2 * (size_t)(group + p * s.hg) + (p == 0 ? 1 : 0)) * part_floats<RG>();
+                if (p0 + 4 * u >= e.parts) break;
+                const float *x = part(p0 + 4 * u);
                 ml[u] = *reinterpret_cast<const f32x2 *>(x + R * SKG_LATENT + 2 * r);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[u][v] = *reinterpret_cast<const f32x4 *>(x + (((rg * 16 + d) * 4 + v) * 64 + lane) * 4);
+                for (int v = 0; v < 4; ++v) y[u][v] = *reinterpret_cast<const f32x4 *>(x + columns(rg, v));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -739,10 +782,7 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
             add_part(m, l, one, stats[w][lane], y);
         }
         __syncthreads();
-        if (!live) continue;
-        const float inv = l == 0.0f ? 0.0f : kv_scale / l;
-        *reinterpret_cast<uint2 *>(a.out + ((size_t)(q.first + tok) * a.H + head) * SKG_LATENT + d * 32 + 8 * wave + 4 * half) =
-            to_bf16x4(one[0][0] * inv, one[0][1] * inv, one[0][2] * inv, one[0][3] * inv);
+        if (live) store(tok, head, one[0], l);
     }
 }
 
