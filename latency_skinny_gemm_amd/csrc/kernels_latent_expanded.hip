@@ -42,7 +42,9 @@ constexpr int kShared = 8 * kOwnBlock, kKeyBytes = kShared + 4 * kSharedBlock, k
 constexpr int kLoads = 5;  // a wave's direct loads a step: 8 keys, their shared parts, 8 values
 constexpr int kFlags = kSlots * (kKeyBytes + kValueBytes);
 constexpr size_t kExpandedLds = std::max<size_t>(kFlags + 64, (SKG_LATENT_MAX_B + 1) * 8 + 64);
-constexpr int kLeast = 8;                                        // a part's least number of steps: the join costs as much
+// A part's least number of steps: 100 tokens of 16 heads over 4000 keys 33, 24, 25 us with
+// 4, 8 and 16 (82 in one part), over 1000 18, 18 and 27.
+constexpr int kLeast = 8;
 constexpr int kAhead = 5;                                        // fragments of keys under way
 constexpr size_t kPart = (size_t)kRows * (SKG_EXPANDED_V + 2);   // floats of a part: sums, maxima, sums of weights
 constexpr int kQuery = SKG_EXPANDED_NOPE + SKG_LATENT_ROPE;

@@ -384,7 +384,8 @@ def test_expanded_unseen_and_behind(skg):
 # ------------------------------------------------------------ products per head
 
 @pytest.mark.parametrize("T,H,N,K,pad", [(1, 1, 8, 32, 0), (1, 128, 512, 128, 64), (3, 5, 40, 96, 0), (16, 2, 128, 512, 0),
-                                         (17, 3, 512, 128, 8), (130, 4, 128, 512, 0), (300, 2, 72, 480, 32)])
+                                         (17, 3, 512, 128, 8), (130, 4, 128, 512, 0), (300, 2, 72, 480, 32),
+                                         (140, 3, 512, 128, 64), (33, 2, 128, 512, 0), (65, 2, 40, 256, 0)])
 def test_heads_gemm(skg, T, H, N, K, pad):
     x, w = _randn(T + N, T, H, K + pad).bfloat16(), (_randn(K, H, N, K) * K ** -0.5).bfloat16()
     out, bound = ref.heads(x[..., :K], w)

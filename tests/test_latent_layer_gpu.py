@@ -233,7 +233,7 @@ def test_expanded_keys_past_32_bits(skg):  # noqa: F811
     ref.check(got, out, bound)
 
 
-@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("T", [3, 70, 200])
 def test_heads_past_32_bits(skg, T):  # noqa: F811
     """Strides from token to token that leave 4 GiB behind, of x and of the output."""
     H, N, K = 2, 40, 128
