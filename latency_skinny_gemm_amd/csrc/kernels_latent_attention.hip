@@ -222,8 +222,45 @@ latent_attention_kernel(Shape s) {
     unsigned epoch = 0;  // steps so far: a step's flag is its number
     Shared mine{0, 0, 0, 0};
 
-    // ---- constants of the lane
+    // ---- the first row tile's queries and table entries, under way with the constants
     const int half = lane >> 5, l15 = lane & 15, l31 = lane & 31, g4 = lane >> 4;
+    const int own_row = (CS == 4 ? (cs >> 1) * 16 : 0) + l15;  // whose weights this lane makes; and, with both halves, own_row + 16
+    int j0 = i * s.tp;                                         // the row tile's first token
+    // (token, head) of a row of the tile
+    auto place = [&](int r, int &tok, int &head) {
+        if (a.H > R) {
+            tok = j0;
+            head = g * R + r;
+            return head < a.H;
+        }
+        tok = r / a.H;
+        head = r - tok * a.H;
+        const bool ok = tok < s.tp && j0 + tok < q.n;
+        tok += j0;
+        return ok;
+    };
+    // queries: fragments of 16 rows by 32 values
+    bf16x8 qf[QR][18];
+    auto load_queries = [&] {
+        const Rsrc rq = make_rsrc(a.q + ((size_t)(q.first + j0) * a.H + (a.H > R ? g * R : 0)) * SKG_LATENT_ROW, left > 0 ? R * SKG_LATENT_ROW * 2u : 0u);
+#pragma unroll
+        for (int x = 0; x < QR; ++x) {
+            int qt, qh;
+            const int r = rg * 32 + own_row + 16 * x;  // rows of a tile lie one after another
+            const unsigned off = place(r, qt, qh) ? (unsigned)(r * SKG_LATENT_ROW + g4 * 8) * 2u : kOOB;
+#pragma unroll
+            for (int k = 0; k < 18; ++k) qf[x][k] = __builtin_bit_cast(bf16x8, load16<kCacheDefault>(rq, off + k * 64));
+        }
+    };
+    const bool wide = a.page_shift >= 5;
+    auto table_entry = [&](int step) {
+        const long e = ((long)step * kTile + here(threadIdx.x & 63) * (wide ? kTile : 8)) >> a.page_shift;
+        return e < a.W ? a.table[(size_t)b * a.W + e] : -1;
+    };
+    load_queries();
+    int page = left > 0 ? table_entry(at) : -1;
+
+    // ---- constants of the lane
     unsigned src[LOADS];
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
@@ -259,11 +296,9 @@ latent_attention_kernel(Shape s) {
     // Weights of 16 cache rows by 16 rows, four of a row a lane: into a row's 32 in the
     // order in which the second product's lanes take eight of them, the row's four
     // 16-byte pieces permuted.  Scores likewise, in the order of the cache rows.
-    const int own_row = (CS == 4 ? (cs >> 1) * 16 : 0) + l15;  // and, with both halves, own_row + 16
     const unsigned put_at = (unsigned)((rg * 32 + own_row) * 64 + (((step_half * 2 + (g4 & 1)) ^ ((own_row >> 2) & 3)) * 16) + (g4 >> 1) * 8);
     const unsigned get_at = (unsigned)((rg * 32 + l31) * 64 + ((half ^ ((l31 >> 2) & 3)) * 16));
     const unsigned ring = (unsigned)uniform((int)lds_address(lds_raw + wave * WR * ROWB));
-    const bool wide = a.page_shift >= 5;
     const float kv_scale = E4M3 ? a.scale[0] : 1.0f;
     const float factor = a.factor * kv_scale;
 
@@ -271,22 +306,8 @@ latent_attention_kernel(Shape s) {
     while (left > 0) {
         const int steps = tile_steps(before, q.n, s.tp, i);
         const int n = uniform((int)min((long)(steps - at), left));  // this workgroup's steps of it
-        const int j0 = i * s.tp;                                   // first token
         const int lim0 = max(before + j0 + 1, 0);                  // rows that it sees
         const int most = max(before + min(j0 + s.tp, q.n), 0);     // and the last one
-        // (token, head) of a row of the tile
-        auto place = [&](int r, int &tok, int &head) {
-            if (a.H > R) {
-                tok = j0;
-                head = g * R + r;
-                return head < a.H;
-            }
-            tok = r / a.H;
-            head = r - tok * a.H;
-            const bool ok = tok < s.tp && j0 + tok < q.n;
-            tok += j0;
-            return ok;
-        };
         // how many cache rows the rows whose weights this lane makes see
         int lim[QR];
 #pragma unroll
@@ -295,19 +316,6 @@ latent_attention_kernel(Shape s) {
             lim[x] = place(rg * 32 + own_row + 16 * x, tok, head) ? max(before + tok + 1, 0) : 0;
         }
 
-        // queries: fragments of 16 rows by 32 values
-        bf16x8 qf[QR][18];
-        {
-            const Rsrc rq = make_rsrc(a.q + ((size_t)(q.first + j0) * a.H + (a.H > R ? g * R : 0)) * SKG_LATENT_ROW, R * SKG_LATENT_ROW * 2u);
-#pragma unroll
-            for (int x = 0; x < QR; ++x) {
-                int qt, qh;
-                const int r = rg * 32 + own_row + 16 * x;  // rows of a tile lie one after another
-                const unsigned off = place(r, qt, qh) ? (unsigned)(r * SKG_LATENT_ROW + g4 * 8) * 2u : kOOB;
-#pragma unroll
-                for (int k = 0; k < 18; ++k) qf[x][k] = __builtin_bit_cast(bf16x8, load16<kCacheDefault>(rq, off + k * 64));
-            }
-        }
         // Where this wave's rows of 64 steps lie in the cache, and how many bytes of them
         // there are, one step a lane; of 16 steps in fours where a step may have several
         // pages.  held: whose page is one of the cache's, a bit a lane.
@@ -315,12 +323,10 @@ latent_attention_kernel(Shape s) {
         const unsigned known = wide ? 64 : 16;  // steps
         unsigned place_lo = 0, place_hi = 0, place_bytes = 0;
         unsigned long long held = 0;
-        auto fill = [&](int step) {
+        auto fill = [&](int step, int page) {
             const int lane = here(threadIdx.x & 63);
             first = step;
             const long row = (long)step * kTile + lane * (wide ? kTile : 8);
-            const long e = row >> a.page_shift;
-            const int page = e < a.W ? a.table[(size_t)b * a.W + e] : -1;
             wait_vmcnt_lds<0>();
             const bool ok = (unsigned)page < (unsigned)a.pages;
             held = __ballot(ok);
@@ -333,7 +339,7 @@ latent_attention_kernel(Shape s) {
         };
         // Its wait is for the queries as well: the compiler then waits for no load inside the
         // loop over the ring.
-        fill(at);
+        fill(at, page);
         // The sums take 128 of the 256 registers that vector instructions reach; the queries,
         // which only the matrix instruction reads, go to the others.
         if constexpr (QR == 2) {
@@ -368,7 +374,7 @@ latent_attention_kernel(Shape s) {
             Rsrc rs;
             unsigned dst;
             auto look_up = [&](int step) {
-                if (__builtin_expect((unsigned)(step - first) >= known, 0)) fill(step);
+                if (__builtin_expect((unsigned)(step - first) >= known, 0)) fill(step, table_entry(step));
             };
             auto locate = [&](int step, int slot) {
                 const int i0 = (step - first) * (wide ? 1 : 4), own = i0 + (wide ? 0 : WR * wave >> 3);
@@ -637,7 +643,7 @@ latent_attention_kernel(Shape s) {
             __syncthreads();
             if (!uniform((int)some)) break;
             careful = true;
-            fill(at);
+            fill(at, table_entry(at));
         }
         l = other_half_sum(l);
 
@@ -682,6 +688,11 @@ latent_attention_kernel(Shape s) {
                 q = uniform(new_tokens(a.q_starts, b, a.T));
             } while (q.n == 0);  // steps are left, so there is one
             before = uniform(length(b)) - q.n;
+        }
+        if (left > 0) {
+            j0 = i * s.tp;
+            load_queries();
+            page = table_entry(0);
         }
     }
     if (!s.by_tile && t == 0) records[group] = mine;
