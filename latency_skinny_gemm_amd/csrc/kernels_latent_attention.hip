@@ -25,7 +25,8 @@ struct Shape {
     int tp;         // tokens a row tile
     int hg;         // head groups (row tiles a token, if it has more heads than a tile rows)
     int teams;      // groups that hold all head groups of some tokens
-    int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 27.1, 22.6, 21.6, 22.0 us with 2, 4, 6, 8
+    int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 24.4, 21.3, 20.5, 21.3 us with
+                    // 2, 4, 6, 8, 10 of 16 heads over 3000 e4m3 rows 22.9, 22.4, 23.4, 25.6
     int anew;       // steps that a team's beginning of another row tile costs it
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
@@ -107,8 +108,7 @@ latent_attention_kernel(Shape s) {
     constexpr int QR = 3 - CS / 2;                                                       // halves of the 32 rows that a wave scores
     constexpr int WR = kTile / NW, PIECES = ROWB / 16, LOADS = (WR * PIECES + 63) / 64;  // rows that a wave brings
     constexpr int DB = 16 / CS;                                                         // blocks of 32 columns a wave
-    constexpr bool ROOMY = groups_of(RG, E4M3) / 256 * NW == 4;  // a wave a SIMD
-    constexpr int KD = ROOMY ? 4 : 2, VD = ROOMY ? 3 : 2, YN = ROOMY ? 2 : 1;  
+    constexpr int KD = 4, VD = 3, YN = 2;  // fragments of keys and of values under way, sums of a score
     using Key = std::conditional_t<E4M3, i32x2, u32x4>;  // fragments as they lie in LDS
     using Value = std::conditional_t<E4M3, i32x2, s16x8>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds_raw[];
@@ -432,7 +432,7 @@ latent_attention_kernel(Shape s) {
             // last step the scores are those of zeros, and unused.
             auto scaled = [&](int row0, unsigned bits) {
 #pragma unroll
-                for (int x = 0; x < QR; ++x) last[x] = (YN == 2 ? y[x][0] + y[x][YN - 1] : y[x][0]) * factor;
+                for (int x = 0; x < QR; ++x) last[x] = (y[x][0] + y[x][1]) * factor;
                 if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
                     const bool held = bits >> (step_half * 2 + (g4 >> 1)) & 1u;
 #pragma unroll
@@ -812,7 +812,7 @@ template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     constexpr int G = groups_of(RG, E4M3);
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, 6, 4, 0};
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, E4M3 ? 4 : 6, 4, 0};
     s.teams = G / s.hg;
     s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
