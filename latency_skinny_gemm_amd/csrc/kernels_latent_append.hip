@@ -30,10 +30,11 @@ __device__ __forceinline__ float to_odd(double v) {
     return __uint_as_float((u & 1u) || d == v ? u : other);
 }
 // The quotient u / s as the division's instructions end, without its scaling: with
-// inv = 1 / s rounded, one correction of u inv; exact where the quotient is.
+// inv = 1 / s rounded, one correction of u inv; exact where the quotient is.  Without it
+// where it would meet an infinity.
 __device__ __forceinline__ double over(double u, double s, double inv) {
     const double q = u * inv;
-    return fabs(q) < __builtin_inf() ? __builtin_fma(__builtin_fma(-q, s, u), inv, q) : q;
+    return fabs(q) < __builtin_inf() && inv != 0.0 ? __builtin_fma(__builtin_fma(-q, s, u), inv, q) : q;
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {

@@ -453,7 +453,10 @@ int launch_latent_expanded(const ExpandedArgs &a, hipStream_t stream) {
     if (e != hipSuccess) return (int)e;
     hipLaunchKernelGGL(latent_expanded_kernel, dim3((unsigned)((total + 7) / 8 * 8)), dim3(256), kExpandedLds, stream, a, (int)tiles);
     if (a.parts > 1) {
-        const size_t lds = a.B > 1 ? ((size_t)a.B + 1) * 8 + 64 : 0;
+        const size_t lds = a.B > 64 ? ((size_t)a.B + 1) * 8 + 64 : 0;
+        static std::atomic<unsigned long long> join_done{0};
+        const hipError_t f = allow_dynamic_lds((const void *)latent_expanded_join_kernel, (SKG_LATENT_MAX_B + 1) * 8 + 64, join_done);
+        if (f != hipSuccess) return (int)f;
         hipLaunchKernelGGL(latent_expanded_join_kernel, dim3((unsigned)(tiles * a.H * 4)), dim3(256), lds, stream, a, (int)tiles);
     }
     return (int)hipGetLastError();

@@ -126,6 +126,21 @@ def test_append_ends_of_the_types(skg):
         assert torch.equal(cd.cpu().view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("scale", [math.inf, 0.0, 2.0 ** -149, -0.05, 3.0, math.nan])
+def test_append_odd_scales(skg, scale):
+    kv = _randn(21, 4, 576)
+    kv[1] = 0.0
+    kv[2, 5] = math.inf
+    kv = kv.bfloat16()
+    cache, _, table = _cache(22, [4], 8, True)
+    rot, s = ref.rotation_rows(8), torch.tensor([scale])
+    want, _, _ = ref.append(kv, None, 0.0, rot, "halves", cache, s, table, [4], [0, 4], None)
+    cd, td, sd = _dev(cache, table, s)
+    skg.latent_append(kv.to(DEV), cd, td, _ints([4]).to(DEV), rot.to(DEV), q_starts=_ints([0, 4]).to(DEV), scale=sd, rope="halves")
+    got, want = cd.cpu().float(), want.float()
+    assert torch.equal(torch.nan_to_num(got, nan=1e9), torch.nan_to_num(want, nan=1e9))
+
+
 def test_append_where_there_is_no_row(skg):
     """Pages outside the cache, tokens before row 0, lengths past the table, tokens behind the last sequence."""
     page, H = 8, 2
@@ -355,6 +370,19 @@ def test_expanded_many_sequences(skg):
     out, bound = ref.expanded(q, kv, lat[:, 512:], qs.tolist(), ks.tolist(), SCALE, True)
     qd, kd, ld, sd = _dev(q, kv, lat, qs)
     ref.check(skg.latent_attention_expanded(qd, kd, ld[:, 512:], sd, SCALE), out, bound)
+
+
+@pytest.mark.parametrize("B,live", [(70, 70), (8192, 6)])
+def test_expanded_many_sequences_share_keys(skg, B, live):
+    """Batches past a wave, and the largest, whose few query tokens have their keys shared among workgroups."""
+    g = torch.Generator().manual_seed(B)
+    counts, keys = [0] * B, [0] * B
+    for b in torch.randperm(B, generator=g)[:live].tolist():
+        counts[b], keys[b] = 1 + b % 2, 500 + 7 * (b % 30)
+    q, kv, lat, qs, ks = _prompt_inputs(3, counts, keys, 1)
+    out, bound = ref.expanded(q, kv, lat[:, 512:], qs.tolist(), ks.tolist(), SCALE, True)
+    qd, kd, ld, sd, td = _dev(q, kv, lat, qs, ks)
+    ref.check(skg.latent_attention_expanded(qd, kd, ld[:, 512:], sd, SCALE, kv_starts=td), out, bound)
 
 
 def test_expanded_unseen_and_behind(skg):
