@@ -324,3 +324,58 @@ def test_refusals(skg):  # noqa: F811
 def test_the_package_has_them():
     for name in ("latent_append", "latent_attention", "latent_attention_expanded", "heads_gemm", "reserve_latent"):
         assert callable(getattr(pkg, name))
+
+
+# ------------------------------------------------------------ the largest batches and head counts
+
+def test_largest_batch(skg):  # noqa: F811
+    """8192 sequences: appended to and read, one token each, and a few of several."""
+    B, page = 8192, 8
+    g = torch.Generator().manual_seed(9)
+    lens = torch.randint(0, 2 * page + 3, (B,), generator=g).tolist()
+    cache, _, table = _cache(23, [2 * page] * B, page, False, spare=1)
+    kv, q = _randn(24, B, 576).bfloat16(), _randn(25, B, 1, 576).bfloat16()
+    rot = ref.rotation_rows(2 * page)
+    n = _ints(lens).to(DEV)
+    cd, td = _dev(cache, table)
+    skg.latent_append(kv.to(DEV), cd, td, n, rot.to(DEV))
+    want, _, _ = ref.append(kv, None, 1e-6, rot, "pairs", cache, None, table, lens, None, None)
+    assert torch.equal(cd.cpu().view(torch.int16), want.view(torch.int16))
+    out, bound = ref.attention(q, want, None, table, lens, None, SCALE)
+    ref.check(skg.latent_attention(q.to(DEV), cd, td, n, SCALE), out, bound)
+    # most of them without a token
+    counts = [0] * B
+    for b in (0, 1, 4000, 8191):
+        counts[b], lens[b] = 3, 9
+    starts = _starts(counts)
+    few, fq = _randn(26, 12, 576).bfloat16(), _randn(27, 12, 2, 576).bfloat16()
+    n = _ints(lens).to(DEV)
+    skg.latent_append(few.to(DEV), cd, td, n, rot.to(DEV), q_starts=starts.to(DEV))
+    want, _, _ = ref.append(few, None, 1e-6, rot, "pairs", want, None, table, lens, starts.tolist(), None)
+    assert torch.equal(cd.cpu().view(torch.int16), want.view(torch.int16))
+    out, bound = ref.attention(fq, want, None, table, lens, starts.tolist(), SCALE)
+    ref.check(skg.latent_attention(fq.to(DEV), cd, td, n, SCALE, q_starts=starts.to(DEV)), out, bound)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_most_heads(skg, e4m3):  # noqa: F811
+    H, lens, counts = 1024, [70, 33], [1, 2]
+    cache, scale, table = _cache(28, lens, 16, e4m3)
+    q = _randn(29, 3, H, 576).bfloat16()
+    starts = _starts(counts)
+    out, bound = ref.attention(q, cache, scale, table, lens, starts.tolist(), SCALE)
+    sd = None if scale is None else scale.to(DEV)
+    ref.check(skg.latent_attention(*_dev(q, cache, table, _ints(lens)), SCALE, q_starts=starts.to(DEV), scale=sd), out, bound)
+    if e4m3:
+        return
+    eq, ekv, ekr = _randn(30, 3, H, 192).bfloat16(), _randn(31, 40, H, 256).bfloat16(), _randn(32, 40, 64).bfloat16()
+    out, bound = ref.expanded(eq, ekv, ekr, [0, 3], [0, 40], SCALE, True)
+    ref.check(skg.latent_attention_expanded(*_dev(eq, ekv, ekr, _ints([0, 3])), SCALE, kv_starts=_ints([0, 40]).to(DEV)), out, bound)
+    x, w = _randn(33, 5, H, 64).bfloat16(), (_randn(34, H, 16, 64) / 8).bfloat16()
+    out, bound = ref.heads(x, w)
+    ref.check(skg.heads_gemm(*_dev(x, w)), out, bound)
+    kv, qr = _randn(35, 3, 576).bfloat16(), _randn(36, 3, H, 64).bfloat16()
+    rot = ref.rotation_rows(table.shape[1] * 16)
+    got = skg.latent_append(kv.to(DEV), cache.to(DEV), table.to(DEV), _ints(lens).to(DEV), rot.to(DEV), q_starts=starts.to(DEV), q_rope=qr.to(DEV)).q_rope
+    _, _, want = ref.append(kv, None, 1e-6, rot, "pairs", cache, None, table, lens, starts.tolist(), qr)
+    ref.check(got, want, 1.01 * 2.0 ** -8 * want.abs() + 2.0 ** -22 * qr.double().abs().amax())  # two fp32 products and their sum, one rounding
