@@ -27,7 +27,7 @@ struct Shape {
     int teams;      // groups that hold all head groups of some tokens
     int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 24.4, 21.3, 20.5, 21.3 us with
                     // 2, 4, 6, 8, 10 of 16 heads over 3000 e4m3 rows 22.9, 22.4, 23.4, 25.6
-    int anew;       // steps that a team's beginning of another row tile costs it
+    int anew;       // steps that beginning a row tile costs
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
 
@@ -127,7 +127,9 @@ latent_attention_kernel(Shape s) {
     Shared *const records = reinterpret_cast<Shared *>(a.ws + 2 * (size_t)G * part_floats<RG>());
 
     // ---- this team's share of all steps
-    int b = 0, i = 0, before = 0, at = 0;  // sequence, row tile and its first step; rows before the sequence's new ones
+    // A row tile counts as `anew` steps more than it has, in front of them; a share that
+    // ends among those does not begin the tile.
+    int b = 0, i = 0, before = 0, unit = 0;  // sequence, row tile and its first counted step; rows before the sequence's new ones
     Tokens q{0, 0};
     long share, left = 0;
     auto uniform_long = [](long v) { return (long)((unsigned long)(unsigned)uniform((int)(v >> 32)) << 32 | (unsigned)uniform((int)v)); };
@@ -142,20 +144,20 @@ latent_attention_kernel(Shape s) {
         int lo = 0, hi = (q.n + s.tp - 1) / s.tp;
         while (hi - lo > 1) {
             const int step = (hi - lo + 63) / 64, cand = lo + lane * step;
-            const bool in = cand < hi && steps_before(before, q.n, s.tp, cand) <= off;
+            const bool in = cand < hi && steps_before(before, q.n, s.tp, cand) + (long)cand * s.anew <= off;
             const int idx = __popcll(__ballot(in)) - 1;
             lo += idx * step;
             hi = min(hi, lo + step);
         }
         i = uniform(lo);
-        at = uniform((int)(off - (i ? steps_before(before, q.n, s.tp, i) : 0)));
+        unit = uniform((int)(off - (i ? steps_before(before, q.n, s.tp, i) + (long)i * s.anew : 0)));
     };
     if (a.B <= 64) {  // a sequence a lane, every wave for itself: one round of loads, no barrier
         const int own_b = min(lane, a.B - 1);
         const Tokens own = new_tokens(a.q_starts, own_b, a.T);
         const int own_before = length(own_b) - own.n, tiles = lane < a.B ? (own.n + s.tp - 1) / s.tp : 0;
         const int longest = tiles ? tile_steps(own_before, own.n, s.tp, tiles - 1) : 0;
-        const long steps = steps_before(own_before, own.n, s.tp, tiles);
+        const long steps = steps_before(own_before, own.n, s.tp, tiles) + (long)tiles * s.anew;
         long upto = steps;
         int all = tiles;
         for (int d = 1; d < a.B; d <<= 1) {
@@ -166,9 +168,9 @@ latent_attention_kernel(Shape s) {
         const long total = of_lane(upto, a.B - 1);
         all = __builtin_amdgcn_readlane(all, a.B - 1);
         share = uniform_long(share_of(total));
-        // Shares of one row tile each, where they are little longer: a team whose share goes
-        // on in another tile begins anew there.
-        int whole = (int)min(share, 0x7FFFFFFFL), parts = 0, need = s.teams + 1;
+        // Shares of one row tile each, where they are little longer: a team that goes on in
+        // the middle of a tile begins it as well.
+        int whole = (int)min(share_of(total - (long)all * s.anew), 0x7FFFFFFFL), parts = 0, need = s.teams + 1;
         while (all <= s.teams && whole <= share + s.anew) {
             parts = (longest + whole - 1) / whole;
             need = tiles * parts;
@@ -193,8 +195,8 @@ latent_attention_kernel(Shape s) {
                 const int k = __builtin_amdgcn_readlane(parts, b), r = team - __builtin_amdgcn_readlane(need - tiles * parts, b);
                 share = whole;
                 i = uniform(r / k);
-                at = (r - i * k) * whole;
-                left = max(min(whole, tile_steps(before, q.n, s.tp, i) - at), 0);
+                unit = s.anew + (r - i * k) * whole;
+                left = max(min(whole, tile_steps(before, q.n, s.tp, i) + s.anew - unit), 0);
             } else {
                 left = min(total, from + share) - from;
                 seek(from - of_lane(upto - steps, b));
@@ -204,7 +206,8 @@ latent_attention_kernel(Shape s) {
         long *pre = reinterpret_cast<long *>(lds_raw);
         block_prefix<NW>(a.B, pre, reinterpret_cast<long *>(exchange), [&](int b) {
             const Tokens q = new_tokens(a.q_starts, b, a.T);
-            return steps_before(length(b) - q.n, q.n, s.tp, (q.n + s.tp - 1) / s.tp);
+            const int tiles = (q.n + s.tp - 1) / s.tp;
+            return steps_before(length(b) - q.n, q.n, s.tp, tiles) + (long)tiles * s.anew;
         });
         const long total = pre[a.B];
         share = uniform_long(share_of(total));
@@ -258,7 +261,7 @@ latent_attention_kernel(Shape s) {
         return e < a.W ? a.table[(size_t)b * a.W + e] : -1;
     };
     load_queries();
-    int page = left > 0 ? table_entry(at) : -1;
+    int page = left > 0 ? table_entry(max(unit - s.anew, 0)) : -1;
 
     // ---- constants of the lane
     unsigned src[LOADS];
@@ -305,7 +308,9 @@ latent_attention_kernel(Shape s) {
     // ---- row tiles of the share, one after another
     while (left > 0) {
         const int steps = tile_steps(before, q.n, s.tp, i);
-        const int n = uniform((int)min((long)(steps - at), left));  // this workgroup's steps of it
+        const int units = uniform((int)min((long)(steps + s.anew - unit), left));
+        const int at = max(unit - s.anew, 0), n = max(unit + units - s.anew, 0) - at;  // this workgroup's steps of it
+        if (n == 0) break;  // the share ends in front of them
         const int lim0 = max(before + j0 + 1, 0);                  // rows that it sees
         const int most = max(before + min(j0 + s.tp, q.n), 0);     // and the last one
         // how many cache rows the rows whose weights this lane makes see
@@ -679,8 +684,8 @@ latent_attention_kernel(Shape s) {
         if (s.by_tile && at == 0 && t == 0)
             records[b * s.hg + g] = n == steps ? Shared{b, i, group, 1} : mine;
 
-        left -= n;
-        at = 0;
+        left -= units;
+        unit = 0;
         if (left > 0 && ++i * s.tp >= q.n) {
             i = 0;
             do {
@@ -812,7 +817,7 @@ template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     constexpr int G = groups_of(RG, E4M3);
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, E4M3 ? 4 : 6, 4, 0};
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, E4M3 ? 4 : 6, 8, 0};
     s.teams = G / s.hg;
     s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
