@@ -27,7 +27,8 @@ struct Shape {
     int teams;      // groups that hold all head groups of some tokens
     int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 24.4, 21.3, 20.5, 21.3 us with
                     // 2, 4, 6, 8, 10 of 16 heads over 3000 e4m3 rows 22.9, 22.4, 23.4, 25.6
-    int anew;       // steps that beginning a row tile costs
+    int anew;       // steps that beginning a row tile costs: with 5, 8, 12, 16 600 tokens over their own rows, 20 heads,
+                    // take 51, 48, 47, 49 us, 512 tokens over 8192 rows, 128 heads, 885, 870, 860, 868; without 153, 929
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
 };
 
@@ -817,7 +818,7 @@ template <int RG, int CS, bool E4M3>
 int go(const LatentArgs &a, hipStream_t stream) {
     constexpr int R = 32 * RG;
     constexpr int G = groups_of(RG, E4M3);
-    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, E4M3 ? 4 : 6, 8, 0};
+    Shape s{a, a.H > R ? 1 : R / a.H, a.H > R ? (a.H + R - 1) / R : 1, 0, E4M3 ? 4 : 6, E4M3 ? 8 : 12, 0};
     s.teams = G / s.hg;
     s.by_tile = !a.q_starts && (long)a.B * s.hg <= G;
     static std::atomic<unsigned long long> done{0};
@@ -840,11 +841,12 @@ int by_rows(const LatentArgs &a, int rows, hipStream_t stream) {
 
 // 64 rows read the cache half as often and waste fewer rows where H does not divide 32,
 // but fill the device with fewer tiles and hand on twice as much.  Measured, 32 against
-// 64 (bf16, us): 512 tokens of 128 heads over 8192 rows 1180, 916; 150 tokens of 20 heads
-// over 2000 to 9000 rows, 12 sequences, 134, 85; 128 tokens of 16 heads over 16000 rows
-// 105, 97, over 4000 (64 tokens) 32, 46; 100 tokens of 7 heads over 12000, 3 sequences,
-// 39, 43; 4 tokens of 128 heads over 6000, 4 sequences, 25, 36.  (e4m3, us): 99, 85 for
-// the second of these, 99, 103 for the third.
+// 64 (bf16, us): 512 tokens of 128 heads over 8192 rows 1095, 860; 150 tokens of 20 heads
+// over 2000 to 9000 rows, 12 sequences, 130, 74; 128 tokens of 16 heads over 16000 rows
+// 105, 92, 64 over 4000 31, 38; 100 tokens of 7 heads over 12000, 3 sequences, 37, 43; 4
+// tokens of 128 heads over 6000, 4 sequences, 24, 35; 100 tokens of 128 heads over 200 34,
+// 27 (more tiles of 32 rows than workgroups).  The same in e4m3, which has twice the
+// workgroups for 32 rows: 1009, 920; 101, 76; 105, 100 and 37, 41; 42, 45; 31, 40; 29, 28.
 int latent_rows(int B, int T, int H, long capacity, bool e4m3) {
     auto tiles = [&](int rows) {  // of the call if its tokens are spread evenly
         const long tp = H > rows ? 1 : rows / H, hg = H > rows ? (H + rows - 1) / rows : 1;
@@ -854,7 +856,7 @@ int latent_rows(int B, int T, int H, long capacity, bool e4m3) {
     if (few == many) return 32;
     // steps of one of 256 workgroups if all sequences are as long as the table lets them be
     const double share = (double)few * capacity / kTile / 256;
-    return few >= 256 || (many > 2 * few && share >= 20) || (!e4m3 && share >= 48) ? 64 : 32;
+    return few >= 256 || (many > 2 * few && share >= 20) || share >= 48 || (!e4m3 && many > 256) ? 64 : 32;
 }
 
 size_t latent_workspace_bytes(int rows, bool e4m3) {
