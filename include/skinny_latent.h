@@ -81,8 +81,8 @@ typedef struct skinny_latent_batch {
  * kv bf16 with kv_stride values from row to row; weight bf16 [512]; cache
  * [pages, page_size, 576] of cache_dtype (SKG_DTYPE_BF16, or SKG_DTYPE_FP8 with
  * scale, one fp32).  Strides are multiples of 8, tensors 16-byte aligned
- * (scale 4).  rotation_rows >= table_width * page_size.  Two sequences that hold one
- * page write to it in no order. */
+ * (scale 4).  rotation_rows >= max(1, table_width * page_size); new tokens before row 0
+ * are turned by row 0.  Two sequences that hold one page write to it in no order. */
 int skinny_latent_append(const skinny_latent_batch *batch, const void *kv, long kv_stride,
                          const void *weight, float eps, const float *rotations, int rotation_rows,
                          int rope_style, void *cache, int cache_dtype, const float *scale,

@@ -71,6 +71,7 @@ extern "C" int skinny_latent_append(const skinny_latent_batch *batch, const void
         (q && (!strides_fit(T, H, q_token_stride, q_head_stride) || !strides_fit(T, H, out_token_stride, out_head_stride))))
         return SKG_ERR_UNSUPPORTED;
     if (T == 0 || batch->B == 0) return SKG_OK;
+    if (rotation_rows == 0) return SKG_ERR_UNSUPPORTED;  // tokens without a row are turned by the first
     rc = check_batch_pointers(batch);
     if (rc != SKG_OK) return rc;
     if (!kv || !rotations || (!cache && rows > 0)) return SKG_ERR_INVALID_ARG;

@@ -89,6 +89,12 @@ def test_append_refusals(lib, kw, status):
     assert _append(lib, **kw) == status
 
 
+def test_append_without_rotations(lib):
+    """No page and no rotation: new tokens, which then have no row, would still be turned by the first."""
+    assert _append(lib, batch=dict(table_width=0), rows=0) == UNSUP
+    assert _append(lib, batch=dict(table_width=0, T=0), rows=0) == OK
+
+
 def _attend(lib, batch=None, q=A, cache=B, dtype=0, scale=0, softmax=0.1, out=C, heads=3):
     return lib.skinny_latent_attention(_batch(**(batch or {})), q, cache, dtype, scale, softmax, out, heads, None)
 
