@@ -98,7 +98,7 @@ int skinny_latent_append(const skinny_latent_batch *batch, const void *kv, long 
  * instruction.  A token that sees no row gets zeros.  A row that a token does
  * not see has no effect on it, whatever it holds; nor has what a page holds
  * behind the sequence's end.  Results do not depend on the order in which
- * workgroups run.  softmax_scale > 0. */
+ * workgroups run.  0 < softmax_scale <= 2e38. */
 int skinny_latent_attention(const skinny_latent_batch *batch, const void *q, const void *cache,
                             int cache_dtype, const float *scale, float softmax_scale, void *out,
                             int H, hipStream_t stream);
@@ -114,7 +114,7 @@ int skinny_latent_attention(const skinny_latent_batch *batch, const void *q, con
  * T or S, not descending).  causal: its last token sees all its keys, the one
  * before one fewer, and so on; else every token sees all.  Empty rows, unseen
  * keys, precision and order as above.  Tensors 16-byte aligned, k_rope_stride a
- * multiple of 8.  softmax_scale > 0. */
+ * multiple of 8.  0 < softmax_scale <= 2e38. */
 int skinny_latent_attention_expanded(const void *q, const void *kv, const void *k_rope,
                                      long k_rope_stride, const int *q_starts, const int *kv_starts,
                                      void *out, float softmax_scale, int causal, int B, int T,

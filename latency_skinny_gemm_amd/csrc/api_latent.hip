@@ -13,6 +13,7 @@ using namespace skg;
 namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
+constexpr float kMostScale = 2e38f;  // times log2 e it is still a number of fp32
 
 // A product of sizes that reach 2^31 each, at most `most`.
 bool within(double product, double most) { return product <= most; }
@@ -110,7 +111,7 @@ extern "C" int skinny_latent_attention(const skinny_latent_batch *batch, const v
                                        void *out, int H, hipStream_t stream) {
     int rc = check_batch(batch);
     if (rc != SKG_OK) return rc;
-    if (H < 1 || !(softmax_scale > 0.0f) || softmax_scale > 3e38f || (cache_dtype != SKG_DTYPE_BF16 && cache_dtype != SKG_DTYPE_FP8) ||
+    if (H < 1 || !(softmax_scale > 0.0f) || softmax_scale > kMostScale || (cache_dtype != SKG_DTYPE_BF16 && cache_dtype != SKG_DTYPE_FP8) ||
         (scale != nullptr) != (cache_dtype == SKG_DTYPE_FP8))
         return SKG_ERR_INVALID_ARG;
     if (H > SKG_LATENT_MAX_H || !within((double)batch->T * H, (double)(1L << 31))) return SKG_ERR_UNSUPPORTED;
@@ -146,7 +147,7 @@ extern "C" int skinny_latent_attention_expanded(const void *q, const void *kv, c
                                                 const int *kv_starts, void *out, float softmax_scale,
                                                 int causal, int B, int T, int S, int H,
                                                 hipStream_t stream) {
-    if (B < 0 || T < 0 || S < 0 || H < 1 || !(softmax_scale > 0.0f) || softmax_scale > 3e38f || (causal != 0 && causal != 1) ||
+    if (B < 0 || T < 0 || S < 0 || H < 1 || !(softmax_scale > 0.0f) || softmax_scale > kMostScale || (causal != 0 && causal != 1) ||
         k_rope_stride < SKG_LATENT_ROPE || k_rope_stride % 8 != 0)
         return SKG_ERR_INVALID_ARG;
     // a step's rows within 2 GiB of their first

@@ -106,7 +106,7 @@ def test_attention_batch_refusals(lib, batch, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(heads=0), ARG), (dict(softmax=0.0), ARG), (dict(softmax=-1.0), ARG), (dict(softmax=math.nan), ARG),
-    (dict(softmax=math.inf), ARG), (dict(dtype=3), ARG), (dict(dtype=1), ARG), (dict(scale=D), ARG),
+    (dict(softmax=math.inf), ARG), (dict(softmax=2.9e38), ARG), (dict(dtype=3), ARG), (dict(dtype=1), ARG), (dict(scale=D), ARG),
     (dict(heads=1025), UNSUP), (dict(batch=dict(T=1 << 22), heads=1024), UNSUP),
     (dict(q=0), ARG), (dict(cache=0), ARG), (dict(out=0), ARG),
     (dict(q=A + 8), ALIGN), (dict(cache=B + 1), ALIGN), (dict(out=C + 2), ALIGN), (dict(dtype=1, scale=D + 2), ALIGN),
@@ -123,7 +123,7 @@ def _expanded(lib, q=A, kv=B, rope=C, stride=64, qs=D, ks=E, out=F, softmax=0.1,
 
 @pytest.mark.parametrize("kw,status", [
     (dict(n=-1), ARG), (dict(T=-1), ARG), (dict(S=-1), ARG), (dict(heads=0), ARG), (dict(softmax=0.0), ARG),
-    (dict(softmax=math.inf), ARG), (dict(causal=2), ARG), (dict(stride=56), ARG), (dict(stride=65), ARG),
+    (dict(softmax=math.inf), ARG), (dict(softmax=2.9e38), ARG), (dict(causal=2), ARG), (dict(stride=56), ARG), (dict(stride=65), ARG),
     (dict(n=8193), UNSUP), (dict(heads=1025), UNSUP), (dict(stride=1 << 25), UNSUP), (dict(T=1 << 22, heads=1024), UNSUP),
     (dict(n=8192, heads=1024), UNSUP),
     (dict(T=0), OK), (dict(n=0), OK), (dict(T=0, q=0, kv=0, qs=0), OK),
