@@ -24,7 +24,8 @@
  * elements; the last dimension is always dense); work enqueued on `stream`
  * without synchronising; SKG_OK or a negative SKG_ERR_*, with every argument
  * checked on the host before any HIP call; outputs must not overlap inputs
- * (except where said) or each other.  Calls of one stream share its workspace
+ * (except where said) or each other, from their first value to their last;
+ * tensors of the same strides may be different columns of one matrix.  Calls of one stream share its workspace
  * (skinny_latent_reserve); nothing is kept from one call for the next.
  */
 #ifndef SKINNY_LATENT_H

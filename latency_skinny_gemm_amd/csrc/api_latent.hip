@@ -37,6 +37,29 @@ int shift_of(int page_size) { return __builtin_ctz((unsigned)page_size); }
 size_t strided_bytes(long T, long H, long ts, long hs, long n) {
     return T && H ? (size_t)((T - 1) * ts + (H - 1) * hs + n) * 2 : 0;
 }
+// Rows of n bf16 values, T tokens by H heads, with strides.
+struct Rows {
+    const void *p;
+    long T, H, ts, hs, n;
+    Span span() const { return {p, strided_bytes(T, H, ts, hs, n)}; }
+};
+// Blocks of a and b that begin at every multiple of one period do not meet.
+bool blocks_apart(const Rows &a, long wa, const Rows &b, long wb, long period) {
+    if (wa > period || wb > period) return false;
+    const uintptr_t p = (uintptr_t)period * 2, x = (uintptr_t)a.p % p, y = (uintptr_t)b.p % p;
+    const uintptr_t d = y >= x ? y - x : y + p - x;  // from a's blocks to b's
+    return d >= (uintptr_t)wa * 2 && d + (uintptr_t)wb * 2 <= p;
+}
+// Whether two tensors share memory.  What their spans have in common may be columns of
+// one matrix that both are slices of: by tokens, or by heads where these go on
+// evenly from token to token.
+bool overlap(const Rows &a, const Rows &b) {
+    if (!overlap(a.span(), b.span())) return false;
+    if (a.ts != b.ts || a.ts == 0) return true;
+    if (blocks_apart(a, (a.H - 1) * a.hs + a.n, b, (b.H - 1) * b.hs + b.n, a.ts)) return false;
+    const bool even = a.hs > 0 && a.hs == b.hs && a.ts % a.hs == 0;
+    return !(even && blocks_apart(a, a.n, b, b.n, a.hs));
+}
 bool strides_ok(long ts, long hs) { return ts >= 0 && hs >= 0 && ts % 8 == 0 && hs % 8 == 0; }
 // Rows of an output are apart: tokens outside of heads, or the other way round.
 bool rows_apart(long T, long H, long ts, long hs, long n) {
@@ -82,22 +105,20 @@ extern "C" int skinny_latent_append(const skinny_latent_batch *batch, const void
         return SKG_ERR_ALIGNMENT;
     const bool e4m3 = cache_dtype == SKG_DTYPE_FP8;
     const bool in_place = q == q_out && q_token_stride == out_token_stride && q_head_stride == out_head_stride;
-    const Span q_span{q, strided_bytes(T, H, q_token_stride, q_head_stride, SKG_LATENT_ROPE)};
-    const Span kv_span{kv, strided_bytes(T, 1, kv_stride, 0, SKG_LATENT_ROW)};
-    const Span outs[] = {{cache, (size_t)rows * SKG_LATENT_ROW * (e4m3 ? 1 : 2)},
-                         {latent_out, (size_t)T * SKG_LATENT_ROW * 2},
-                         {q_out, strided_bytes(T, H, out_token_stride, out_head_stride, SKG_LATENT_ROPE)}};
-    const Span ins[] = {kv_span,
-                        {in_place ? nullptr : q, q_span.bytes},
-                        {weight, SKG_LATENT * 2},
+    const Rows kv_rows{kv, T, 1, kv_stride, 0, SKG_LATENT_ROW}, q_rows{q, T, H, q_token_stride, q_head_stride, SKG_LATENT_ROPE},
+        q_out_rows{q_out, T, H, out_token_stride, out_head_stride, SKG_LATENT_ROPE};
+    const Span written[] = {{cache, (size_t)rows * SKG_LATENT_ROW * (e4m3 ? 1 : 2)}, {latent_out, (size_t)T * SKG_LATENT_ROW * 2}};
+    const Span outs[] = {written[0], written[1], q_out_rows.span()};
+    const Span read[] = {kv_rows.span(), q_rows.span()};
+    const Span ins[] = {{weight, SKG_LATENT * 2},
                         {rotations, (size_t)rotation_rows * SKG_LATENT_ROPE * 4},
                         {scale, 4},
                         {batch->table, (size_t)batch->B * batch->table_width * 4},
                         {batch->kv_lens, (size_t)batch->B * 4},
                         {batch->q_starts, ((size_t)batch->B + 1) * 4}};
-    if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
-    const Span apart[] = {outs[0], outs[1]}, query[] = {q_span};
-    if (any_overlap(apart, query)) return SKG_ERR_INVALID_ARG;
+    if (any_overlap(outs, ins) || any_overlap(written, read) || overlap(q_out_rows, kv_rows) ||
+        (!in_place && overlap(q_out_rows, q_rows)))
+        return SKG_ERR_INVALID_ARG;
     const LatentAppendArgs a{(const uint16_t *)kv, (const uint16_t *)weight, (const uint16_t *)q, rotations, scale,
                              batch->table, batch->kv_lens, batch->q_starts, (uint8_t *)cache, (uint16_t *)latent_out,
                              (uint16_t *)q_out, kv_stride, q_token_stride, q_head_stride, out_token_stride,
@@ -192,9 +213,8 @@ extern "C" int skinny_heads_gemm(const void *x, long x_token_stride, long x_head
     if (T == 0 || N == 0) return SKG_OK;
     if (!x || !W || !out || !rows_apart(T, H, out_token_stride, out_head_stride, N)) return SKG_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(out, 16)) return SKG_ERR_ALIGNMENT;
-    const Span outs[] = {{out, strided_bytes(T, H, out_token_stride, out_head_stride, N)}};
-    const Span ins[] = {{x, strided_bytes(T, H, x_token_stride, x_head_stride, K)}, {W, (size_t)H * N * K * 2}};
-    if (any_overlap(outs, ins)) return SKG_ERR_INVALID_ARG;
+    const Rows x_rows{x, T, H, x_token_stride, x_head_stride, K}, out_rows{out, T, H, out_token_stride, out_head_stride, N};
+    if (overlap(out_rows, x_rows) || overlap(out_rows.span(), {W, (size_t)H * N * K * 2})) return SKG_ERR_INVALID_ARG;
     const HeadsArgs a{(const uint16_t *)x, (const uint16_t *)W, (uint16_t *)out, x_token_stride, x_head_stride,
                       out_token_stride, out_head_stride, T, H, N, K};
     return hip_status(launch_heads(a, stream));

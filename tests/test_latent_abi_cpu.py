@@ -83,6 +83,10 @@ def test_append_batch_refusals(lib, batch, status):
     (dict(dtype=1, scale=B + 0x1002), ALIGN), (dict(latent=F + 0x100008), ALIGN), (dict(q=E + 2), ALIGN),
     (dict(cache=A), ARG), (dict(latent=A + 1152 * 4), ARG), (dict(qo=D + 16), ARG), (dict(qo=E + 16), ARG),
     (dict(qo=E, ot=200), ARG),                       # in place, but with other strides
+    (dict(kv_stride=1280, q=A + 1152, qt=1280, qo=A + 1136, ot=1280), ARG),      # queries beside the latents, one piece into them
+    (dict(kv_stride=1280, qo=A + 2192, ot=1280), ARG),                           # or into the next row's
+    (dict(kv_stride=1280, qo=A + 1152, ot=1288), ARG),                           # or at another stride
+    (dict(kv_stride=0x7000, q=E, qt=320, qh=64, qo=E + 368, ot=320, oh=64), ARG),
     (dict(latent=E), ARG), (dict(cache=G - 1152 * 9 * 16 + 16), ARG), (dict(qo=C), ARG),
 ])
 def test_append_refusals(lib, kw, status):
@@ -147,6 +151,8 @@ def _heads(lib, x=A, xt=96, xh=32, W=B, out=C, ot=48, oh=16, T=5, heads=3, N=16,
     (dict(x=0), ARG), (dict(W=0), ARG), (dict(out=0), ARG), (dict(oh=8), ARG), (dict(ot=40), ARG),
     (dict(x=A + 8), ALIGN), (dict(W=B + 4), ALIGN), (dict(out=C + 2), ALIGN),
     (dict(out=A), ARG), (dict(out=B + 16), ARG),
+    (dict(xt=144, xh=48, out=A + 48, ot=144, oh=48), ARG), (dict(xt=144, xh=48, out=A + 80, ot=144, oh=48), ARG),  # columns into others
+    (dict(xt=152, xh=48, out=A + 64, ot=152, oh=48, N=40), ARG),
 ])
 def test_heads_refusals(lib, kw, status):
     assert _heads(lib, **kw) == status

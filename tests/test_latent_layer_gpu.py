@@ -251,6 +251,37 @@ def test_heads_past_32_bits(skg, T):  # noqa: F811
 
 # ------------------------------------------------------------ nothing to do, and refusals
 
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("H", [1, 3])
+def test_columns_of_one_matrix(skg, T, H):  # noqa: F811
+    """Inputs and outputs that are slices of one projection's output: the same values as apart, the rest untouched."""
+    cache, _, table = _cache(60, [9] * T, 8, False)
+    cd, td, lens, rot = cache.to(DEV), table.to(DEV), _ints([9] * T).to(DEV), ref.rotation_rows(16).to(DEV)
+    m = _randn(61, T, H * 192 + 576).bfloat16().to(DEV)
+    q, kv = m[:, :H * 192].unflatten(1, (H, 192)), m[:, H * 192:]
+    apart = skg.latent_append(kv.clone(), cd.clone(), td, lens, rot, q_rope=q[..., 128:].clone(), latent=True)
+    before = m.clone()
+    got = skg.latent_append(kv, cd, td, lens, rot, q_rope=q[..., 128:], q_rope_out=q[..., 128:], latent=True)
+    assert torch.equal(got.latent, apart.latent) and torch.equal(q[..., 128:], apart.q_rope)
+    before[:, :H * 192].unflatten(1, (H, 192))[..., 128:] = apart.q_rope
+    assert torch.equal(m, before)
+    # a head's 128 values, and its 512 latent ones behind them
+    both = _randn(62, T, H, 640).bfloat16().to(DEV)
+    w = _randn(63, H, 512, 128).bfloat16().to(DEV)
+    x, before = both[..., :128], both.clone()
+    want = skg.heads_gemm(x.clone(), w)
+    skg.heads_gemm(x, w, out=both[..., 128:])
+    assert torch.equal(both[..., 128:], want) and torch.equal(x, before[..., :128])
+    # all heads' inputs, then all heads' outputs
+    row = _randn(64, T, H * 640).bfloat16().to(DEV)
+    x, out = row[:, :H * 128].unflatten(1, (H, 128)), row[:, H * 128:].unflatten(1, (H, 512))
+    want = skg.heads_gemm(x.clone(), w)
+    skg.heads_gemm(x, w, out=out)
+    assert torch.equal(out, want)
+    with pytest.raises(skg.SkinnyGemmError):  # one piece into the inputs
+        skg.heads_gemm(both[..., :128], w, out=both[..., 120:632])
+
+
 def test_nothing_to_do(skg):  # noqa: F811
     cache = torch.zeros(2, 8, 576, dtype=torch.bfloat16, device=DEV)
     e = dict(dtype=torch.bfloat16, device=DEV)
