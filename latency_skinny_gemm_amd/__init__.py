@@ -183,6 +183,8 @@ def _empty(shape, dtype, device, stream):
             return _empty(shape, dtype, device, None)
     if len(shape) == 2:  # 1.3 us of host time; torch.empty takes 1.7
         return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+    if len(shape) == 3:
+        return torch.empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype=dtype, device=device)
     return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -114,7 +114,7 @@ def _batch(cache, table, kv_lens, q_starts, T):
         _tensor("q_starts", q_starts, _I32, (B + 1,))
     elif T != B:
         raise ValueError(f"without q_starts every sequence has one new token, got {T} for {B} sequences")
-    _count(max(B, T, W, page, pages))
+    _count(B | T | W | page | pages)  # one of 32 bits or more shows in the union
     return LatentBatch(table.data_ptr(), kv_lens.data_ptr(), None if q_starts is None else q_starts.data_ptr(),
                        B, T, W, page, pages)
 
@@ -225,10 +225,11 @@ def latent_attention_expanded(q, kv, k_rope, q_starts, softmax_scale, kv_starts=
     else:
         _tensor("out", out, _BF16, (T, H, V))
     B = q_starts.shape[0] - 1
+    _count(B | T | S | H)
     rc = _c._launch(_same_device(q, kv, k_rope, q_starts, kv_starts, out), stream,
                     _c._load().skinny_latent_attention_expanded, q.data_ptr(), kv.data_ptr(), k_rope.data_ptr(), rs,
                     q_starts.data_ptr(), kv_starts.data_ptr(), out.data_ptr(), softmax_scale, 1 if causal else 0,
-                    _count(B), _count(T), _count(S), _count(H))
+                    B, T, S, H)
     if rc:
         _c._check(rc, f"skinny_latent_attention_expanded(T={T}, S={S}, B={B}, H={H})")
     return out
@@ -243,13 +244,14 @@ def heads_gemm(x, W, out=None, stream=None):
     H, N, K = W.shape
     xs = _heads("x", x, None, H, K)
     T = x.shape[0]
+    _count(T | H | N | K)
     if out is None:
         out = _c._empty((T, H, N), torch.bfloat16, x.device, stream)
         os = (H * N, N)
     else:
         os = _heads("out", out, T, H, N)
     rc = _c._launch(_same_device(x, W, out), stream, _c._load().skinny_heads_gemm, x.data_ptr(), *xs, W.data_ptr(),
-                    out.data_ptr(), *os, _count(T), _count(H), _count(N), _count(K))
+                    out.data_ptr(), *os, T, H, N, K)
     if rc:
         _c._check(rc, f"skinny_heads_gemm(T={T}, H={H}, N={N}, K={K})")
     return out
