@@ -92,13 +92,14 @@ __device__ __forceinline__ long steps_before(int before, int n, int tp, int upto
 //
 // Workgroups that hold different heads of the same tokens form a team, which takes
 // its share of all steps together, so that a cache row is read from memory once.  Shares
-// are equal numbers of steps, whatever row tile they begin or end in, or of one tile each
-// where that makes them little longer; parts of a tile are joined by the kernel below.
+// are equal numbers of steps, the beginning of a tile counted as some, whatever row tile
+// they begin or end in, or of one tile each where that makes them little longer; parts of
+// a tile are joined by the kernel below.
 //
-// 512 tokens of 128 heads over 8192 rows: 925 us, 945 TFLOP/s, the clock below 1.8 GHz as
+// 512 tokens of 128 heads over 8192 rows: 855 us, 1020 TFLOP/s, the clock below 1.8 GHz as
 // in every kernel here that keeps the matrix pipes half busy.  Decode of 128 sequences,
-// 128 heads, 588 MB: 175 us, of which its loads alone take 150 (4.3 TB/s: a team's
-// workgroups have the same rows under way); 32 sequences, 16 heads, e4m3, 272 MB: 61 us,
+// 128 heads, 588 MB: 170 us, of which its loads alone take 150 (4.3 TB/s: a team's
+// workgroups have the same rows under way); 32 sequences, 16 heads, e4m3, 272 MB: 59 us,
 // loads alone 57.  One token over 4000 rows: 15.5 us, six steps of 0.8 us behind four trips
 // to memory (lengths, table, queries, rows) and a first run through 27 KB of code.
 template <int RG, int CS, bool E4M3>
