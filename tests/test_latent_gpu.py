@@ -425,3 +425,12 @@ def test_heads_gemm(skg, T, H, N, K, pad):
     assert (wide[..., N:] == 5.0).all()
     turned = torch.empty(H, T, N, dtype=torch.bfloat16, device=DEV)
     ref.check(skg.heads_gemm(xd[..., :K].transpose(0, 1).contiguous().transpose(0, 1), wd, out=turned.transpose(0, 1)), out, bound)
+
+
+@pytest.mark.parametrize("K", range(32, 513, 32))
+def test_heads_gemm_of_every_depth(skg, K):
+    """From the tokens on whose rows are worth a ring in LDS, with a last step that is not full, and below."""
+    for T in (19, 16384 // K + 5):
+        x, w = _randn(T + K, T, 2, K).bfloat16(), (_randn(K, 2, 136, K) * K ** -0.5).bfloat16()
+        out, bound = ref.heads(x, w)
+        ref.check(skg.heads_gemm(*_dev(x, w)), out, bound)

@@ -165,6 +165,21 @@ def test_two_graphs_of_one_stream(skg):  # noqa: F811
         assert torch.equal(a, want) and torch.equal(b, ewant), i
 
 
+def test_first_call_of_a_kernel_in_a_graph(skg):  # noqa: F811
+    """A depth that nothing else here takes: its kernel is loaded while the graph is captured."""
+    x, w = _randn(70, 100, 2, 448).bfloat16().to(DEV)[..., :384], (_randn(71, 2, 128, 384) / 20).bfloat16().to(DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = skg.heads_gemm(x, w)
+    for i in range(3):
+        x.copy_(_randn(72 + i, 100, 2, 384).bfloat16())
+        want = skg.heads_gemm(x, w)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+
+
 def test_capture_needs_reserved_workspace(skg):  # noqa: F811
     (q, c, t, n), _ = _absorbed(5, [100], 16)
     eq, ekv, ekr, qs, ks = _expanded(6, 10, 1000, 2)
