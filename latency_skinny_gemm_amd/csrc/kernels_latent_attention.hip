@@ -848,6 +848,10 @@ int by_rows(const LatentArgs &a, int rows, hipStream_t stream) {
 // tokens of 128 heads over 6000, 4 sequences, 24, 35; 100 tokens of 128 heads over 200 34,
 // 27 (more tiles of 32 rows than workgroups).  The same in e4m3, which has twice the
 // workgroups for 32 rows: 1009, 920; 101, 76; 105, 100 and 37, 41; 42, 45; 31, 40; 29, 28.
+// What a table lets sequences be they seldom are, and then 64 rows cost most where the
+// tiles are few: 128 heads (bf16), 32 tokens of sequences of 4000 rows 51, 48, of 24000
+// 208, 172; 16 heads, 64 tokens of 2 sequences of 2000 25, 35, of 24000 75, 67; 128 heads, 4 of 6000
+// 25, 35, of 100000 92, 85.  So below 32 tiles the table's width does not count.
 int latent_rows(int B, int T, int H, long capacity, bool e4m3) {
     auto tiles = [&](int rows) {  // of the call if its tokens are spread evenly
         const long tp = H > rows ? 1 : rows / H, hg = H > rows ? (H + rows - 1) / rows : 1;
@@ -857,7 +861,7 @@ int latent_rows(int B, int T, int H, long capacity, bool e4m3) {
     if (few == many) return 32;
     // steps of one of 256 workgroups if all sequences are as long as the table lets them be
     const double share = (double)few * capacity / kTile / 256;
-    return few >= 256 || (many > 2 * few && share >= 20) || share >= 48 || (!e4m3 && many > 256) ? 64 : 32;
+    return few >= 256 || (many > 2 * few && share >= 20) || (few >= 32 && share >= 48) || (!e4m3 && many > 256) ? 64 : 32;
 }
 
 size_t latent_workspace_bytes(int rows, bool e4m3) {

@@ -179,7 +179,8 @@ def latent_attention(q, cache, table, kv_lens, softmax_scale, q_starts=None, sca
     """Attention in the absorbed form, bf16 [T, H, 512]: q bf16 [T, H, 576] over the
     cache rows (bf16, or float8_e4m3fn with scale) of each token's sequence up to
     its own.  One new token a sequence, or q_starts[b] .. q_starts[b + 1] - 1.
-    Outputs of tokens behind the last sequence are left as they were."""
+    Outputs of tokens behind the last sequence are left as they were.  A table no
+    wider than the longest sequence needs is fastest."""
     _tensor("q", q, _BF16)
     if q.dim() != 3 or q.shape[2] != ROW:
         raise ValueError(f"q must be [T, H, {ROW}], got {list(q.shape)}")

@@ -245,6 +245,17 @@ def test_wide_tables(skg, counts, lens, H, e4m3):
     _attention_case(skg, counts, lens, H, page, e4m3, seed=sum(lens), single=False, table=table)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("counts,lens,H", [([20], [60], 100), ([11, 9], [400, 9], 65)])
+def test_wide_tables_of_many_heads(skg, counts, lens, H, e4m3):
+    """Sequences that may be long and are not: the larger tile at few rows, and tables whose ends are never read."""
+    page, width = 64, 4096
+    cache, scale, made = _cache(sum(lens), lens, page, e4m3)
+    table = torch.full((len(lens), width), -7, dtype=torch.int32)
+    table[:, :made.shape[1]] = made
+    _attention_case(skg, counts, lens, H, page, e4m3, seed=sum(lens), single=False, table=table)
+
+
 @pytest.mark.parametrize("B", [63, 64, 65])
 def test_batches_around_a_wave(skg, B):
     g = torch.Generator().manual_seed(B)
