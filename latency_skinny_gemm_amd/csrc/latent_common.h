@@ -88,11 +88,20 @@ __device__ __forceinline__ unsigned lds_address(const unsigned char *p) {
 // 16 bytes a lane from a buffer straight into LDS, at dst + AT + 16 * lane (dst uniform).
 // Written as an instruction: beside the builtin, the compiler waits for every such
 // load that is under way before a transposed read (vmcnt(0) in each step of the
-// ring).  It writes no register but m0, which nothing else here keeps a value in;
-// the ring's own waits count it.
+// ring).  The ring's own waits count it.  It writes no register but m0, which no asm may
+// declare, being reserved; that nothing else in these kernels uses m0 is checked in the
+// built library.
+//
+// A buffer instruction may read a scalar register that a vector instruction wrote (the
+// descriptors come from v_readlane) five wait states later at the earliest, and one after
+// m0 was written; the compiler does not see that this is one.  The addition and s_nop 3
+// are five, whatever stands before.  Waiting once for each new descriptor instead gains
+// 1 % at most (150 e4m3 tokens of 12 sequences 76.0 us for 76.7, 512 tokens of 128 heads
+// over 8192 rows 934 for 939, a prompt of 4096 759 for 759), and would be wrong where the
+// compiler brings a spilled word back by v_readlane.
 template <int AT>
 __device__ __forceinline__ void ring_load16(Rsrc r, unsigned dst, unsigned off) {
-    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(r), "i"(AT)
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(r), "i"(AT)
                  : "memory", "scc");
 }
 
