@@ -93,7 +93,8 @@ int skinny_latent_append(const skinny_latent_batch *batch, const void *kv, long 
 
 /* out[t, h] = sum_p w_p row_p[0:512], w = softmax over p of
  * softmax_scale * (q[t, h] . row_p), over the rows p of t's sequence up to its
- * own.  Rows of an e4m3 cache stand for code * *scale.  q bf16 [T, H, 576],
+ * own.  Rows of an e4m3 cache stand for code * *scale; softmax_scale * *scale may
+ * leave fp32 where the scores themselves do not.  q bf16 [T, H, 576],
  * out bf16 [T, H, 512], dense.  Scores, maxima, sums and outputs are held in
  * fp32; the weights before their division are rounded to bf16 for the matrix
  * instruction.  A token that sees no row gets zeros.  A row that a token does

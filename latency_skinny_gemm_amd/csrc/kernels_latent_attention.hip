@@ -306,6 +306,10 @@ latent_attention_kernel(Shape s) {
     const unsigned ring = (unsigned)uniform((int)lds_address(lds_raw + wave * WR * ROWB));
     const float kv_scale = E4M3 ? a.scale[0] : 1.0f;
     const float factor = a.factor * kv_scale;
+    // Both are numbers of fp32, their product may be none: then one after the other, so that
+    // a score of 0 is 0 and one that fits is there.
+    bool in_two = false;
+    if constexpr (E4M3) in_two = !(__builtin_fabsf(factor) < __builtin_inff());
 
     // ---- row tiles of the share, one after another
     while (left > 0) {
@@ -440,7 +444,15 @@ latent_attention_kernel(Shape s) {
             auto scaled = [&](int row0, unsigned bits) {
 #pragma unroll
                 for (int x = 0; x < QR; ++x) last[x] = (y[x][0] + y[x][1]) * factor;
-                if (__builtin_expect(row0 + kTile > lim0 || bits != 15u, 0)) {
+                bool rare = row0 + kTile > lim0 || bits != 15u;
+                if constexpr (E4M3) rare |= in_two;
+                if (__builtin_expect(rare, 0)) {
+                    if constexpr (E4M3) {
+                        if (in_two) {
+#pragma unroll
+                            for (int x = 0; x < QR; ++x) last[x] = (y[x][0] + y[x][1]) * kv_scale * a.factor;
+                        }
+                    }
                     const bool held = bits >> (step_half * 2 + (g4 >> 1)) & 1u;
 #pragma unroll
                     for (int x = 0; x < QR; ++x)
