@@ -52,6 +52,19 @@ constexpr size_t lds_bytes() {
 static_assert(lds_bytes<2, false>() <= 160 * 1024 && 2 * lds_bytes<1, true>() <= 160 * 1024, "a CU's LDS");
 static_assert((SKG_LATENT_MAX_B + 1) * 8 <= kRing * kTile * row_bytes(true), "prefix sums fit the ring");
 
+// Sums of weighted codes to values: times the cache's scale, over the sum of weights l; 0
+// where there is none.  The quotient of a small scale may fall below fp32's normal
+// numbers, where it has few bits; then 2^64 is taken out of it.
+struct Quotient {
+    float inv, rest;
+    __device__ __forceinline__ Quotient(float scale, float l) {
+        const float up = __builtin_fabsf(scale) < 0x1p-64f ? 0x1p64f : 1.0f;
+        inv = l == 0.0f ? 0.0f : scale * up / l;
+        rest = up == 1.0f ? 1.0f : 0x1p-64f;
+    }
+    __device__ __forceinline__ float of(float sum) const { return sum * inv * rest; }
+};
+
 // Steps of one row tile, at least one so that empty rows are written too.
 __device__ __forceinline__ int tile_steps(int before, int n, int tp, int i) {
     return max(1, (before + min((i + 1) * tp, n) + kTile - 1) / kTile);
@@ -667,7 +680,7 @@ latent_attention_kernel(Shape s) {
         l = other_half_sum(l);
 
         if (at == 0 && n == steps) {
-            const float inv = l == 0.0f ? 0.0f : kv_scale / l;
+            const Quotient by(kv_scale, l);
             const int lane = here(threadIdx.x & 63), half = lane >> 5, l31 = lane & 31;
             int tok, head;
             if (place(rg * 32 + l31, tok, head)) {
@@ -677,7 +690,7 @@ latent_attention_kernel(Shape s) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         *reinterpret_cast<uint2 *>(o + d * 32 + 8 * v) =
-                            to_bf16x4(acc[d][4 * v] * inv, acc[d][4 * v + 1] * inv, acc[d][4 * v + 2] * inv, acc[d][4 * v + 3] * inv);
+                            to_bf16x4(by.of(acc[d][4 * v]), by.of(acc[d][4 * v + 1]), by.of(acc[d][4 * v + 2]), by.of(acc[d][4 * v + 3]));
             }
         } else {
             // a part: the sums in the registers' order, then maxima and sums of weights
@@ -747,9 +760,9 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(Shape s, const floa
         return ok;
     };
     auto store = [&](int tok, int head, f32x4 sum, float l) {
-        const float inv = l == 0.0f ? 0.0f : kv_scale / l;
+        const Quotient by(kv_scale, l);
         *reinterpret_cast<uint2 *>(a.out + ((size_t)(q.first + tok) * a.H + head) * SKG_LATENT + d * 32 + 8 * wave + 4 * half) =
-            to_bf16x4(sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+            to_bf16x4(by.of(sum[0]), by.of(sum[1]), by.of(sum[2]), by.of(sum[3]));
     };
     constexpr int U = 4;  // parts whose loads are under way together
     if (e.parts <= U) {
