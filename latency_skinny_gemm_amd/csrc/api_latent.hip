@@ -220,6 +220,12 @@ extern "C" int skinny_heads_gemm(const void *x, long x_token_stride, long x_head
     return hip_status(launch_heads(a, stream));
 }
 
+// For the tests: the forms that calls take (the rows of a workgroup, the parts that
+// share a tile's keys at most, whether rows of x come through a ring).
+extern "C" int skg_latent_rows(int B, int T, int H, long capacity, int e4m3) { return latent_rows(B, T, H, capacity, e4m3 != 0); }
+extern "C" int skg_latent_parts(int B, int T, int S, int H) { return latent_expanded_parts(B, T, S, H); }
+extern "C" int skg_heads_ring(int T, int K, long x_token_stride) { return heads_ring(T, K, x_token_stride); }
+
 extern "C" int skinny_latent_reserve(int H, hipStream_t stream) {
     if (H < 1) return SKG_ERR_INVALID_ARG;
     if (H > SKG_LATENT_MAX_H) return SKG_ERR_UNSUPPORTED;

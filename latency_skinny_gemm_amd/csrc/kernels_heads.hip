@@ -123,16 +123,18 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))
     wait_vmcnt_lds<0>();  // no load to LDS outlives the loop
 }
 
+// The ring from the tokens on whose rows it saves more than its start costs (direct
+// against ring, 128 heads, us: K = 512, 16 tokens 8.2, 8.3, 32 10.1, 8.1, 128 24, 10;
+// K = 128, 96 tokens 11.4, 13.0, 128 13.7, 13.0, 256 23, 18).  A row of 16 tokens
+// spans less than 2 GiB.
+bool heads_ring(int T, int K, long x_token_stride) { return K % 128 == 0 && (long)T * K >= 16384 && x_token_stride < 1L << 26; }
+
 namespace {
 
 template <int KS>
 int go(const HeadsArgs &a, hipStream_t stream) {
     if constexpr (KS % 4 == 0) {
-        // The ring from the tokens on whose rows it saves more than its start costs (direct
-        // against ring, 128 heads, us: K = 512, 16 tokens 8.2, 8.3, 32 10.1, 8.1, 128 24, 10;
-        // K = 128, 96 tokens 11.4, 13.0, 128 13.7, 13.0, 256 23, 18).  A row of 16 tokens
-        // spans less than 2 GiB.
-        if ((long)a.T * a.K >= 16384 && a.xt < 1L << 26) {
+        if (heads_ring(a.T, a.K, a.xt)) {
             static std::atomic<unsigned long long> done{0};
             const hipError_t e = allow_dynamic_lds((const void *)heads_ring_kernel<KS>, kHeadsRing * KS * 1024, done);
             if (e != hipSuccess) return (int)e;

@@ -57,6 +57,7 @@ struct HeadsArgs {
     long xt, xh, ot, oh;
     int T, H, N, K;
 };
+bool heads_ring(int T, int K, long x_token_stride);  // x through an LDS ring, else straight from memory
 int launch_heads(const HeadsArgs &a, hipStream_t stream);
 
 }  // namespace skg

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from tests import latent_reference as ref
-from tests.test_latent_gpu import DEV, SCALE, _cache, _dev, _ints, _randn, _starts, skg  # noqa: F401
+from tests import latent_sizes as sizes
+from tests.test_latent_gpu import DEV, SCALE, _attention_case, _cache, _dev, _ints, _randn, _starts, skg  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,124 @@ def test_scale_whose_quotient_is_no_normal_number(skg, counts, lens):  # noqa: F
     got = skg.latent_attention(*_dev(q, cache, table, _ints(lens)), SCALE, scale=scale.to(DEV)).cpu()
     assert (got[..., 0::2].double() == 448 * 2.0 ** -130).all()
     assert (got[..., 1::2].double() == -(2.0 ** -130)).all()
+
+
+# ------------------------------------------------------------ rows that some tokens do not see
+
+NAN = {torch.bfloat16: 0x7FC0, torch.float8_e4m3fn: 0x7F}
+
+
+def _codes(cache):
+    return cache.view(torch.int16 if cache.dtype == torch.bfloat16 else torch.uint8)
+
+
+def _softmax_over(q, rows, values, seen, scale):
+    """ref.softmax_rows with rows that no token of `seen` has taken as zeros, so that their contents touch no bound."""
+    clean = torch.where(seen.any(0)[:, None, None], rows, torch.zeros_like(rows))
+    vals = torch.where(seen.any(0)[:, None, None], values, torch.zeros_like(values))
+    return ref.softmax_rows(q, clean, vals, seen, scale)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("counts,lens,H,page,width,rows", sizes.UNSEEN)
+def test_unseen_rows(skg, counts, lens, H, page, width, rows, e4m3):  # noqa: F811
+    """The last tokens' rows hold NaN, infinities or both, and so does everything that no sequence has: tokens before
+    them get what they would without; those that see a NaN get nothing but NaN; one that sees an infinity where its
+    weight is zero gets NaN in that column alone."""
+    B, T = len(counts), sum(counts)
+    cache, scale, made = _cache(sum(lens) + H, lens, page, e4m3)
+    table = made
+    if width is not None:
+        table = torch.full((B, width), -9, dtype=torch.int32)
+        table[:, :made.shape[1]] = made
+    q = (1.2 * _randn(T + H, T, H, 576)).bfloat16()
+    q[..., 100] = 0.5 + q[..., 100].abs()
+    dirty = torch.empty_like(cache)
+    _codes(dirty)[:] = NAN[cache.dtype]
+    held = [[(int(table[b, p // page]), p % page) for p in range(lens[b])] for b in range(B)]
+    for b in range(B):
+        for p, (pg, r) in enumerate(held[b]):
+            _codes(dirty)[pg, r] = _codes(cache)[pg, r]
+    # sequence b: from its last token's row backwards a NaN in column 300, one in the rotated part, and (bf16) an
+    # infinity of weight zero before them, all on rows that its first token does not see
+    nan_from, minus = [], []
+    for b in range(B):
+        n, m = counts[b], lens[b]
+        bad = [p for p in range(max(m - n + 1, 0), m)][-2:]
+        for k, p in enumerate(reversed(bad)):
+            pg, r = held[b][p]
+            _codes(dirty)[pg, r, 300 if k == 0 else 530] = NAN[cache.dtype]
+        nan_from.append(min(bad) if bad else m)
+        at = nan_from[b] - 2
+        if not e4m3 and at > m - n:
+            pg, r = held[b][at]
+            dirty[pg, r, 100] = -float("inf")
+            minus.append(at)
+        else:
+            minus.append(None)
+    starts = _starts(counts)
+    qd, cd, td, ld, sd, zd = _dev(q, dirty, table, _ints(lens), starts, scale)
+    got = skg.latent_attention(qd, cd, td, ld, SCALE, q_starts=sd, scale=zd).cpu()
+    assert torch.equal(torch.nan_to_num(got.float(), nan=1e9),
+                       torch.nan_to_num(skg.latent_attention(qd, cd, td, ld, SCALE, q_starts=sd, scale=zd).cpu().float(), nan=1e9))
+    reached = 0
+    for b in range(B):
+        n, m, t0 = counts[b], lens[b], int(starts[b])
+        x = torch.stack([cache[pg, r] for pg, r in held[b]]).double() * (1.0 if scale is None else float(scale))
+        for j in range(n):
+            own = m - n + j  # the token's own row
+            out = got[t0 + j]
+            if own >= nan_from[b]:
+                assert torch.isnan(out.float()).all(), (b, j)
+                reached += 1
+                continue
+            seen = (torch.arange(m) <= own)[None]
+            columns = torch.ones(512, dtype=torch.bool)
+            if minus[b] is not None and own >= minus[b]:
+                seen[0, minus[b]] = False
+                columns[100] = False
+                assert torch.isnan(out[:, 100].float()).all(), (b, j)
+                reached += 1
+            want, bound = _softmax_over(q[t0 + j:t0 + j + 1].double(), x[:, None], x[:, None, :512], seen, SCALE)
+            ref.check(out[None][..., columns], want[..., columns], bound[..., columns])
+    assert reached
+
+
+@pytest.mark.parametrize("counts,keys,H,shared", sizes.UNSEEN_KEYS)
+def test_unseen_keys(skg, counts, keys, H, shared):  # noqa: F811
+    """The same in the expanded form: values and keys of the last tokens, in keys of one workgroup and of several."""
+    T, S = sum(counts), sum(keys)
+    q, kv, kr = (1.5 * _randn(T, T, H, 192)).bfloat16(), _randn(T + 1, S, H, 256).bfloat16(), _randn(T + 2, S, 64).bfloat16()
+    qs, ks = _starts(counts), _starts(keys)
+    out, bound = ref.expanded(q, kv, kr, qs.tolist(), ks.tolist(), SCALE, True)
+    dirty, dr = kv.clone(), kr.clone()
+    end = ks[1:].tolist()
+    for b, e in enumerate(end):
+        dirty[e - 1] = float("nan")
+        dr[e - 3] = float("nan")
+        dirty[e - 5, 0, 128 + 77] = float("inf")
+    got = skg.latent_attention_expanded(*_dev(q, dirty, dr, qs), SCALE, kv_starts=ks.to(DEV)).cpu()
+    for b, (n, m) in enumerate(zip(counts, keys)):
+        rows = got[int(qs[b]):int(qs[b]) + n]
+        want, lim = out[int(qs[b]):int(qs[b]) + n], bound[int(qs[b]):int(qs[b]) + n]
+        ref.check(rows[:n - 5], want[:n - 5], lim[:n - 5])
+        # five tokens see the infinity, of head 0's column 77, three the NaN of all heads
+        other = [c for c in range(128) if c != 77]
+        ref.check(rows[n - 5:n - 3][:, 0][:, other], want[n - 5:n - 3][:, 0][:, other], lim[n - 5:n - 3][:, 0][:, other])
+        assert (rows[n - 5:n - 3, 0, 77] == float("inf")).all()
+        ref.check(rows[n - 5:n - 3, 1:], want[n - 5:n - 3, 1:], lim[n - 5:n - 3, 1:])
+        assert torch.isnan(rows[n - 3:].float()).all()
+
+
+# ------------------------------------------------------------ tables wider than the sequences, long caches
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("counts,lens,H,page,width,rows", sizes.SHORT + sizes.LONG)
+def test_wide_tables_and_long_caches(skg, counts, lens, H, page, width, rows, e4m3):  # noqa: F811
+    """Either tile, tables entered by steps and by eight rows; their ends are never read."""
+    cache, scale, made = _cache(sum(lens) + 1, lens, page, e4m3)
+    table = made
+    if width is not None:
+        table = torch.full((len(lens), width), -7, dtype=torch.int32)
+        table[:, :made.shape[1]] = made
+    _attention_case(skg, counts, lens, H, page, e4m3, seed=sum(lens) + 1, single=False, table=table)
