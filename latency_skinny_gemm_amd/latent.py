@@ -262,6 +262,7 @@ def reserve_latent(H, stream=None):
     """Reserves workspace for `stream` (else the current stream): latent_attention
     calls of H heads, any batch and lengths, and latent_attention_expanded calls.
     Before graph capture."""
+    _count(H)
     s = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(s.device):
         _c._check(_c._load().skinny_latent_reserve(H, ctypes.c_void_p(s.cuda_stream)), "skinny_latent_reserve")
