@@ -96,15 +96,17 @@ int skinny_latent_append(const skinny_latent_batch *batch, const void *kv, long 
  * own.  Rows of an e4m3 cache stand for code * *scale; softmax_scale * *scale may
  * leave fp32 where the scores themselves do not.  q bf16 [T, H, 576],
  * out bf16 [T, H, 512], dense.  Scores, maxima, sums and outputs are held in
- * fp32; the weights before their division are rounded to bf16 for the matrix
- * instruction.  A token that sees no row gets zeros.  A row that a token does
- * not see has no effect on it, whatever it holds; nor has what a page holds
- * behind the sequence's end.  Results do not depend on the order in which
- * workgroups run.  0 < softmax_scale <= 2e38.
+ * fp32; the weights before their division, up to 2^8, are rounded to bf16 for the
+ * matrix instruction.  So a value of the cache times its sequence's length must stay
+ * below 2^119, and a sum of 576 products of queries and codes or values below 2^128.
+ * A token that sees no row gets zeros.  A row that a token does not see has no
+ * effect on it, whatever it holds; nor has what a page holds behind the
+ * sequence's end.  Results do not depend on the order in which workgroups run.
+ * 0 < softmax_scale <= 2e38.
  * All that the host knows of the lengths is table_width, by which it chooses how many
  * rows a workgroup takes where there are tiles enough: a table much wider than the
- * longest sequence costs time (64 tokens of 16 heads, 2 sequences of 2000 rows: 25 us,
- * with room for 100000 35) and may move an output by a rounding, as other sums are
+ * longest sequence costs time (128 tokens of 16 heads, 2 sequences of 2000 rows: 32 us,
+ * with room for 100000 37) and may move an output by a rounding, as other sums are
  * joined. */
 int skinny_latent_attention(const skinny_latent_batch *batch, const void *q, const void *cache,
                             int cache_dtype, const float *scale, float softmax_scale, void *out,

@@ -148,7 +148,7 @@ int go(const HeadsArgs &a, hipStream_t stream) {
         }
     }
     const int n_tiles = (a.N + 31) / 32;
-    // tokens a wave: as many waves as fill the card, then up to 128
+    // tokens a wave: all up to 128, however many waves that makes
     const int step = std::min(128, (a.T + 15) / 16 * 16);
     const int parts = (a.T + step - 1) / step;
     const long waves = (long)a.H * parts * n_tiles;

@@ -25,8 +25,8 @@ struct Shape {
     int tp;         // tokens a row tile
     int hg;         // head groups (row tiles a token, if it has more heads than a tile rows)
     int teams;      // groups that hold all head groups of some tokens
-    int min_share;  // least number of steps a workgroup takes: one token over 4000 rows 24.4, 21.3, 20.5, 21.3 us with
-                    // 2, 4, 6, 8, 10 of 16 heads over 3000 e4m3 rows 22.9, 22.4, 23.4, 25.6
+    int min_share;  // least number of steps a workgroup takes.  With 2, 4, 6 and 8: one token of 128 heads over 4000 bf16
+                    // rows 24.4, 21.3, 20.5 and 21.3 us; 10 sequences of 16 heads over 3000 e4m3 rows 22.9, 22.4, 23.4 and 25.6
     int anew;       // steps that beginning a row tile costs: with 5, 8, 12, 16 600 tokens over their own rows, 20 heads,
                     // take 51, 48, 47, 49 us, 512 tokens over 8192 rows, 128 heads, 885, 870, 860, 868; without 153, 929
     int by_tile;    // records of row tiles, all of which are known on the host; else of workgroups
@@ -109,12 +109,17 @@ __device__ __forceinline__ long steps_before(int before, int n, int tp, int upto
 // they begin or end in, or of one tile each where that makes them little longer; parts of
 // a tile are joined by the kernel below.
 //
-// 512 tokens of 128 heads over 8192 rows: 855 us, 1020 TFLOP/s, the clock below 1.8 GHz as
-// in every kernel here that keeps the matrix pipes half busy.  Decode of 128 sequences,
-// 128 heads, 588 MB: 170 us, of which its loads alone take 150 (4.3 TB/s: a team's
-// workgroups have the same rows under way); 32 sequences, 16 heads, e4m3, 272 MB: 59 us,
-// loads alone 57.  One token over 4000 rows: 15.5 us, six steps of 0.8 us behind four trips
-// to memory (lengths, table, queries, rows) and a first run through 27 KB of code.
+// 512 tokens of 128 heads over 8192 rows: 857 to 940 us by the card, 1020 to 930 TFLOP/s, at
+// 2.0 GHz of 2.4.  The matrix pipes are busy 43 % of the cycles; a wave, the only one of its
+// SIMD, issues instructions in 47 % of them, waits for counters and barriers in 25 % and for
+// a unit to take its next instruction in 28 %.  Decode of 128 sequences, 128 heads, 588 MB:
+// 176 us, of which its loads alone take 150 (3.9 TB/s: a team's workgroups have the same
+// rows under way); 32 sequences, 16 heads, e4m3, 272 MB: 59 us, loads alone 57.  One token
+// of 128 heads over 4000 rows: 15.8 us; one workgroup's share alone takes 9.0 with one step
+// and 12.4 with its six (0.7 a step).
+//
+// A share brings its ring's rows up to the sequence's end, not its own: three steps more
+// than it uses (the 32 sequences read 299 MB for 272).
 template <int RG, int CS, bool E4M3>
 __global__ void __launch_bounds__(64 * RG * CS)
     __attribute__((amdgpu_waves_per_eu(groups_of(RG, E4M3) / 256 * RG * CS / 4, groups_of(RG, E4M3) / 256 * RG * CS / 4)))

@@ -8,16 +8,15 @@
 // one's scores, so that vector and matrix instructions run beside each other; weights
 // are 2^(score - m), m a maximum that follows only when a score is over m + 8.
 //
-// 4096 tokens, 128 heads: 720 us, 950 TFLOP/s.  The matrix pipes are busy half of the
-// time, and the clock falls below 1.8 GHz of 2.4 under this mix of instructions (a loop of
-// nothing but matrix instructions on random numbers: 1770 TFLOP/s, with two exponentials
-// and four fused multiply-adds each 1100).  Waves of 64 tokens, one a SIMD, which read
-// LDS half as often, took 784 us for 723; blocks of 16 rows by 64 bytes in LDS, loaded
-// 64 bytes a row, 811.
+// 4096 tokens, 128 heads: 722 us, 950 TFLOP/s, at 1.9 GHz of 2.4.  The matrix pipes are busy
+// 46 % of the cycles; a SIMD's two waves each issue instructions in 36 % of them, wait for
+// counters and barriers in 26 % and for a unit to take the next instruction in 37 %.  Waves
+// of 64 tokens, one a SIMD, which read LDS half as often, took 784 us for 723; blocks of 16
+// rows by 64 bytes in LDS, loaded 64 bytes a row, 811.
 //
 // Query tokens that fill less than half of the device have their keys shared among
 // workgroups, two a CU in all; a second kernel joins the parts (500 tokens of 32 heads
-// over 8100 keys: 155 us in one part, 85 + 9 in four).
+// over 8100 keys: 155 us in one part, 89 + 8 in four).
 #include <algorithm>
 
 #include "internal.h"

@@ -165,7 +165,9 @@ __device__ __forceinline__ bf16x8 to_bf16x8(const float *v) {
     for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];
     return r;
 }
-// sum + the eight values.  The sum of the weights is made of the rounded ones, which
+// sum + the eight values.  Weights go to the second product in bf16, since the matrix
+// instruction takes both operands in one type and the values have no more bits (weights of
+// 16 bits would take a second product of what the first left).  The sum of the weights is made of the rounded ones, which
 // the second product takes: what their roundings have in common then cancels in the
 // quotient (errors of 1.0 to 1.4 times the output's own rounding instead of 1.1 to 1.5).
 __device__ __forceinline__ float add_bf16x8(bf16x8 v, float sum) {

@@ -163,3 +163,23 @@ def test_wide_tables_and_long_caches(skg, counts, lens, H, page, width, rows, e4
         table = torch.full((len(lens), width), -7, dtype=torch.int32)
         table[:, :made.shape[1]] = made
     _attention_case(skg, counts, lens, H, page, e4m3, seed=sum(lens) + 1, single=False, table=table)
+
+
+# ------------------------------------------------------------ large values
+
+@pytest.mark.parametrize("qscale", [0.5, 40.0])
+def test_values_near_the_largest(skg, qscale):  # noqa: F811
+    """Half of the columns 2^107 times as large, 600 of them a sequence: sums below 2^119 that scores know nothing of."""
+    page, counts, lens, H = 64, [5, 1], [600, 40], 6
+    cache, _, table = _cache(31, lens, page, False)
+    cache[..., 256:512] *= 2.0 ** 107
+    q = (qscale * _randn(32, 6, H, 576)).bfloat16()
+    q[..., 256:512] = 0.0
+    starts = _starts(counts)
+    out, bound = ref.attention(q, cache, None, table, lens, starts.tolist(), SCALE)
+    ref.check(skg.latent_attention(*_dev(q, cache, table, _ints(lens)), SCALE, q_starts=starts.to(DEV)), out, bound)
+    eq, kv, kr = (qscale * _randn(33, 6, H, 192)).bfloat16(), _randn(34, 640, H, 256).bfloat16(), _randn(35, 640, 64).bfloat16()
+    kv[..., 192:] *= 2.0 ** 107
+    ks = _starts(lens)
+    out, bound = ref.expanded(eq, kv, kr, starts.tolist(), ks.tolist(), SCALE, True)
+    ref.check(skg.latent_attention_expanded(*_dev(eq, kv, kr, starts), SCALE, kv_starts=ks.to(DEV)), out, bound)
