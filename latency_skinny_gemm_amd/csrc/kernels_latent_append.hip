@@ -5,7 +5,7 @@
 // A token's row is one wave's, 8 latents a lane and one of the 32 pairs in each of
 // the first 32 lanes; everything about it is in fp64, so that a code next to a tie is
 // the exact one's.  That costs 2 us of 19 at 8192 tokens of 16 heads to e4m3 (59 MB at
-// 3.1 TB/s); one token of 128 heads takes 2.7 us, four trips to memory one after another.
+// 3.1 TB/s); one token of 128 heads takes 2.6 us, four trips to memory one after another.
 // Rows before queries: both kinds in turn, on every XCD, took 23 us for 19.  Two heads'
 // queries a thread: 3.4 us for one token, 19.8 for 18.6 at 8192.
 #include <algorithm>

@@ -7,6 +7,13 @@ A buffer instruction may read a scalar register that a vector instruction wrote
 instruction is one, s_nop N is N + 1.  Between m0 being written and a load to LDS
 stands one.  Both over every path that leads to the load.  And m0 is those loads'
 alone: each writes it for itself, and no other instruction has it.
+
+The ring's waits count loads: before the barrier of a step the newest may still be under
+way, as many as the wait names.  That is right if at least so many loads belong to
+later steps, that is, if on every path from one such wait to the next a step's loads
+are issued.  (Not for latent_expanded_kernel, which has two copies of a step's loads, one for
+waves that see none of its keys: the compiler tests that condition twice, so that
+paths exist with both copies and with neither that no wave takes.)
 """
 import os
 import re
@@ -174,6 +181,69 @@ def test_m0_is_the_loads_own(functions):
     for name, code in functions.items():
         if any(k in name for k in KERNELS):
             assert others_with_m0(code) == [], name
+
+
+def is_lds_load(name, ops):
+    return name.startswith("buffer_load") and any(re.search(r"\blds\b", o) for o in ops)
+
+
+def least_loads(code, start, ends):
+    """The least number of loads to LDS on any path from behind instruction `start` to one of `ends`.  A branch around
+    a load for waves without a lane that makes it is none: the lanes that make a step's last load are the first ones."""
+    at = {offset: i for i, (_, _, _, offset) in enumerate(code)}
+    best, todo, least = {}, [(0, start + 1)], None
+    while todo:
+        n, i = todo.pop()
+        if i >= len(code) or best.get(i, n + 1) <= n:
+            continue
+        best[i] = n
+        if i in ends:
+            least = n if least is None else min(least, n)
+            continue
+        name, ops, target, _ = code[i]
+        n += is_lds_load(name, ops)
+        around = name == "s_cbranch_execz" and target in at and any(is_lds_load(*code[k][:2]) for k in range(i, at[target]))
+        if target in at and not around:
+            todo.append((n, at[target]))
+        if name not in ("s_branch", "s_endpgm"):
+            todo.append((n, i + 1))
+    return least
+
+
+def ring_waits(code, count):
+    """Waits for all but `count` loads in front of a barrier."""
+    return {i for i, (name, ops, _, _) in enumerate(code)
+            if name == "s_waitcnt" and f"vmcnt({count})" in " ".join(ops) and code[i + 1][0] == "s_barrier"}
+
+
+# kernel: loads of a step that a wave makes, and how many may be under way behind a step's wait
+RINGS = {"latent_attention_kernelILi1ELi4ELb0E": (9, 9), "latent_attention_kernelILi2ELi2ELb0E": (9, 9),
+         "latent_attention_kernelILi1ELi4ELb1E": (5, 5), "latent_attention_kernelILi2ELi2ELb1E": (5, 5),
+         "heads_ring_kernelILi4E": (1, 2), "heads_ring_kernelILi8E": (2, 4),
+         "heads_ring_kernelILi12E": (3, 6), "heads_ring_kernelILi16E": (4, 8)}
+
+
+@pytest.mark.parametrize("kernel", RINGS)
+def test_ring_waits_count_a_steps_loads(functions, kernel):
+    (code,) = [c for name, c in functions.items() if kernel in name]
+    loads, wait = RINGS[kernel]
+    waits = ring_waits(code, wait)
+    assert waits, "no wait of this count"
+    for w in waits:
+        least = least_loads(code, w, waits)
+        assert least is None or least >= loads, f"{least} loads from the wait at {code[w][3]:#x}"
+    assert any(least_loads(code, w, waits) == loads for w in waits)
+    assert least_loads(code, -1, waits) >= 3 * loads  # before the first step: of all slots of the ring but one
+    assert not any(name.startswith("scratch_") for name, *_ in code)
+
+
+def test_the_loads_of_a_path_are_counted():
+    wait = "s_waitcnt vmcnt(2) lgkmcnt(0)"
+    code = _code(wait, "s_barrier", LOAD, ("s_cbranch_scc0 2", 20), LOAD, ("s_cbranch_scc1 65530", 0), "s_endpgm")
+    assert ring_waits(code, 2) == {0}
+    assert least_loads(code, 0, {0}) == 1  # round the second
+    assert least_loads(code, -1, {0}) == 0
+    assert least_loads(code, 0, {99}) is None
 
 
 def _code(*lines):
