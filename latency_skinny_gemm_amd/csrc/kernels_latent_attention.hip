@@ -115,7 +115,7 @@ __device__ __forceinline__ long steps_before(int before, int n, int tp, int upto
 // a unit to take its next instruction in 28 %.  Decode of 128 sequences, 128 heads, 588 MB:
 // 176 us, of which its loads alone take 150 (3.9 TB/s: a team's workgroups have the same
 // rows under way); 32 sequences, 16 heads, e4m3, 272 MB: 59 us, loads alone 57.  One token
-// of 128 heads over 4000 rows: 15.8 us; one workgroup's share alone takes 9.0 with one step
+// of 128 heads over 4000 rows: 16 us; one workgroup's share alone takes 9.0 with one step
 // and 12.4 with its six (0.7 a step).
 //
 // A share brings its ring's rows up to the sequence's end, not its own: three steps more
